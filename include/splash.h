@@ -257,6 +257,157 @@ SPLASH_API int splash_kv_migrate(const void* src_pool, void* dst_pool, size_t pa
                       const int32_t* src_ids, const int32_t* dst_ids, int n_pages,
                       int32_t src_num_pages, int32_t dst_num_pages, splash_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The serving step around the attention: rotary positions, writing new tokens
+ * into the paged cache (plain or quantised), reading quantised pages back, and
+ * causal attention of a chunk of new tokens.
+ *
+ * A ragged batch of new tokens is described the same way everywhere: the new
+ * tokens of all requests are packed in one array of total_q rows, and
+ *   cu_q        int32 [B + 1] device, ascending, 0 <= cu_q[r] <= total_q: request r owns
+ *               rows [cu_q[r], cu_q[r + 1]); rows outside every request are padding
+ *   ctx_lens    int32 [B]: tokens of request r once its new tokens are written, so that
+ *               row cu_q[r] + i is the token at position ctx_lens[r] - n_r + i
+ *               (n_r = cu_q[r + 1] - cu_q[r])
+ *   block_table int32 [B][max_pages_per_req], as for splash_decode_attn
+ * ------------------------------------------------------------------------- */
+
+/* Element types of splash_rope and of splash_chunk_attn's output. */
+enum { SPLASH_BF16 = 0, SPLASH_F16 = 1, SPLASH_F32 = 2 };
+
+/* Frequency scaling of rotary positions. */
+enum { SPLASH_ROPE_PLAIN = 0, SPLASH_ROPE_LINEAR = 1, SPLASH_ROPE_YARN = 2 };
+
+/*
+ * Rotary positions (host struct, read during the call only).
+ *   dims         d, rotated dims of a head: even, 2..256
+ *   interleaved  nonzero: pair i is dims (2i, 2i + 1); zero: dims (i, i + d / 2)
+ *   scaling      SPLASH_ROPE_PLAIN   f_i = base^(-2i / d) radians per position
+ *                SPLASH_ROPE_LINEAR  f_i / factor
+ *                SPLASH_ROPE_YARN    f_i * ((1 - g_i) + g_i / factor), g_i = clamp((i - lo) /
+ *                    max(hi - lo, 0.001), 0, 1), lo = max(floor(pair(beta_fast)), 0),
+ *                    hi = min(ceil(pair(beta_slow)), d - 1), pair(b) = d ln(orig_ctx / (2 pi b))
+ *                    / (2 ln base)
+ *   base         >= 1 (> 1 for YARN); factor >= 1; orig_ctx, beta_fast, beta_slow > 0 (YARN only)
+ *   amplitude    multiplies cos and sin (1: a pure rotation); finite
+ */
+typedef struct {
+    int32_t dims;
+    int32_t interleaved;
+    int32_t scaling;
+    int32_t reserved; /* 0 */
+    double base;
+    double factor;
+    double orig_ctx;
+    double beta_fast;
+    double beta_slow;
+    double amplitude;
+} splash_rope_desc;
+
+/*
+ * Rotates the d = rope->dims leading dims of every head row:
+ *   (y_a, y_b) = amplitude * (x_a cos w - x_b sin w, x_a sin w + x_b cos w),  w = positions[t] * f_i
+ * for the pairs (a, b) of rope->interleaved.  Pass pointers to the first rotated dim:
+ * a position part at the end of a wider head is reached through the strides.
+ *   dtype       SPLASH_BF16, SPLASH_F16 or SPLASH_F32, of x and y; computed in fp32 and
+ *               rounded once.  The angle is reduced exactly: its error does not grow with the position
+ *   x, y        [T][H][d] with strides in elements (head rows contiguous); y may be x with
+ *               the same strides, otherwise the two may not overlap
+ *   positions   int32 [T]; negative positions turn the other way (amplitude 1: they undo
+ *               the rotation)
+ * Elements of y outside the d dims are not written.  Any alignment of the elements' own
+ * size is taken; 16-byte aligned pointers and strides run fastest.
+ */
+SPLASH_API int splash_rope(const splash_rope_desc* rope, int dtype, const void* x,
+                           int64_t x_token_stride, int64_t x_head_stride, void* y,
+                           int64_t y_token_stride, int64_t y_head_stride, const int32_t* positions,
+                           int T, int H, splash_stream_t stream);
+
+/*
+ * Cache formats of splash_kv_append:
+ *   SPLASH_KV_BF16   rows of 576 bf16 (1,152 bytes), what the attention reads
+ *   SPLASH_KV_MXFP8  rows of 656 bytes: 512 e4m3 latents, 16 scale bytes (one per 32 latents),
+ *                    64 bf16 rope dims.  A scale byte b stands for 2^(b - 127); a group's is
+ *                    the least with max |x| <= 448 * 2^(b - 127) over its finite x (0 for a group
+ *                    of zeros), and its codes are x / 2^(b - 127) rounded to nearest even.  NaN stays
+ *                    NaN, an infinity becomes the group's largest code.  Every held value
+ *                    is exact in bf16 (scale bytes below 3 aside, where values reach below
+ *                    bf16's least).
+ * Pages are P consecutive rows either way, so splash_kv_migrate moves both.
+ */
+enum { SPLASH_KV_BF16 = 0, SPLASH_KV_MXFP8 = 1 };
+
+/*
+ * Writes new tokens' keys into the paged cache: row cu_q[r] + i goes to slot
+ * p % P of page block_table[r][p / P], p = ctx_lens[r] - n_r + i.
+ *   desc         num_reqs, page_size, num_pages, max_pages_per_req, d_qk = 576 and d_v = 512;
+ *                num_heads must be positive and is otherwise unused, as is scale
+ *   rope         rotates the 64 rope dims by the token's position (dims must be 64), or
+ *                NULL: they are written as they are
+ *   format       SPLASH_KV_BF16 or SPLASH_KV_MXFP8, of kv_pool
+ *   latent       bf16 [total_q][512], rows latent_stride elements apart (a multiple of 8),
+ *                16-byte aligned
+ *   k_rope       bf16 [total_q][64], rows k_rope_stride elements apart (even), 4-byte aligned
+ *   kv_pool      16-byte aligned; slots that no new token owns are left as they are
+ * A token is skipped when it is padding, when its position is outside [0, max_pages_per_req
+ * * P) or when its page id is outside [0, num_pages).  Two tokens may not own one slot.
+ */
+SPLASH_API int splash_kv_append(const splash_attn_desc* desc, const splash_rope_desc* rope, int format,
+                                const void* latent, int64_t latent_stride, const void* k_rope,
+                                int64_t k_rope_stride, const int32_t* cu_q, int total_q,
+                                const int32_t* block_table, const int32_t* ctx_lens, void* kv_pool,
+                                splash_stream_t stream);
+
+/*
+ * Reads MXFP8 pages back: dst_pool page dst_ids[i] (bf16 [P][576]) <- the values of src_pool
+ * page src_ids[i] (MXFP8 [P][656]), i < n_pages, all P rows.
+ *   page_size   any positive number of tokens; ids and pool sizes as in splash_kv_migrate (a
+ *               pair with an id outside its pool is skipped); the pools may not overlap, and
+ *               dst_ids must be distinct.  A scale byte of 255 gives NaN.
+ */
+SPLASH_API int splash_kv_unpack(const void* src_pool, void* dst_pool, int page_size,
+                                const int32_t* src_ids, const int32_t* dst_ids, int n_pages,
+                                int32_t src_num_pages, int32_t dst_num_pages, splash_stream_t stream);
+
+/*
+ * Bytes of device workspace splash_chunk_attn needs for this shape, number of new
+ * tokens and head range on the current device.  Returns 0 when the shape is invalid or
+ * unsupported.
+ */
+SPLASH_API size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int total_q, int head_lo,
+                                              int head_hi);
+
+/*
+ * Causal attention of new tokens over the paged cache that already holds them
+ * (a prompt, a chunk of one, drafted tokens, or single tokens; any mix of them).
+ *
+ * For the token at row t = cu_q[r] + i and head h in [head_lo, head_hi), over the tokens
+ *   T = [tok_lo, min(tok_hi < 0 ? e : tok_hi, e)),  e = ctx_lens[r] - n_r + i + 1,
+ * out[t][h] and lse[t][h] are those of splash_decode_attn with q[t][h].  An empty T gives
+ * out = 0 and lse = -inf.  A share [tok_lo, tok_hi) gives the partial that splash_lse_merge
+ * combines (fp32 out).
+ *   q           bf16 [total_q][H][576], contiguous, 16-byte aligned
+ *   out         [total_q][H][512] of out_dtype (SPLASH_BF16 or SPLASH_F32), 16-byte aligned
+ *   lse         fp32 [total_q][H]
+ *   head_lo/hi, tok_lo/hi, kv_pool, block_table, ctx_lens: as for splash_decode_attn, desc->num_reqs
+ *               = B; one shared KV head
+ *   workspace   >= splash_chunk_workspace_size(...) bytes, 256-byte aligned; one call at a time
+ * Only rows that a request owns and heads [head_lo, head_hi) are written.  The scores of one
+ * row never depend on another row.  Slots past a context may hold any bits; a token within a
+ * context whose latent is not finite can make NaN of every new row of that request, also of
+ * those that precede it.
+ * A cu_q that descends or leaves [0, total_q] is clamped into order; it, a context length
+ * outside [0, max_pages_per_req * P] (clamped) and a needed page id outside [0, num_pages) (its
+ * tokens are left out) set SPLASH_DEVICE_BAD_INPUT, read with splash_workspace_status.
+ * The result does not depend on how the work is cut over the GPU's SMs by chance: the
+ * same call on the same device gives the same bits.
+ */
+SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool,
+                                 const int32_t* cu_q, int total_q, const int32_t* block_table,
+                                 const int32_t* ctx_lens, int head_lo, int head_hi, int64_t tok_lo,
+                                 int64_t tok_hi, int out_dtype, void* out, float* lse,
+                                 void* workspace, size_t ws_bytes, splash_stream_t stream);
+
 /*
  * Reads the device status word of a decode workspace (SPLASH_DEVICE_* bits set
  * by the most recent splash_decode_attn that used it): synchronises `stream`,

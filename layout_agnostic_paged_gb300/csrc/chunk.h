@@ -1,0 +1,98 @@
+// chunk.h -- what the chunk attention's host code, plan, kernel and combine share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace splash {
+
+constexpr int kChunkRows = 64;         // query rows of one CTA; a pair works on 128
+constexpr int kChunkKeys = 128;        // keys of one tile
+constexpr int kChunkKBlocks = 3;       // 64-dim blocks of the keys loaded and released together
+constexpr int kChunkSlotsPerPair = 8;  // partial results the workspace holds, per CTA pair
+
+// How a head slice is laid over the rows of CTA pairs.  A CTA's rows are `tokens`
+// consecutive new tokens times `heads` consecutive heads (head fastest), at most 64.  With one head
+// group the pair's CTAs take consecutive token blocks, with several (then an even number) they take
+// consecutive head groups of the same tokens.
+struct ChunkTiling {
+    int groups;   // head groups of a token block: 1 or an even number
+    int heads;    // heads of a group (the last may have fewer)
+    int tokens;   // tokens of a CTA's block
+    __host__ __device__ int pair_tokens() const { return groups == 1 ? 2 * tokens : tokens; }
+    __host__ __device__ int pair_groups() const { return groups == 1 ? 1 : groups / 2; }
+};
+
+inline ChunkTiling chunk_tiling(int Hs) {
+    ChunkTiling t;
+    t.groups = Hs <= kChunkRows ? 1 : 2 * ((Hs + 2 * kChunkRows - 1) / (2 * kChunkRows));
+    t.heads = (Hs + t.groups - 1) / t.groups;
+    t.tokens = kChunkRows / t.heads;
+    return t;
+}
+
+// Workspace: header, work items, split row tiles, partial lse, partial out (256-byte
+// aligned each).
+struct ChunkHeader {
+    uint32_t status;      // SPLASH_DEVICE_* bits of the last call
+    int32_t num_items;
+    int32_t num_splits;   // row tiles cut into several items
+    int32_t pad;
+};
+
+// One pair's work: the rows of one token block and head group pair against key tiles
+// [t_lo, t_hi).
+struct alignas(16) ChunkItem {
+    int32_t r;            // request
+    int32_t tok;          // first new token (row of q)
+    int32_t ntok;         // tokens of the request from there on
+    int32_t seen;         // keys that token `tok` sees: its position + 1
+    int32_t pair_group;   // head groups 2 * pair_group and the next one (one group: 0)
+    int32_t t_lo, t_hi;   // key tiles
+    int32_t slot;         // partial slot, or -1: the result goes to out
+    int32_t ctx;          // context length (keys at or past it do not exist)
+    int32_t pad[3];
+};
+static_assert(sizeof(ChunkItem) == 48, "ChunkItem layout");
+
+struct alignas(16) ChunkSplit {
+    int32_t tok, ntok, pair_group, slot, pieces, pad[3];
+};
+static_assert(sizeof(ChunkSplit) == 32, "ChunkSplit layout");
+
+struct ChunkArgs {
+    const int32_t* cu_q;
+    const int32_t* block_table;
+    const int32_t* ctx_lens;
+    void* out;
+    float* lse;
+    uint8_t* ws;
+    size_t items_off, splits_off, plse_off, pout_off;
+    int64_t cap_items;
+    int cap_slots;
+    int B, total_q, H, head_lo, Hs;
+    int P, num_pages, max_pages, max_ctx;
+    int past_row;         // a row of the pool's maps that does not exist: copies from there fill zeros
+    int tok_lo, tok_hi;   // tok_hi: INT32_MAX for "to the end"
+    int pairs;            // CTA pairs of the grid
+    ChunkTiling tile;
+    int out_f32;
+    float scale;
+};
+
+struct ChunkMaps {
+    CUtensorMap q;        // [9][total_q][H][64] box {64, heads, tokens, 1}
+    CUtensorMap k;        // pool as [9][rows][64], box {64, 64, 3} (pages of 64 and more)
+    CUtensorMap v;        // box {64, min(P, 64), 4}
+    CUtensorMap rows[6];  // box {64, 2^i, 1}
+};
+
+// Capacities for the shape (cap_items, cap_slots), and the offsets; returns the bytes.
+size_t chunk_layout(ChunkArgs& a);
+cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream);
+cudaError_t launch_chunk_combine(const ChunkArgs& a, int sms, cudaStream_t stream);
+
+}  // namespace splash

@@ -1,0 +1,485 @@
+// chunk_attn.cu -- causal attention of new tokens over the paged latent cache, on pairs of
+// CTAs (cta_group::2 tensor cores, TMEM, TMA).
+//
+// With H heads reading one latent KV head, a new token is H query rows over the same keys,
+// so a chunk is a matrix product with many rows: 2 * (576 + 512) operations per row and key.
+// It is bound by the tensor cores; a single token per request is bound by HBM as in the decode.
+//
+// Per 128 query rows and 128 keys:
+//   S [128 x 128] = Q [128 x 576] . K^T          36 MMAs of M 128, N 128, K 16
+//   online softmax per row (fp32, exp2 domain, lazily rescaled running maximum)
+//   O [128 x 512] += P [128 x 128] . V           16 MMAs of M 128, N 256, K 16
+// The value is the latent prefix of the key.
+//
+// Why a pair.  O of 128 rows fills the whole TMEM of one SM (512 fp32 columns), and Q of 128
+// rows plus one key tile is more than its shared memory.  A pair of CTAs splits the rows: each has
+// 64 (Q 72 KB, O in 256 columns because an M = 128 pair MMA puts its two column halves on
+// lanes 0-63 and 64-127), so a thread's lane is one row and one half of the columns, and the
+// softmax needs no exchange beyond its own CTA.  The hardware splits B between the CTAs: for
+// S each holds 64 of the 128 keys, for O each holds its 256 of the 512 value dims of all
+// 128 keys.  These are different cuts of the cache, so K and V are loaded separately (the V
+// bytes come from L2).  Measured MMA rates at M = 128 in a pair: 64.7 clocks at N = 256 (the
+// full rate), 50.6 at N = 128 (32 at the full rate).
+//
+// Shared memory of each CTA: Q 72 KB, K 72 KB, V 64 KB, P 16 KB.  K and V have one buffer
+// each: a piece of it is loaded again as soon as the MMAs that read it are done, and needed a
+// whole tile later, because S of the next tile is computed before O of this one.
+//
+// Roles (256 threads): warp 0 loads Q and K, warp 2 loads V, lane 0 of the leader's warp 1 issues
+// every MMA, warps 4-7 run the softmax and the epilogue.
+#include <math.h>
+
+#include "chunk.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "pair.cuh"
+
+namespace splash {
+namespace {
+
+constexpr int kBlk = kChunkRows * 128;           // 64 rows of one 64-dim block: 8 KB
+constexpr int kKBlks = kChunkKBlocks;
+constexpr int kKGroups = 9 / kKBlks;             // K is loaded and released in groups of its 9 blocks
+constexpr int kQOff = 0;
+constexpr int kKOff = 9 * kBlk;
+constexpr int kVOff = kKOff + 9 * kBlk;          // [2 halves of the keys][pages][4 blocks][rows][128 B]
+constexpr int kVHalf = 4 * kBlk;
+constexpr int kPOff = kVOff + 2 * kVHalf;        // [2 halves of the keys][64 rows][128 B]
+constexpr int kBarOff = kPOff + 2 * kBlk;
+// barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O free, drain
+constexpr int kNumBars = 2 * kKGroups + 4 + 2 + 2 + 1 + 1 + 1 + 1;
+constexpr int kMiscOff = kBarOff + kNumBars * 8;
+constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][2 halves][64]
+constexpr int kSumOff = kMaxOff + 4 * kChunkRows * 4;   // row sums [2 halves][64]
+constexpr int kSmem = kSumOff + 2 * kChunkRows * 4 + 1024;   // + alignment slack
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr int kThreads = 256;
+constexpr int kSoftThreads = 128;
+constexpr int kOCol = 0, kSCol = 256;            // TMEM: O in columns 0-255, S in 2 x 64
+constexpr int kTmemCols = 512;
+constexpr float kTau = 8.0f;                     // rescale O when a score beats the maximum by 2^8
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// The page id behind a key, or -1 where there is none (past the context, or a bad id).
+__device__ __forceinline__ int page_of(const ChunkArgs& a, const int32_t* table, int key, int ctx) {
+    if (key >= ctx) return -1;
+    const int id = table[key / a.P];
+    return id >= 0 && id < a.num_pages ? id : -1;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
+    uint64_t* k_full = bars;                     // leader's: both CTAs' loads
+    uint64_t* k_empty = k_full + kKGroups;       // each CTA's own, as every *_empty
+    uint64_t* v_full = k_empty + kKGroups;       // leader's
+    uint64_t* v_empty = v_full + 2;
+    uint64_t* q_full = v_empty + 2;              // leader's
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_full + 2;               // each CTA's
+    uint64_t* p_full = s_full + 2;               // leader's: the softmax warps of both CTAs
+    uint64_t* pv_done = p_full + 1;              // each CTA's
+    uint64_t* o_free = pv_done + 1;              // leader's
+    uint64_t* drain = o_free + 1;                // each CTA's
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 8);
+    uint32_t* status = reinterpret_cast<uint32_t*>(smem + kMiscOff + 16);
+    float* sm_max = reinterpret_cast<float*>(smem + kMaxOff);
+    float* sm_sum = reinterpret_cast<float*>(smem + kSumOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        // eight softmax warps of the pair arrive on P full and O free, one thread on the others
+        for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], &bars[i] == p_full || &bars[i] == o_free ? 8 : 1);
+        *abort_flag = 0;
+        *status = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                              // both CTAs' barriers exist
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    pdl_wait();
+    const ChunkHeader* head = reinterpret_cast<const ChunkHeader*>(a.ws);
+    const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.items_off);
+    const int num_items = head->num_items;
+    const int R = min(a.P, kChunkRows);          // rows of one load: pages of 128 come in halves
+    const int loads = kChunkRows / R;            // loads for 64 keys
+    const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
+    const bool one_group = a.tile.groups == 1;
+
+    if (warp == 0) {
+        // -------------------------------------------------------- Q and K loads
+        const uint32_t sq = smem_u32(smem + kQOff), sk = smem_u32(smem + kKOff);
+        const uint32_t bq = map_to_rank(smem_u32(q_full), 0);
+        int ph = 0, qph = 0;
+        bool ok = true;
+        for (int i = pair; ok && i < num_items; i += a.pairs) {
+            const ChunkItem it = items[i];
+            if (it.t_lo >= it.t_hi) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(q_empty, qph ^ 1, abort_flag, status))) break;
+            qph ^= 1;
+            const int tok = it.tok + (one_group ? int(rank) * a.tile.tokens : 0);
+            const int h0 = a.head_lo + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
+            if (rank == 0 && lane == 0)
+                mbar_arrive_expect_tx(q_full, 2 * 9 * a.tile.heads * a.tile.tokens * 128);
+            __syncwarp();
+            if (lane < 9) tma_pair_4d(sq + lane * kBlk, &maps.q, bq, 0, h0, tok, lane);
+            const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
+            for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
+                // lane k < loads looks up the page behind keys [64 c + k R, + R) of the tile
+                const int key = t * kChunkKeys + int(rank) * kChunkRows + lane * R;
+                int row = a.past_row;            // past the pool: the copy fills zeros
+                if (lane < loads) {
+                    const int id = page_of(a, table, key, it.ctx);
+                    if (id >= 0) row = id * a.P + key % a.P;
+                    else if (key < it.ctx) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
+                }
+                for (int g = 0; g < kKGroups; ++g) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&k_empty[g], ph ^ 1, abort_flag, status))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = map_to_rank(smem_u32(&k_full[g]), 0);
+                    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kKBlks * kBlk);
+                    __syncwarp();
+                    if (R == kChunkRows) {
+                        if (lane == 0) tma_pair_3d(sk + g * kKBlks * kBlk, &maps.k, bar, 0, row, g * kKBlks);
+                    } else {
+                        const CUtensorMap* m = &maps.rows[R == 32 ? 5 : 4];
+                        for (int j = lane; j < (kKBlks * loads + 31) / 32 * 32; j += 32) {
+                            const int b = j / loads, p = j % loads;
+                            const int y = __shfl_sync(0xffffffffu, row, p);
+                            if (b < kKBlks)
+                                tma_pair_3d(sk + (g * kKBlks + b) * kBlk + p * R * 128, m, bar, 0, y, g * kKBlks + b);
+                        }
+                    }
+                }
+                ph ^= 1;
+            }
+        }
+    } else if (warp == 2) {
+        // -------------------------------------------------------- V loads
+        // this CTA's 256 value dims (blocks 4 c .. 4 c + 3) of all 128 keys, in two halves.  Rows
+        // past the context must be zero, whatever their slots hold (0 * NaN is NaN): whole absent pages
+        // are loaded from past the pool, and the page in which the context ends is loaded in
+        // runs of 2^i rows, the valid ones from the pool and the others from past it.
+        const uint32_t sv = smem_u32(smem + kVOff);
+        const int past = a.past_row;
+        int ph = 0;
+        bool ok = true;
+        for (int i = pair; ok && i < num_items; i += a.pairs) {
+            const ChunkItem it = items[i];
+            const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
+            for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
+                const int key = t * kChunkKeys + lane * R;      // lane k < 2 * loads: load k of the tile
+                int row = past;
+                if (lane < 2 * loads) {
+                    const int id = page_of(a, table, key, it.ctx);
+                    if (id >= 0) row = id * a.P + key % a.P;
+                }
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&v_empty[hh], ph ^ 1, abort_flag, status))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = map_to_rank(smem_u32(&v_full[hh]), 0);
+                    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&v_full[hh], 2 * kVHalf);
+                    __syncwarp();
+                    const int first = hh * loads;
+                    const bool mine = lane >= first && lane < first + loads;
+                    const bool cut = mine && row != past && key + R > it.ctx;
+                    if (mine && !cut)
+                        tma_pair_3d(sv + lane * R * 512, &maps.v, bar, 0, row, 4 * int(rank));
+                    const uint32_t cuts = __ballot_sync(0xffffffffu, cut);
+                    if (cuts) {                                  // one page at most
+                        const int src = __ffs(cuts) - 1;
+                        const int y = __shfl_sync(0xffffffffu, row, src);
+                        const int n = it.ctx - (t * kChunkKeys + src * R);   // valid rows, 0 < n < R
+                        if (lane < 4) {
+                            const uint32_t d0 = sv + src * R * 512 + lane * R * 128;
+                            int o = 0;
+                            for (int b = 5; b >= 0; --b)
+                                if (n >> b & 1) {
+                                    tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, y + o, 4 * int(rank) + lane);
+                                    o += 1 << b;
+                                }
+                            for (int b = 0; b < 6; ++b)
+                                if ((R - n) >> b & 1) {
+                                    tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, past, 4 * int(rank) + lane);
+                                    o += 1 << b;
+                                }
+                        }
+                        __syncwarp();
+                    }
+                }
+                ph ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMA issue (leader, lane 0)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kChunkKeys, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, false, true);
+            const uint64_t dq = smem_desc(smem_u32(smem + kQOff), 16, 1024, 2);
+            const uint64_t dk = smem_desc(smem_u32(smem + kKOff), 16, 1024, 2);
+            const uint64_t dp = smem_desc(smem_u32(smem + kPOff), 16, 1024, 2);
+            const uint64_t dv = smem_desc(smem_u32(smem + kVOff), uint32_t(R) * 128, 1024, 2);
+            int kph = 0, vph = 0, qph = 0, pph = 0, ofph = 0;
+            uint32_t g = 0;                      // tiles so far: S of tile g is in buffer g & 1
+            bool ok = true;
+            auto qk = [&](uint32_t buf) -> bool {
+                for (int j = 0; j < kKGroups; ++j) {
+                    if (!mbar_wait_cluster(&k_full[j], kph, abort_flag, status)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = 0; b < kKBlks; ++b)
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const uint32_t o = uint32_t((j * kKBlks + b) * kBlk + k4 * 32) >> 4;
+                            mma_pair_bf16(tmem + kSCol + buf * 64, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u);
+                        }
+                    commit_pair(&k_empty[j]);
+                }
+                kph ^= 1;
+                commit_pair(&s_full[buf]);
+                return true;
+            };
+            for (int i = pair; ok && i < num_items; i += a.pairs) {
+                const ChunkItem it = items[i];
+                const int nt = it.t_hi - it.t_lo;
+                if (nt <= 0) continue;
+                if (!mbar_wait_cluster(q_full, qph, abort_flag, status)) break;
+                qph ^= 1;
+                if (!qk(g & 1)) break;
+                for (int t = 0; t < nt; ++t, ++g) {
+                    if (t + 1 < nt) {
+                        if (!qk((g + 1) & 1)) { ok = false; break; }
+                    } else {
+                        commit_pair(q_empty);
+                    }
+                    if (!mbar_wait_cluster(p_full, pph, abort_flag, status)) { ok = false; break; }
+                    pph ^= 1;
+                    if (t == 0) {
+                        if (!mbar_wait_cluster(o_free, ofph ^ 1, abort_flag, status)) { ok = false; break; }
+                        ofph ^= 1;
+                    }
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (!mbar_wait_cluster(&v_full[hh], vph, abort_flag, status)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll
+                        for (int s4 = 0; s4 < 4; ++s4) {
+                            const int row = s4 * 16;
+                            const uint32_t vo = uint32_t(hh * kVHalf + row / R * (R * 512) + row % R * 128) >> 4;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                mma_pair_bf16(tmem + kOCol + h * 128, dp + uint64_t((hh * kBlk + s4 * 32) >> 4),
+                                              dv + uint64_t(vo + uint32_t(h * R * 256 >> 4)), idesc_pv,
+                                              (t | hh | s4) != 0 ? 1u : 0u);
+                        }
+                        commit_pair(&v_empty[hh]);
+                    }
+                    if (!ok) break;
+                    vph ^= 1;
+                    commit_pair(pv_done);
+                }
+            }
+            commit_pair(drain);
+        }
+        // every MMA has completed before TMEM and shared memory go (bounded like every wait)
+        volatile int never = 0;
+        if (lane == 0) mbar_wait_cluster(drain, 0, &never, status);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // -------------------------------------------------------- softmax and epilogue
+        const int quad = warp & 3;
+        const int tl = quad * 32 + lane;         // TMEM lane: row tl & 63, half tl >> 6 of the columns
+        const int row = tl & 63, half = tl >> 6;
+        const uint32_t t_lane = tmem + (uint32_t(quad * 32) << 16);
+        const uint32_t bp = map_to_rank(smem_u32(p_full), 0), bo = map_to_rank(smem_u32(o_free), 0);
+        const float cl = a.scale * 1.4426950408889634f;
+        const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
+        uint8_t* prow = smem + kPOff + half * kBlk + row * 128;
+        float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
+        float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
+        uint32_t g = 0;
+        bool ok = true;
+        for (int i = pair; ok && i < num_items; i += a.pairs) {
+            const ChunkItem it = items[i];
+            const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
+            const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
+            const bool live = qi_in < a.tile.tokens && qi < it.ntok && hs < a.Hs;
+            const int lim = live ? min(it.seen + qi, a.tok_hi) : 0;      // keys [tok_lo, lim)
+            const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
+            float m = -INFINITY, l = 0.f;
+            for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
+                const int key0 = t * kChunkKeys + half * kChunkRows;
+                bool missing = false;            // a page without a valid id among this half's keys
+                for (int k = 0; k < loads; ++k)
+                    missing |= key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s_full[g & 1], (g >> 1) & 1, abort_flag, status)))
+                    ok = false;
+                if (named_barrier_or(1, kSoftThreads, !ok)) { ok = false; break; }
+                tc_fence_after();
+                float x[64];
+                tmem_ld32(t_lane + kSCol + (g & 1) * 64, x);
+                tmem_ld32(t_lane + kSCol + (g & 1) * 64 + 32, x + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 64; ++e) x[e] *= cl;
+                if (missing || key0 < a.tok_lo || key0 + kChunkRows > lim) {
+                    uint32_t gone = 0;           // bit k: load k's page has no valid id
+                    for (int k = 0; k < loads; ++k)
+                        if (page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        if (key0 + e < a.tok_lo || key0 + e >= lim || (gone >> (e >> rlog) & 1)) x[e] = -INFINITY;
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = x[e];
+#pragma unroll
+                for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float* ex = sm_max + (g & 1) * (2 * kChunkRows);
+                ex[half * kChunkRows + row] = top;
+                named_barrier_sync(1, kSoftThreads);
+                top = fmaxf(top, ex[(half ^ 1) * kChunkRows + row]);
+                // both threads of a row see the same maxima, so they take the same branch
+                float alpha = 1.f;
+                const bool up = top > m + kTau;
+                if (up) {
+                    alpha = m == -INFINITY ? 0.f : ex2(m - top);
+                    m = top;
+                    l *= alpha;
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                uint32_t pk[32];
+                float ls[2] = {0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const float p0 = ex2(x[e] - base), p1 = ex2(x[e + 1] - base);
+                    ls[0] += p0;                 // the sum takes P before its rounding to bf16
+                    ls[1] += p1;
+                    pk[e >> 1] = pack2(p0, p1);
+                }
+                l += ls[0] + ls[1];
+                // P's buffer is free and O is at rest once the previous tile's MMAs are done
+                if (g > 0) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status)))
+                        ok = false;
+                }
+                if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 32) {
+                        float o[32];
+                        tmem_ld32(t_lane + kOCol + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            tmem_st16(t_lane + kOCol + c + q * 16, *reinterpret_cast<float(*)[16]>(o + q * 16));
+                    }
+                    tmem_wait_st();
+                }
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch)
+                    *reinterpret_cast<uint4*>(prow + ((ch ^ (row & 7)) << 4)) =
+                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(bp);
+            }
+            if (!ok) break;
+            // ---------------------------------------------------- epilogue
+            const bool worked = it.t_hi > it.t_lo;
+            if (worked) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status))) ok = false;
+                if (named_barrier_or(1, kSoftThreads, !ok)) break;
+                tc_fence_after();
+            }
+            sm_sum[half * kChunkRows + row] = l;
+            named_barrier_sync(1, kSoftThreads);
+            l += sm_sum[(half ^ 1) * kChunkRows + row];
+            const bool none = l == 0.f;
+            const float inv = 1.f / l;
+            const bool whole = it.slot < 0;
+            const int64_t orow = int64_t(it.tok + qi) * a.H + a.head_lo + hs;
+            const int64_t prow_i = int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
+            float* of = whole ? static_cast<float*>(a.out) + orow * kDv : pout + prow_i * kDv;
+            of += half * 256;
+            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
+            const bool as_f32 = a.out_f32 || !whole;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                float o[32];
+                if (worked) {
+                    tmem_ld32(t_lane + kOCol + c, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                if (live && as_f32) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(of + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(ob + c + e) =
+                            make_uint4(pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]), pack2(o[e + 4], o[e + 5]),
+                                       pack2(o[e + 6], o[e + 7]));
+                }
+                __syncwarp();
+            }
+            if (live && half == 0)
+                *(whole ? a.lse + orow : plse + prow_i) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            if (worked) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(bo);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *status)
+        atomicOr(&reinterpret_cast<ChunkHeader*>(a.ws)->status, *status);
+    cluster_sync();                              // no CTA leaves while the other may still reach its memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
+    const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(chunk_attn_kernel), kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(chunk_attn_kernel, dim3(2 * a.pairs), dim3(kThreads), size_t(kSmem), stream, maps, a);
+}
+
+}  // namespace splash

@@ -63,6 +63,23 @@ cudaError_t launch_kv_migrate(const void* src, void* dst, size_t page_bytes, con
                               const int32_t* dst_ids, int n, int src_np, int dst_np, int sm_count,
                               cudaStream_t stream);
 
+struct RopeTable;
+struct RopeTable32;
+// Rotary positions of T x H head rows (dtype: SPLASH_BF16 / F16 / F32); `vec`: pointers, strides
+// and dims allow 16-byte vectors.
+cudaError_t launch_rope(const RopeTable& table, int dtype, int dims, bool interleaved, bool vec,
+                        const void* x, int64_t xt, int64_t xh, void* y, int64_t yt, int64_t yh,
+                        const int32_t* positions, int T, int H, int sms, cudaStream_t stream);
+// New tokens' keys into the cache (table null: the rope dims are not rotated).
+cudaError_t launch_kv_append(const RopeTable32* table, bool interleaved, bool mxfp8, const void* latent,
+                             int64_t latent_stride, const void* k_rope, int64_t rope_stride,
+                             const int32_t* cu_q, int B, int total_q, const int32_t* block_table,
+                             const int32_t* ctx_lens, int P, int num_pages, int max_pages, void* pool,
+                             cudaStream_t stream);
+cudaError_t launch_kv_unpack(const void* src, void* dst, int P, const int32_t* src_ids,
+                             const int32_t* dst_ids, int n, int src_np, int dst_np, int sms,
+                             cudaStream_t stream);
+
 // Tensor-core decode kernel: head groups of at most 64 heads, one CTA per (CTA group,
 // head group), persistent over the plan.  map_q covers q as [B*H rows][576] bf16 with
 // a {64, pad(group_heads)} box; map_kv covers the pool as [num_pages*P rows][576] with

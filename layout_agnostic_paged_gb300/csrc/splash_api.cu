@@ -4,11 +4,15 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <math.h>
+
 #include <mutex>
 #include <unordered_map>
 
+#include "chunk.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "rope.cuh"
 
 namespace splash {
 namespace {
@@ -103,6 +107,68 @@ bool encode_rows_576(CUtensorMap* m, const void* base, uint64_t rows, uint32_t b
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 map over rows of 576 seen as [9 blocks][...][64], innermost first: box {64, rest...} and
+// the 128-byte swizzle.  dims / strides (bytes) / box of the rank - 1 outer dims.
+bool encode_blocks(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[5] = {64}, s[5];
+    cuuint32_t b[5] = {64}, es[5] = {1, 1, 1, 1, 1};
+    for (int i = 1; i < rank; ++i) {
+        d[i] = dims[i - 1];
+        s[i - 1] = strides[i - 1];
+        b[i] = box[i - 1];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), d, s, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pool map [9][rows][64] with a {64, box_rows, box_blocks} box.
+bool encode_pool(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_blocks) {
+    const uint64_t dims[2] = {rows, 9}, strides[2] = {uint64_t(kDqk) * 2, 128};
+    const uint32_t box[2] = {box_rows, box_blocks};
+    return encode_blocks(m, base, 3, dims, strides, box);
+}
+
+// The frequencies of a rope description as 64-bit fractions of a turn per position.
+// Returns SPLASH_OK or the argument error.
+int rope_turns(const splash_rope_desc* d, uint64_t* turns, float* amplitude) {
+    if (!d) return SPLASH_ERR_INVALID_ARG;
+    if (d->dims < 2 || d->dims % 2 != 0) return SPLASH_ERR_INVALID_ARG;
+    if (d->dims > 2 * kMaxRopePairs) return SPLASH_ERR_UNSUPPORTED;
+    if (d->scaling < SPLASH_ROPE_PLAIN || d->scaling > SPLASH_ROPE_YARN) return SPLASH_ERR_INVALID_ARG;
+    if (!(d->base >= 1.0) || !isfinite(d->base) || !isfinite(d->amplitude)) return SPLASH_ERR_INVALID_ARG;
+    double lo = 0, hi = 0;
+    if (d->scaling != SPLASH_ROPE_PLAIN && (!(d->factor >= 1.0) || !isfinite(d->factor)))
+        return SPLASH_ERR_INVALID_ARG;
+    if (d->scaling == SPLASH_ROPE_YARN) {
+        if (!(d->base > 1.0) || !(d->orig_ctx > 0) || !(d->beta_fast > 0) || !(d->beta_slow > 0) ||
+            !isfinite(d->orig_ctx) || !isfinite(d->beta_fast) || !isfinite(d->beta_slow))
+            return SPLASH_ERR_INVALID_ARG;
+        const double two_pi = 6.283185307179586476925;
+        lo = floor(d->dims * log(d->orig_ctx / (two_pi * d->beta_fast)) / (2 * log(d->base)));
+        hi = ceil(d->dims * log(d->orig_ctx / (two_pi * d->beta_slow)) / (2 * log(d->base)));
+        lo = lo > 0 ? lo : 0;
+        hi = hi < d->dims - 1 ? hi : d->dims - 1;
+    }
+    for (int i = 0; i < d->dims / 2; ++i) {
+        double f = pow(d->base, -2.0 * i / d->dims);
+        if (d->scaling == SPLASH_ROPE_LINEAR) f /= d->factor;
+        if (d->scaling == SPLASH_ROPE_YARN) {
+            const double w = hi - lo > 0.001 ? hi - lo : 0.001;
+            double g = (i - lo) / w;
+            g = g < 0 ? 0 : (g > 1 ? 1 : g);
+            f = f * (1 - g) + f * g / d->factor;
+        }
+        // f <= 1 radian, so the fraction of a turn is below 1 / 6
+        turns[i] = uint64_t(ldexp(f * 0.15915494309189533577, 64) + 0.5);
+    }
+    *amplitude = float(d->amplitude);
+    return SPLASH_OK;
 }
 
 }  // namespace
@@ -298,6 +364,182 @@ int splash_kv_migrate(const void* src_pool, void* dst_pool, size_t page_bytes,
     if (launch_kv_migrate(src_pool, dst_pool, page_bytes, src_ids, dst_ids, n_pages, src_num_pages,
                           dst_num_pages, sms, reinterpret_cast<cudaStream_t>(stream)) !=
         cudaSuccess)
+        return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+int splash_rope(const splash_rope_desc* rope, int dtype, const void* x, int64_t x_token_stride,
+                int64_t x_head_stride, void* y, int64_t y_token_stride, int64_t y_head_stride,
+                const int32_t* positions, int T, int H, splash_stream_t stream) {
+    RopeTable table;
+    const int st = rope_turns(rope, table.turns, &table.amplitude);
+    if (st != SPLASH_OK) return st;
+    if (dtype != SPLASH_BF16 && dtype != SPLASH_F16 && dtype != SPLASH_F32) return SPLASH_ERR_UNSUPPORTED;
+    if (T < 0 || H < 0 || x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0)
+        return SPLASH_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return SPLASH_OK;
+    // rows of y may not share elements: the head rows of a token, then the tokens, or the other way round
+    const int64_t d = rope->dims, yt = y_token_stride, yh = y_head_stride;
+    if ((H > 1 && yh < d) || (T > 1 && yt < d)) return SPLASH_ERR_INVALID_ARG;
+    if (T > 1 && H > 1 && yt < (H - 1) * yh + d && yh < (T - 1) * yt + d) return SPLASH_ERR_INVALID_ARG;
+    if (!x || !y || !positions || !aligned(positions, 4)) return SPLASH_ERR_INVALID_ARG;
+    const int size = dtype == SPLASH_F32 ? 4 : 2;
+    if (!aligned(x, size) || !aligned(y, size)) return SPLASH_ERR_INVALID_ARG;
+    if (int64_t(T) * H >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
+    // 16-byte vectors where every head row allows them: the interleaved layout takes 8 (fp32: 4)
+    // consecutive dims, the half layout as many of each half
+    const int ve = 16 / size;
+    const bool vec = aligned(x, 16) && aligned(y, 16) && x_token_stride % ve == 0 && x_head_stride % ve == 0 &&
+                     yt % ve == 0 && yh % ve == 0 && (rope->interleaved ? d : d / 2) % ve == 0;
+    int dev = 0;
+    if (current_device(&dev) != 0) return SPLASH_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SPLASH_ERR_CUDA;
+    if (launch_rope(table, dtype, rope->dims, rope->interleaved != 0, vec, x, x_token_stride, x_head_stride, y, yt,
+                    yh, positions, T, H, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+int splash_kv_append(const splash_attn_desc* desc, const splash_rope_desc* rope, int format, const void* latent,
+                     int64_t latent_stride, const void* k_rope, int64_t k_rope_stride, const int32_t* cu_q,
+                     int total_q, const int32_t* block_table, const int32_t* ctx_lens, void* kv_pool,
+                     splash_stream_t stream) {
+    int st = validate_desc(desc);
+    if (st != SPLASH_OK) return st;
+    if (format != SPLASH_KV_BF16 && format != SPLASH_KV_MXFP8) return SPLASH_ERR_UNSUPPORTED;
+    RopeTable wide;
+    RopeTable32 table;
+    if (rope) {
+        st = rope_turns(rope, wide.turns, &table.amplitude);
+        if (st != SPLASH_OK) return st;
+        if (rope->dims != kDqk - kDv) return SPLASH_ERR_UNSUPPORTED;
+        for (int i = 0; i < 32; ++i) table.turns[i] = wide.turns[i];
+    }
+    if (total_q < 0 || latent_stride < 0 || k_rope_stride < 0) return SPLASH_ERR_INVALID_ARG;
+    if (total_q == 0 || desc->num_reqs == 0 || desc->num_pages == 0 || desc->max_pages_per_req == 0) return SPLASH_OK;
+    if (latent_stride % 8 != 0 || k_rope_stride % 2 != 0) return SPLASH_ERR_INVALID_ARG;
+    if (!latent || !k_rope || !cu_q || !block_table || !ctx_lens || !kv_pool) return SPLASH_ERR_INVALID_ARG;
+    if (!aligned(latent, 16) || !aligned(k_rope, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4) ||
+        !aligned(ctx_lens, 4) || !aligned(kv_pool, 16))
+        return SPLASH_ERR_INVALID_ARG;
+    if (launch_kv_append(rope ? &table : nullptr, rope ? rope->interleaved != 0 : true, format == SPLASH_KV_MXFP8,
+                         latent, latent_stride, k_rope, k_rope_stride, cu_q, desc->num_reqs, total_q, block_table,
+                         ctx_lens, desc->page_size, desc->num_pages, desc->max_pages_per_req, kv_pool,
+                         reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+int splash_kv_unpack(const void* src_pool, void* dst_pool, int page_size, const int32_t* src_ids,
+                     const int32_t* dst_ids, int n_pages, int32_t src_num_pages, int32_t dst_num_pages,
+                     splash_stream_t stream) {
+    if (n_pages < 0 || page_size <= 0 || src_num_pages < 0 || dst_num_pages < 0) return SPLASH_ERR_INVALID_ARG;
+    if (n_pages == 0) return SPLASH_OK;
+    if (!src_pool || !dst_pool || !src_ids || !dst_ids) return SPLASH_ERR_INVALID_ARG;
+    if (!aligned(src_pool, 16) || !aligned(dst_pool, 16) || !aligned(src_ids, 4) || !aligned(dst_ids, 4))
+        return SPLASH_ERR_INVALID_ARG;
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(src_pool), d0 = reinterpret_cast<uintptr_t>(dst_pool);
+    const uintptr_t s1 = s0 + uintptr_t(src_num_pages) * page_size * kMxRowBytes;
+    const uintptr_t d1 = d0 + uintptr_t(dst_num_pages) * page_size * (kDqk * 2);
+    if (s0 < d1 && d0 < s1) return SPLASH_ERR_INVALID_ARG;
+    int dev = 0;
+    if (current_device(&dev) != 0) return SPLASH_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SPLASH_ERR_CUDA;
+    if (launch_kv_unpack(src_pool, dst_pool, page_size, src_ids, dst_ids, n_pages, src_num_pages, dst_num_pages, sms,
+                         reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+namespace {
+
+// Shape, tiling and workspace layout of a chunk call; returns its workspace bytes, 0 for a bad shape.
+size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi, ChunkArgs* a, int* sms) {
+    if (validate_desc(desc) != SPLASH_OK || total_q < 0) return 0;
+    if (head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return 0;
+    int dev = 0;
+    if (current_device(&dev) != 0) return 0;
+    *sms = sm_count(dev);
+    if (*sms < 2) return 0;
+    a->B = desc->num_reqs;
+    a->total_q = total_q;
+    a->H = desc->num_heads;
+    a->head_lo = head_lo;
+    a->Hs = head_hi - head_lo;
+    a->P = desc->page_size;
+    a->num_pages = desc->num_pages;
+    a->max_pages = desc->max_pages_per_req;
+    a->max_ctx = desc->max_pages_per_req * desc->page_size;
+    a->past_row = desc->num_pages > 0 ? desc->num_pages * desc->page_size : 1;
+    a->pairs = *sms / 2;
+    a->tile = chunk_tiling(a->Hs);
+    a->scale = desc->scale;
+    const size_t bytes = chunk_layout(*a);
+    if (a->cap_items >= (int64_t(1) << 31)) return 0;
+    return bytes;
+}
+
+}  // namespace
+
+size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi) {
+    ChunkArgs a = {};
+    int sms = 0;
+    return chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
+}
+
+int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool, const int32_t* cu_q,
+                      int total_q, const int32_t* block_table, const int32_t* ctx_lens, int head_lo, int head_hi,
+                      int64_t tok_lo, int64_t tok_hi, int out_dtype, void* out, float* lse, void* workspace,
+                      size_t ws_bytes, splash_stream_t stream_) {
+    const int st = validate_desc(desc);
+    if (st != SPLASH_OK) return st;
+    if (total_q < 0 || head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return SPLASH_ERR_INVALID_ARG;
+    if (tok_lo < 0 || (tok_hi >= 0 && tok_hi < tok_lo)) return SPLASH_ERR_INVALID_ARG;
+    if (out_dtype != SPLASH_BF16 && out_dtype != SPLASH_F32) return SPLASH_ERR_UNSUPPORTED;
+    if (int64_t(total_q) * desc->num_heads >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
+    if (!workspace || !aligned(workspace, 256)) return SPLASH_ERR_INVALID_ARG;
+    const bool work = desc->num_reqs > 0 && total_q > 0;
+    if (work) {
+        if (!q || !cu_q || !block_table || !ctx_lens || !out || !lse) return SPLASH_ERR_INVALID_ARG;
+        if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_q, 4) ||
+            !aligned(block_table, 4) || !aligned(ctx_lens, 4))
+            return SPLASH_ERR_INVALID_ARG;
+        if (desc->num_pages > 0 && (!kv_pool || !aligned(kv_pool, 16))) return SPLASH_ERR_INVALID_ARG;
+    }
+    ChunkArgs a = {};
+    int sms = 0;
+    const size_t need = chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
+    if (need == 0) return sms < 2 ? SPLASH_ERR_CUDA : SPLASH_ERR_UNSUPPORTED;
+    if (ws_bytes < need) return SPLASH_ERR_WORKSPACE;
+    if (!work) return SPLASH_OK;
+
+    const int64_t most = (int64_t(1) << 31) - 1;
+    a.cu_q = cu_q;
+    a.block_table = block_table;
+    a.ctx_lens = ctx_lens;
+    a.out = out;
+    a.lse = lse;
+    a.ws = static_cast<uint8_t*>(workspace);
+    a.tok_lo = int(tok_lo < most ? tok_lo : most);
+    a.tok_hi = int(tok_hi >= 0 && tok_hi < most ? tok_hi : most);
+    a.out_f32 = out_dtype == SPLASH_F32;
+    ChunkMaps maps;
+    const uint64_t row = uint64_t(kDqk) * 2;
+    const uint64_t qd[3] = {uint64_t(a.H), uint64_t(total_q), 9}, qs[3] = {row, row * a.H, 128};
+    const uint32_t qb[3] = {uint32_t(a.tile.heads), uint32_t(a.tile.tokens), 1};
+    // an empty pool still needs a valid map: one row of the workspace, which no copy reads
+    const void* kv = desc->num_pages > 0 ? kv_pool : workspace;
+    const uint64_t rows = uint64_t(a.past_row);
+    const uint32_t R = uint32_t(a.P < kChunkRows ? a.P : kChunkRows);
+    bool ok = encode_blocks(&maps.q, q, 4, qd, qs, qb) && encode_pool(&maps.k, kv, rows, kChunkRows, kChunkKBlocks) &&
+              encode_pool(&maps.v, kv, rows, R, 4);
+    for (int i = 0; ok && i < 6; ++i) ok = encode_pool(&maps.rows[i], kv, rows, 1u << i, 1);
+    if (!ok) return SPLASH_ERR_CUDA;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (launch_chunk_plan(a, stream) != cudaSuccess || launch_chunk_attn(a, maps, stream) != cudaSuccess ||
+        launch_chunk_combine(a, sms, stream) != cudaSuccess)
         return SPLASH_ERR_CUDA;
     return SPLASH_OK;
 }

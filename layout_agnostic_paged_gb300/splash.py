@@ -7,6 +7,7 @@ missing or the tensors are not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -26,8 +27,16 @@ SPLASH_DEVICE_BAD_INPUT = 2
 
 EXPORTED = ("splash_decode_workspace_size", "splash_decode_attn", "splash_decode_attn_ex",
             "splash_decode_attn_noalloc", "splash_noalloc_status",
-            "splash_lse_merge", "splash_kv_migrate", "splash_workspace_status",
-            "splash_status_string")
+            "splash_lse_merge", "splash_kv_migrate", "splash_rope", "splash_kv_append",
+            "splash_kv_unpack", "splash_chunk_workspace_size", "splash_chunk_attn",
+            "splash_workspace_status", "splash_status_string")
+
+SPLASH_BF16, SPLASH_F16, SPLASH_F32 = 0, 1, 2
+SPLASH_ROPE_PLAIN, SPLASH_ROPE_LINEAR, SPLASH_ROPE_YARN = 0, 1, 2
+SPLASH_KV_BF16, SPLASH_KV_MXFP8 = 0, 1
+MXFP8_ROW_BYTES = 656     # a token of an MXFP8 pool: 512 e4m3, 16 scale bytes, 64 bf16
+_DTYPES = {torch.bfloat16: SPLASH_BF16, torch.float16: SPLASH_F16, torch.float32: SPLASH_F32}
+_SCALINGS = {"none": SPLASH_ROPE_PLAIN, "linear": SPLASH_ROPE_LINEAR, "yarn": SPLASH_ROPE_YARN}
 
 
 class SplashError(RuntimeError):
@@ -47,6 +56,14 @@ class SplashDecodeExt(ctypes.Structure):
     _fields_ = [("tok_lo", ctypes.c_void_p), ("tok_hi", ctypes.c_void_p),
                 ("rows", ctypes.c_void_p), ("num_rows", ctypes.c_int32),
                 ("max_sms", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32)]
+
+
+class SplashRopeDesc(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_ctx", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double)]
 
 
 _lock = threading.Lock()
@@ -80,6 +97,18 @@ def load_library(path: str | None = None):
         lib.splash_lse_merge.restype = i32
         lib.splash_kv_migrate.argtypes = [vp, vp, sz, vp, vp, i32, ctypes.c_int32, ctypes.c_int32, vp]
         lib.splash_kv_migrate.restype = i32
+        rp = ctypes.POINTER(SplashRopeDesc)
+        lib.splash_rope.argtypes = [rp, i32, vp, i64, i64, vp, i64, i64, vp, i32, i32, vp]
+        lib.splash_rope.restype = i32
+        lib.splash_kv_append.argtypes = [dp, rp, i32, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp]
+        lib.splash_kv_append.restype = i32
+        lib.splash_kv_unpack.argtypes = [vp, vp, i32, vp, vp, i32, ctypes.c_int32, ctypes.c_int32, vp]
+        lib.splash_kv_unpack.restype = i32
+        lib.splash_chunk_workspace_size.argtypes = [dp, i32, i32, i32]
+        lib.splash_chunk_workspace_size.restype = sz
+        lib.splash_chunk_attn.argtypes = [dp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i64, i32, vp, vp,
+                                          vp, sz, vp]
+        lib.splash_chunk_attn.restype = i32
         lib.splash_workspace_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         lib.splash_workspace_status.restype = i32
         lib.splash_status_string.argtypes = [i32]
@@ -275,6 +304,160 @@ def splash_kv_migrate(src_pool: torch.Tensor, dst_pool: torch.Tensor, src_ids: t
                                               src_pool.shape[0], dst_pool.shape[0], _stream(stream))
     if rc != SPLASH_OK:
         raise SplashError(rc, "splash_kv_migrate")
+
+
+def _on(device: torch.device):
+    """Context in which `device` is current (none is entered where it is already)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(where: str, *ts):
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError(f"{where}: tensors must live on a CUDA device")
+        if t.device != ts[0].device:
+            raise ValueError(f"{where}: tensors must live on one device")
+
+
+def _index_arrays(where: str, B: int, cu_q, block_table, ctx_lens):
+    for t in (cu_q, block_table, ctx_lens):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{where}: cu_q, block_table and ctx_lens must be contiguous int32")
+    if cu_q.shape != (B + 1,) or block_table.dim() != 2 or block_table.shape[0] != B or ctx_lens.shape != (B,):
+        raise ValueError(f"{where}: cu_q [B + 1], block_table [B][max_pages] and ctx_lens [B] disagree")
+
+
+def make_rope_desc(dims: int, base: float = 10000.0, interleaved: bool = True, scaling: str = "none",
+                   factor: float = 1.0, orig_ctx: float = 4096.0, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0, amplitude: float = 1.0) -> SplashRopeDesc:
+    """Rotary positions of a model (see splash_rope_desc in splash.h); scaling is "none",
+    "linear" or "yarn"."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"make_rope_desc: scaling must be one of {sorted(_SCALINGS)}")
+    return SplashRopeDesc(int(dims), int(bool(interleaved)), _SCALINGS[scaling], 0, float(base), float(factor),
+                          float(orig_ctx), float(beta_fast), float(beta_slow), float(amplitude))
+
+
+def splash_rope(x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor, rope: SplashRopeDesc,
+                stream=None) -> None:
+    """out [T][H][d] <- x [T][H][d] rotated by positions int32 [T] (d = rope.dims).  Both are
+    views with dense head rows and any token and head strides, e.g. q[..., 512:]; out may
+    be x, and elements outside the views are not touched."""
+    _same_device("splash_rope", x, positions, out)
+    if x.dtype not in _DTYPES or out.dtype != x.dtype or positions.dtype != torch.int32:
+        raise ValueError("splash_rope: x and out must share bfloat16, float16 or float32; positions int32")
+    if x.dim() != 3 or x.shape != out.shape or x.shape[2] != rope.dims or positions.shape != (x.shape[0],):
+        raise ValueError("splash_rope: x and out must be [T][H][rope.dims], positions [T]")
+    if x.numel() and (x.stride(2) != 1 or out.stride(2) != 1 or not positions.is_contiguous()):
+        raise ValueError("splash_rope: head rows and positions must be dense")
+    with _on(x.device):
+        rc = load_library().splash_rope(
+            ctypes.byref(rope), _DTYPES[x.dtype], x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(),
+            out.stride(0), out.stride(1), positions.data_ptr(), x.shape[0], x.shape[1], _stream(stream))
+    if rc != SPLASH_OK:
+        raise SplashError(rc, "splash_rope")
+
+
+def splash_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, cu_q: torch.Tensor,
+                     block_table: torch.Tensor, ctx_lens: torch.Tensor, kv_pool: torch.Tensor,
+                     rope: SplashRopeDesc | None = None, stream=None) -> None:
+    """Writes new tokens (latent [N][512] and k_rope [N][64], bf16 with dense rows) to their slots
+    of kv_pool: bf16 [num_pages][P][576], or uint8 [num_pages][P][656] for MXFP8.  cu_q, block_table and
+    ctx_lens (the new tokens included) say where; rope rotates k_rope by the tokens' positions."""
+    _same_device("splash_kv_append", latent, k_rope, cu_q, block_table, ctx_lens, kv_pool)
+    N, B = latent.shape[0], ctx_lens.shape[0]
+    if latent.dtype != torch.bfloat16 or k_rope.dtype != torch.bfloat16:
+        raise ValueError("splash_kv_append: latent and k_rope must be bfloat16")
+    if latent.shape != (N, 512) or k_rope.shape != (N, 64) or (N and (latent.stride(1) != 1 or k_rope.stride(1) != 1)):
+        raise ValueError("splash_kv_append: latent [N][512] and k_rope [N][64] with dense rows")
+    if kv_pool.dtype == torch.bfloat16:
+        fmt, width = SPLASH_KV_BF16, 576
+    elif kv_pool.dtype == torch.uint8:
+        fmt, width = SPLASH_KV_MXFP8, MXFP8_ROW_BYTES
+    else:
+        raise ValueError("splash_kv_append: kv_pool must be bfloat16 or uint8 (MXFP8)")
+    if kv_pool.dim() != 3 or kv_pool.shape[2] != width or not kv_pool.is_contiguous():
+        raise ValueError(f"splash_kv_append: kv_pool must be contiguous [num_pages][P][{width}]")
+    _index_arrays("splash_kv_append", B, cu_q, block_table, ctx_lens)
+    desc = SplashAttnDesc(B, 1, 576, 512, kv_pool.shape[1], kv_pool.shape[0], block_table.shape[1], 1.0)
+    with _on(kv_pool.device):
+        rc = load_library().splash_kv_append(
+            ctypes.byref(desc), ctypes.byref(rope) if rope is not None else None, fmt, latent.data_ptr(),
+            latent.stride(0), k_rope.data_ptr(), k_rope.stride(0), cu_q.data_ptr(), N, block_table.data_ptr(),
+            ctx_lens.data_ptr(), kv_pool.data_ptr(), _stream(stream))
+    if rc != SPLASH_OK:
+        raise SplashError(rc, "splash_kv_append")
+
+
+def splash_kv_unpack(src_pool: torch.Tensor, dst_pool: torch.Tensor, src_ids: torch.Tensor,
+                     dst_ids: torch.Tensor, stream=None) -> None:
+    """bf16 dst_pool[dst_ids[i]] <- the values of MXFP8 src_pool[src_ids[i]] (uint8 [num_pages][P][656])."""
+    _same_device("splash_kv_unpack", src_pool, dst_pool, src_ids, dst_ids)
+    _check_cuda(src_pool, dst_pool, src_ids, dst_ids)
+    if src_ids.dtype != torch.int32 or dst_ids.dtype != torch.int32 or src_ids.shape != dst_ids.shape:
+        raise ValueError("splash_kv_unpack: ids must be int32 of equal length")
+    if (src_pool.dtype != torch.uint8 or dst_pool.dtype != torch.bfloat16 or src_pool.dim() != 3
+            or dst_pool.dim() != 3 or src_pool.shape[2] != MXFP8_ROW_BYTES or dst_pool.shape[2] != 576
+            or src_pool.shape[1] != dst_pool.shape[1]):
+        raise ValueError("splash_kv_unpack: src uint8 [num_pages][P][656], dst bfloat16 [num_pages][P][576]")
+    with _on(dst_pool.device):
+        rc = load_library().splash_kv_unpack(
+            src_pool.data_ptr(), dst_pool.data_ptr(), src_pool.shape[1], src_ids.data_ptr(), dst_ids.data_ptr(),
+            src_ids.numel(), src_pool.shape[0], dst_pool.shape[0], _stream(stream))
+    if rc != SPLASH_OK:
+        raise SplashError(rc, "splash_kv_unpack")
+
+
+def _chunk_desc(q, kv_pool, block_table, scale) -> SplashAttnDesc:
+    if q.dim() != 3 or kv_pool.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("splash_chunk_attn: q [N][H][576], kv_pool [num_pages][P][576], block_table [B][max_pages]")
+    desc = make_desc(q, kv_pool, block_table, scale)
+    desc.num_reqs = block_table.shape[0]
+    return desc
+
+
+def chunk_workspace(q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor, scale: float,
+                    head_lo: int = 0, head_hi: int | None = None) -> torch.Tensor:
+    """Allocates (with torch, on q's device) a workspace for splash_chunk_attn on q's rows; it serves
+    every later call with no more new tokens, requests and pages per request."""
+    desc = _chunk_desc(q, kv_pool, block_table, scale)
+    head_hi = q.shape[1] if head_hi is None else head_hi
+    with _on(q.device):
+        n = int(load_library().splash_chunk_workspace_size(ctypes.byref(desc), q.shape[0], int(head_lo),
+                                                           int(head_hi)))
+    if n == 0:
+        raise SplashError(SPLASH_ERR_UNSUPPORTED, "splash_chunk_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
+                      ctx_lens: torch.Tensor, head_lo: int, head_hi: int, tok_lo: int, tok_hi: int,
+                      out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, scale: float,
+                      stream=None) -> None:
+    """Causal attention of new tokens q [N][H][576] over the paged cache that holds them (see
+    splash.h); writes heads [head_lo, head_hi) of out [N][H][512] (bf16 or fp32) and lse [N][H]."""
+    _same_device("splash_chunk_attn", q, kv_pool, cu_q, block_table, ctx_lens, out, lse, workspace)
+    for t in (q, kv_pool, out, lse, workspace):
+        if not t.is_contiguous():
+            raise ValueError("splash_chunk_attn: tensors must be contiguous")
+    if (q.dtype != torch.bfloat16 or kv_pool.dtype != torch.bfloat16 or lse.dtype != torch.float32
+            or out.dtype not in (torch.bfloat16, torch.float32)):
+        raise ValueError("splash_chunk_attn: dtype mismatch")
+    desc = _chunk_desc(q, kv_pool, block_table, scale)
+    N, H, _ = q.shape
+    if out.shape != (N, H, 512) or lse.shape != (N, H):
+        raise ValueError("splash_chunk_attn: shape mismatch")
+    _index_arrays("splash_chunk_attn", desc.num_reqs, cu_q, block_table, ctx_lens)
+    with _on(q.device):
+        rc = load_library().splash_chunk_attn(
+            ctypes.byref(desc), q.data_ptr(), kv_pool.data_ptr(), cu_q.data_ptr(), N, block_table.data_ptr(),
+            ctx_lens.data_ptr(), int(head_lo), int(head_hi), int(tok_lo), int(tok_hi), _DTYPES[out.dtype],
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream(stream))
+    if rc != SPLASH_OK:
+        raise SplashError(rc, "splash_chunk_attn")
 
 
 def splash_workspace_status(workspace: torch.Tensor, stream=None) -> int:

@@ -25,8 +25,8 @@
 // each: a piece of it is loaded again as soon as the MMAs that read it are done, and needed a
 // whole tile later, because S of the next tile is computed before O of this one.
 //
-// Roles (256 threads): warp 0 loads Q and K, warp 2 loads V, lane 0 of the leader's warp 1 issues
-// every MMA, warps 4-7 run the softmax and the epilogue.
+// Roles (384 threads): warp 0 loads Q and K, warp 2 loads V, the leader's warp 1 issues every
+// MMA, warps 4-11 run the softmax and the epilogue.
 #include <math.h>
 
 #include "chunk.h"
@@ -49,12 +49,11 @@ constexpr int kBarOff = kPOff + 2 * kBlk;
 // barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O free, drain
 constexpr int kNumBars = 2 * kKGroups + 4 + 2 + 2 + 1 + 1 + 1 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
-constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][2 halves][64]
-constexpr int kSumOff = kMaxOff + 4 * kChunkRows * 4;   // row sums [2 halves][64]
-constexpr int kSmem = kSumOff + 2 * kChunkRows * 4 + 1024;   // + alignment slack
+constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 shares of the keys][64]; row sums reuse them
+constexpr int kSmem = kMaxOff + 8 * kChunkRows * 4;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kThreads = 256;
-constexpr int kSoftThreads = 128;
+constexpr int kThreads = 384;
+constexpr int kSoftThreads = 256;
 constexpr int kOCol = 0, kSCol = 256;            // TMEM: O in columns 0-255, S in 2 x 64
 constexpr int kTmemCols = 512;
 constexpr float kTau = 8.0f;                     // rescale O when a score beats the maximum by 2^8
@@ -79,8 +78,11 @@ __device__ __forceinline__ int page_of(const ChunkArgs& a, const int32_t* table,
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {                 // no room is left to align it here
+        if (threadIdx.x == 0) atomicOr(&reinterpret_cast<ChunkHeader*>(a.ws)->status, uint32_t(SPLASH_DEVICE_TIMEOUT));
+        return;
+    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint64_t* k_full = bars;                     // leader's: both CTAs' loads
     uint64_t* k_empty = k_full + kKGroups;       // each CTA's own, as every *_empty
@@ -97,15 +99,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 8);
     uint32_t* status = reinterpret_cast<uint32_t*>(smem + kMiscOff + 16);
     float* sm_max = reinterpret_cast<float*>(smem + kMaxOff);
-    float* sm_sum = reinterpret_cast<float*>(smem + kSumOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        // eight softmax warps of the pair arrive on P full and O free, one thread on the others
-        for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], &bars[i] == p_full || &bars[i] == o_free ? 8 : 1);
+        // the pair's 16 softmax warps arrive on P full and O free, one thread on the others
+        for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], &bars[i] == p_full || &bars[i] == o_free ? 16 : 1);
         *abort_flag = 0;
         *status = 0;
         fence_barrier_init();
@@ -235,87 +236,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // -------------------------------------------------------- MMA issue (leader, lane 0)
-        if (rank == 0 && lane == 0) {
+        // -------------------------------------------------------- MMA issue (leader)
+        // The whole warp walks the schedule in uniform control flow and one elected lane
+        // issues (see mma_pair_bf16).
+        if (rank == 0) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kChunkKeys, false, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, false, true);
+            const uint32_t on = elect_one();
             const uint64_t dq = smem_desc(smem_u32(smem + kQOff), 16, 1024, 2);
             const uint64_t dk = smem_desc(smem_u32(smem + kKOff), 16, 1024, 2);
             const uint64_t dp = smem_desc(smem_u32(smem + kPOff), 16, 1024, 2);
             const uint64_t dv = smem_desc(smem_u32(smem + kVOff), uint32_t(R) * 128, 1024, 2);
+            uint32_t vo[4];                      // 16-key steps of a V half
+            for (int s = 0; s < 4; ++s) vo[s] = uint32_t((s * 16 >> rlog) * (R * 512) + (s * 16 & (R - 1)) * 128) >> 4;
+            const uint32_t vh = uint32_t(R) * 256 >> 4;              // two 64-dim blocks on
             int kph = 0, vph = 0, qph = 0, pph = 0, ofph = 0;
             uint32_t g = 0;                      // tiles so far: S of tile g is in buffer g & 1
             bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+                const bool w = __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, status));
+                tc_fence_after();
+                return w;
+            };
             auto qk = [&](uint32_t buf) -> bool {
+#pragma unroll 1
                 for (int j = 0; j < kKGroups; ++j) {
-                    if (!mbar_wait_cluster(&k_full[j], kph, abort_flag, status)) return false;
-                    tc_fence_after();
+                    if (!wait(&k_full[j], kph)) return false;
+                    const uint32_t jo = uint32_t(j * kKBlks * kBlk) >> 4;
 #pragma unroll
                     for (int b = 0; b < kKBlks; ++b)
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
-                            const uint32_t o = uint32_t((j * kKBlks + b) * kBlk + k4 * 32) >> 4;
-                            mma_pair_bf16(tmem + kSCol + buf * 64, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u);
+                            const uint32_t o = jo + (uint32_t(b * kBlk + k4 * 32) >> 4);
+                            mma_pair_bf16(tmem + kSCol + buf * 64, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u, on);
                         }
-                    commit_pair(&k_empty[j]);
+                    commit_pair(&k_empty[j], on);
                 }
                 kph ^= 1;
-                commit_pair(&s_full[buf]);
+                commit_pair(&s_full[buf], on);
                 return true;
             };
             for (int i = pair; ok && i < num_items; i += a.pairs) {
-                const ChunkItem it = items[i];
-                const int nt = it.t_hi - it.t_lo;
+                const int nt = items[i].t_hi - items[i].t_lo;
                 if (nt <= 0) continue;
-                if (!mbar_wait_cluster(q_full, qph, abort_flag, status)) break;
+                if (!wait(q_full, qph)) break;
                 qph ^= 1;
                 if (!qk(g & 1)) break;
                 for (int t = 0; t < nt; ++t, ++g) {
                     if (t + 1 < nt) {
                         if (!qk((g + 1) & 1)) { ok = false; break; }
                     } else {
-                        commit_pair(q_empty);
+                        commit_pair(q_empty, on);
                     }
-                    if (!mbar_wait_cluster(p_full, pph, abort_flag, status)) { ok = false; break; }
+                    if (!wait(p_full, pph)) { ok = false; break; }
                     pph ^= 1;
                     if (t == 0) {
-                        if (!mbar_wait_cluster(o_free, ofph ^ 1, abort_flag, status)) { ok = false; break; }
+                        if (!wait(o_free, ofph ^ 1)) { ok = false; break; }
                         ofph ^= 1;
                     }
+#pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
-                        if (!mbar_wait_cluster(&v_full[hh], vph, abort_flag, status)) { ok = false; break; }
-                        tc_fence_after();
+                        if (!wait(&v_full[hh], vph)) { ok = false; break; }
+                        const uint32_t ho = uint32_t(hh * kVHalf) >> 4, po = uint32_t(hh * kBlk) >> 4;
 #pragma unroll
-                        for (int s4 = 0; s4 < 4; ++s4) {
-                            const int row = s4 * 16;
-                            const uint32_t vo = uint32_t(hh * kVHalf + row / R * (R * 512) + row % R * 128) >> 4;
+                        for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                mma_pair_bf16(tmem + kOCol + h * 128, dp + uint64_t((hh * kBlk + s4 * 32) >> 4),
-                                              dv + uint64_t(vo + uint32_t(h * R * 256 >> 4)), idesc_pv,
-                                              (t | hh | s4) != 0 ? 1u : 0u);
-                        }
-                        commit_pair(&v_empty[hh]);
+                                mma_pair_bf16(tmem + kOCol + h * 128, dp + (po + uint32_t(s4 * 2)), dv + (ho + vo[s4] + h * vh),
+                                              idesc_pv, (t | hh | s4) != 0 ? 1u : 0u, on);
+                        commit_pair(&v_empty[hh], on);
                     }
                     if (!ok) break;
                     vph ^= 1;
-                    commit_pair(pv_done);
+                    commit_pair(pv_done, on);
                 }
             }
-            commit_pair(drain);
+            commit_pair(drain, on);
         }
         // every MMA has completed before TMEM and shared memory go (bounded like every wait)
         volatile int never = 0;
-        if (lane == 0) mbar_wait_cluster(drain, 0, &never, status);
+        mbar_wait_cluster(drain, 0, &never, status);
         __syncwarp();
     } else if (warp >= 4) {
         // -------------------------------------------------------- softmax and epilogue
-        const int quad = warp & 3;
-        const int tl = quad * 32 + lane;         // TMEM lane: row tl & 63, half tl >> 6 of the columns
+        // Two warps per TMEM lane quadrant, each with 32 of a lane's 64 score columns: a lane
+        // is a row (tl & 63) and one half of the tile's keys, so four threads share a row.
+        const int quad = warp & 3, part = (warp - 4) >> 2;
+        const int tl = quad * 32 + lane;
         const int row = tl & 63, half = tl >> 6;
+        const int share = half * 2 + part;       // keys [32 share, 32 share + 32) of the tile
         const uint32_t t_lane = tmem + (uint32_t(quad * 32) << 16);
         const uint32_t bp = map_to_rank(smem_u32(p_full), 0), bo = map_to_rank(smem_u32(o_free), 0);
-        const float cl = a.scale * 1.4426950408889634f;
+        // scores in the exp2 domain are c * x, c > 0: the maximum is taken over x, so a negative
+        // scale moves its sign to x, and a zero one (0 * -inf is NaN) becomes part of x
+        const bool odd_scale = a.scale <= 0.f;
+        const float sign = a.scale < 0.f ? -1.f : 0.f;
+        const float cl = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
         uint8_t* prow = smem + kPOff + half * kBlk + row * 128;
         float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
@@ -329,41 +345,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool live = qi_in < a.tile.tokens && qi < it.ntok && hs < a.Hs;
             const int lim = live ? min(it.seen + qi, a.tok_hi) : 0;      // keys [tok_lo, lim)
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;        // maximum and sum (this thread's keys) of c * x
             for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
-                const int key0 = t * kChunkKeys + half * kChunkRows;
-                bool missing = false;            // a page without a valid id among this half's keys
-                for (int k = 0; k < loads; ++k)
-                    missing |= key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0;
+                const int key0 = t * kChunkKeys + share * 32;
+                uint32_t gone = 0;               // bit k: this thread's keys k R .. have no page
+                for (int k = 0; k * R < 32; ++k)
+                    if (key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s_full[g & 1], (g >> 1) & 1, abort_flag, status)))
                     ok = false;
-                if (named_barrier_or(1, kSoftThreads, !ok)) { ok = false; break; }
                 tc_fence_after();
-                float x[64];
-                tmem_ld32(t_lane + kSCol + (g & 1) * 64, x);
-                tmem_ld32(t_lane + kSCol + (g & 1) * 64 + 32, x + 32);
+                float x[32];
+                tmem_ld32(t_lane + kSCol + (g & 1) * 64 + part * 32, x);
                 tmem_wait_ld();
+                if (odd_scale) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e] *= cl;
-                if (missing || key0 < a.tok_lo || key0 + kChunkRows > lim) {
-                    uint32_t gone = 0;           // bit k: load k's page has no valid id
-                    for (int k = 0; k < loads; ++k)
-                        if (page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
+                    for (int e = 0; e < 32; ++e) x[e] *= sign;
+                }
+                if (gone || key0 < a.tok_lo || key0 + 32 > lim) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
+                    for (int e = 0; e < 32; ++e)
                         if (key0 + e < a.tok_lo || key0 + e >= lim || (gone >> (e >> rlog) & 1)) x[e] = -INFINITY;
                 }
                 float mx[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = x[e];
 #pragma unroll
-                for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+                for (int e = 4; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                float* ex = sm_max + (g & 1) * (2 * kChunkRows);
-                ex[half * kChunkRows + row] = top;
-                named_barrier_sync(1, kSoftThreads);
-                top = fmaxf(top, ex[(half ^ 1) * kChunkRows + row]);
-                // both threads of a row see the same maxima, so they take the same branch
+                float* ex = sm_max + (g & 1) * (4 * kChunkRows) + row;
+                ex[share * kChunkRows] = top;
+                if (named_barrier_or(1, kSoftThreads, !ok)) { ok = false; break; }
+                top = fmaxf(fmaxf(ex[0], ex[kChunkRows]), fmaxf(ex[2 * kChunkRows], ex[3 * kChunkRows]));
+                // the four threads of a row see the same maxima, so they take the same branch; a row
+                // whose keys are all masked so far has top = -inf and stays at m = -inf
+                top = top == -INFINITY ? top : top * cl;
                 float alpha = 1.f;
                 const bool up = top > m + kTau;
                 if (up) {
@@ -372,11 +387,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     l *= alpha;
                 }
                 const float base = m == -INFINITY ? 0.f : m;
-                uint32_t pk[32];
+                uint32_t pk[16];
                 float ls[2] = {0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const float p0 = ex2(x[e] - base), p1 = ex2(x[e + 1] - base);
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2(fmaf(x[e], cl, -base)), p1 = ex2(fmaf(x[e + 1], cl, -base));
                     ls[0] += p0;                 // the sum takes P before its rounding to bf16
                     ls[1] += p1;
                     pk[e >> 1] = pack2(p0, p1);
@@ -390,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
+                    for (int c = part * 128; c < part * 128 + 128; c += 32) {
                         float o[32];
                         tmem_ld32(t_lane + kOCol + c, o);
                         tmem_wait_ld();
@@ -403,8 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch)
-                    *reinterpret_cast<uint4*>(prow + ((ch ^ (row & 7)) << 4)) =
+                for (int ch = 0; ch < 4; ++ch)
+                    *reinterpret_cast<uint4*>(prow + (((part * 4 + ch) ^ (row & 7)) << 4)) =
                         make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -414,14 +429,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // ---------------------------------------------------- epilogue
             const bool worked = it.t_hi > it.t_lo;
-            if (worked) {
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status))) ok = false;
-                if (named_barrier_or(1, kSoftThreads, !ok)) break;
-                tc_fence_after();
-            }
-            sm_sum[half * kChunkRows + row] = l;
-            named_barrier_sync(1, kSoftThreads);
-            l += sm_sum[(half ^ 1) * kChunkRows + row];
+            if (worked && !__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status)))
+                ok = false;
+            float* sums = sm_max + (g & 1) * (4 * kChunkRows) + row;   // not the last tile's buffer
+            sums[share * kChunkRows] = l;
+            if (named_barrier_or(1, kSoftThreads, !ok)) break;
+            tc_fence_after();
+            l = (sums[0] + sums[kChunkRows]) + (sums[2 * kChunkRows] + sums[3 * kChunkRows]);
             const bool none = l == 0.f;
             const float inv = 1.f / l;
             const bool whole = it.slot < 0;
@@ -432,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
             const bool as_f32 = a.out_f32 || !whole;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = part * 128; c < part * 128 + 128; c += 32) {
                 float o[32];
                 if (worked) {
                     tmem_ld32(t_lane + kOCol + c, o);
@@ -453,13 +467,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (live && half == 0)
+            if (live && share == 0)
                 *(whole ? a.lse + orow : plse + prow_i) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             if (worked) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(bo);
             }
+            named_barrier_sync(1, kSoftThreads);  // the sums are read before the next tile writes there
         }
     }
 

@@ -136,7 +136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = pair; ok && i < num_items; i += a.pairs) {
             const ChunkItem it = items[i];
             if (it.t_lo >= it.t_hi) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(q_empty, qph ^ 1, abort_flag, status))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(q_empty, qph ^ 1, abort_flag, status))) break;
             qph ^= 1;
             const int tok = it.tok + (one_group ? int(rank) * a.tile.tokens : 0);
             const int h0 = a.head_lo + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
@@ -155,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     else if (key < it.ctx) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
                 for (int g = 0; g < kKGroups; ++g) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&k_empty[g], ph ^ 1, abort_flag, status))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[g], ph ^ 1, abort_flag, status))) {
                         ok = false;
                         break;
                     }
@@ -198,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (id >= 0) row = id * a.P + key % a.P;
                 }
                 for (int hh = 0; hh < 2; ++hh) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&v_empty[hh], ph ^ 1, abort_flag, status))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[hh], ph ^ 1, abort_flag, status))) {
                         ok = false;
                         break;
                     }
@@ -254,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t g = 0;                      // tiles so far: S of tile g is in buffer g & 1
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                const bool w = __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, status));
+                const bool w = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
                 tc_fence_after();
                 return w;
             };
@@ -315,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // every MMA has completed before TMEM and shared memory go (bounded like every wait)
         volatile int never = 0;
-        mbar_wait_cluster(drain, 0, &never, status);
+        mbar_wait(drain, 0, &never, status);
         __syncwarp();
     } else if (warp >= 4) {
         // -------------------------------------------------------- softmax and epilogue
@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t gone = 0;               // bit k: this thread's keys k R .. have no page
                 for (int k = 0; k * R < 32; ++k)
                     if (key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s_full[g & 1], (g >> 1) & 1, abort_flag, status)))
+                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag, status)))
                     ok = false;
                 tc_fence_after();
                 float x[32];
@@ -399,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 l += ls[0] + ls[1];
                 // P's buffer is free and O is at rest once the previous tile's MMAs are done
                 if (g > 0) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status)))
+                    if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, abort_flag, status)))
                         ok = false;
                 }
                 if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
@@ -424,12 +424,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(bp);
+                if (lane == 0) mbar_arrive_pair(bp);
             }
             if (!ok) break;
             // ---------------------------------------------------- epilogue
             const bool worked = it.t_hi > it.t_lo;
-            if (worked && !__all_sync(0xffffffffu, mbar_wait_cluster(pv_done, (g - 1) & 1, abort_flag, status)))
+            if (worked && !__all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, abort_flag, status)))
                 ok = false;
             float* sums = sm_max + (g & 1) * (4 * kChunkRows) + row;   // not the last tile's buffer
             sums[share * kChunkRows] = l;
@@ -472,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (worked) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(bo);
+                if (lane == 0) mbar_arrive_pair(bo);
             }
             named_barrier_sync(1, kSoftThreads);  // the sums are read before the next tile writes there
         }

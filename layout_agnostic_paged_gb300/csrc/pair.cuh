@@ -27,39 +27,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     return r;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// mbar_wait (common.cuh) for a phase that the other CTA's threads or copies complete.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  uint32_t* status) {
-    const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait_cluster(a, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait_cluster(a, parity)) return true;
-        if ((it & 63) == 63) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                atomicOr(status, (uint32_t)SPLASH_DEVICE_TIMEOUT);
-                return false;
-            }
-        }
-    }
+// Arrives on a barrier of the pair.  No generic-proxy data crosses the CTAs with it: what
+// the arrival announces is read by the tensor core, from the shared memory or TMEM of the SM that wrote it, after
+// the writer's own proxy fence (or tcgen05 fence) has completed.  So neither this nor the
+// waits need cluster scope.  With .release.cluster here and .acquire.cluster in the waits an
+// arrival took 1,500 clocks, and every wait emptied the L1 cache of the block table.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // TMA loads into this CTA's shared memory that complete on a barrier of the pair

@@ -387,7 +387,7 @@ SPLASH_API size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int 
  * out = 0 and lse = -inf.  A share [tok_lo, tok_hi) gives the partial that splash_lse_merge
  * combines (fp32 out).
  *   q           bf16 [total_q][H][576], contiguous, 16-byte aligned
- *   out         [total_q][H][512] of out_dtype (SPLASH_BF16 or SPLASH_F32), 16-byte aligned
+ *   out         [total_q][H][512] of out_dtype (SPLASH_BF16 or SPLASH_F32), 32-byte aligned
  *   lse         fp32 [total_q][H]
  *   head_lo/hi, tok_lo/hi, kv_pool, block_table, ctx_lens: as for splash_decode_attn, desc->num_reqs
  *               = B; one shared KV head

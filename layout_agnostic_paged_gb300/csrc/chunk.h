@@ -33,13 +33,13 @@ inline ChunkTiling chunk_tiling(int Hs) {
     return t;
 }
 
-// Workspace: header, work items, split row tiles, partial lse, partial out (256-byte
-// aligned each).
+// Workspace: header, the pairs' item ranges (int2), work items, split row tiles, partial
+// lse, partial out (256-byte aligned each).
 struct ChunkHeader {
     uint32_t status;      // SPLASH_DEVICE_* bits of the last call
     int32_t num_items;
     int32_t num_splits;   // row tiles cut into several items
-    int32_t pad;
+    int32_t stride;       // pair j works on items first[j], first[j] + stride, .. below last[j]
 };
 
 // One pair's work: the rows of one token block and head group pair against key tiles
@@ -69,11 +69,11 @@ struct ChunkArgs {
     void* out;
     float* lse;
     uint8_t* ws;
-    size_t items_off, splits_off, plse_off, pout_off;
+    size_t ranges_off, items_off, splits_off, plse_off, pout_off;
     int64_t cap_items;
     int cap_slots;
     int B, total_q, H, head_lo, Hs;
-    int P, num_pages, max_pages, max_ctx;
+    int P, P_log, num_pages, max_pages, max_ctx;   // P = 2^P_log
     int past_row;         // a row of the pool's maps that does not exist: copies from there fill zeros
     int tok_lo, tok_hi;   // tok_hi: INT32_MAX for "to the end"
     int pairs;            // CTA pairs of the grid

@@ -69,10 +69,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// One 32-byte store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // The page id behind a key, or -1 where there is none (past the context, or a bad id).
 __device__ __forceinline__ int page_of(const ChunkArgs& a, const int32_t* table, int key, int ctx) {
     if (key >= ctx) return -1;
-    const int id = table[key / a.P];
+    const int id = table[key >> a.P_log];
     return id >= 0 && id < a.num_pages ? id : -1;
 }
 
@@ -121,7 +128,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     const ChunkHeader* head = reinterpret_cast<const ChunkHeader*>(a.ws);
     const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.items_off);
-    const int num_items = head->num_items;
+    const int2 range = reinterpret_cast<const int2*>(a.ws + a.ranges_off)[pair];
+    const int stride = head->stride;
     const int R = min(a.P, kChunkRows);          // rows of one load: pages of 128 come in halves
     const int loads = kChunkRows / R;            // loads for 64 keys
     const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
@@ -133,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bq = map_to_rank(smem_u32(q_full), 0);
         int ph = 0, qph = 0;
         bool ok = true;
-        for (int i = pair; ok && i < num_items; i += a.pairs) {
+        for (int i = range.x; ok && i < range.y; i += stride) {
             const ChunkItem it = items[i];
             if (it.t_lo >= it.t_hi) continue;
             if (!__all_sync(0xffffffffu, mbar_wait(q_empty, qph ^ 1, abort_flag, status))) break;
@@ -151,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int row = a.past_row;            // past the pool: the copy fills zeros
                 if (lane < loads) {
                     const int id = page_of(a, table, key, it.ctx);
-                    if (id >= 0) row = id * a.P + key % a.P;
+                    if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
                     else if (key < it.ctx) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
                 for (int g = 0; g < kKGroups; ++g) {
@@ -187,7 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int past = a.past_row;
         int ph = 0;
         bool ok = true;
-        for (int i = pair; ok && i < num_items; i += a.pairs) {
+        for (int i = range.x; ok && i < range.y; i += stride) {
             const ChunkItem it = items[i];
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
@@ -195,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int row = past;
                 if (lane < 2 * loads) {
                     const int id = page_of(a, table, key, it.ctx);
-                    if (id >= 0) row = id * a.P + key % a.P;
+                    if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
                 }
                 for (int hh = 0; hh < 2; ++hh) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[hh], ph ^ 1, abort_flag, status))) {
@@ -276,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 commit_pair(&s_full[buf], on);
                 return true;
             };
-            for (int i = pair; ok && i < num_items; i += a.pairs) {
+            for (int i = range.x; ok && i < range.y; i += stride) {
                 const int nt = items[i].t_hi - items[i].t_lo;
                 if (nt <= 0) continue;
                 if (!wait(q_full, qph)) break;
@@ -338,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
         uint32_t g = 0;
         bool ok = true;
-        for (int i = pair; ok && i < num_items; i += a.pairs) {
+        for (int i = range.x; ok && i < range.y; i += stride) {
             const ChunkItem it = items[i];
             const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
             const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
@@ -445,39 +453,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             of += half * 256;
             __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
             const bool as_f32 = a.out_f32 || !whole;
+            if (as_f32) {
 #pragma unroll 1
-            for (int c = part * 128; c < part * 128 + 128; c += 32) {
-                float o[32];
+                for (int c = part * 128; c < part * 128 + 128; c += 32) {
+                    float o[32];
+                    if (worked) {
+                        tmem_ld32(t_lane + kOCol + c, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store32(of + c + e, reinterpret_cast<const uint32_t*>(o) + e);
+                    }
+                    __syncwarp();
+                }
                 if (worked) {
-                    tmem_ld32(t_lane + kOCol + c, o);
-                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bo);
                 }
+            } else {
+                // all of this thread's columns into registers first: O is free for the next item's MMAs while
+                // they are stored (the stores, a row of each lane, take longer than the loads)
+                uint32_t packed[64];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                if (live && as_f32) {
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    if (worked) {
+                        tmem_ld32(t_lane + kOCol + part * 128 + c * 32, o);
+                        tmem_wait_ld();
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(of + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(ob + c + e) =
-                            make_uint4(pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]), pack2(o[e + 4], o[e + 5]),
-                                       pack2(o[e + 6], o[e + 7]));
+                    for (int e = 0; e < 16; ++e)
+                        packed[c * 16 + e] = none ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
                 }
-                __syncwarp();
+                if (worked) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bo);
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8) store32(ob + part * 128 + 2 * e, packed + e);
+                }
             }
             if (live && share == 0)
                 *(whole ? a.lse + orow : plse + prow_i) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            if (worked) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(bo);
-            }
             named_barrier_sync(1, kSoftThreads);  // the sums are read before the next tile writes there
         }
     }
 
+    // the merge may launch: at the start its waiting blocks would hold SMs that another stream needs
+    pdl_trigger();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *status)

@@ -2,10 +2,14 @@
 // and keys) and the merge of row tiles that the plan cut.
 //
 // A row tile (128 query rows of one request, see chunk.h) is the natural unit of work, but
-// there may be fewer of them than CTA pairs, with contexts of any length.  The plan cuts a
-// request's row tiles along the keys into equal pieces when that shortens the call: it
-// estimates the call's length in key tiles for five piece lengths, from the requests' lengths,
-// and takes the best.  One block; a few microseconds.
+// there may be fewer of them than CTA pairs, with contexts of any length.  The plan has two ways to
+// lay the row tiles over the pairs, and takes the one that it expects to be shorter:
+//   - even: the row tiles' key tiles, in order, cut into one equal run per pair.  A run's ends may
+//     fall inside a row tile, whose pieces are then merged.  For up to 1,024 row tiles, unless
+//     the row tiles of one request would sweep a context larger than L2 out of step;
+//   - dealt: row tile i goes to pair i mod pairs, so that the pairs sweep the same context together
+//     and share it in L2.  Requests with long contexts are cut into equal pieces if that helps.
+// One block; its time is latency, so the block is small for few requests.
 #include <limits.h>
 #include <math.h>
 
@@ -18,13 +22,16 @@
 namespace splash {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;        // most threads of the plan's block, and row tiles of an even cut
 constexpr int kCuts = 4;                  // piece lengths tried: an even share of 1..4 rounds of the pairs
-// Costs in key tiles, measured against the 1.5 us of a key tile: what an item costs beside its tiles
-// (first loads, epilogue), what a partial costs to write and merge, and the merge's own latency.
-constexpr float kItemCost = 2.0f;
-constexpr float kSlotCost = 0.06f;
+// Costs in key tiles (1.15 us each): what an item costs beside its tiles (first loads, epilogue), what a
+// partial costs to write and merge, and the merge's own latency.
+constexpr float kItemCost = 3.0f;
+constexpr float kSlotCost = 0.04f;
 constexpr float kMergeCost = 1.5f;
+constexpr int kLeastPiece = 2;            // an even cut leaves no piece of fewer tiles
+// Contexts (bytes) whose row tiles may be swept out of step: what stays in the 129 MB L2.
+constexpr int64_t kSharedBytes = 96ll << 20;
 
 struct Span {
     int c0, n;        // first row and number of new tokens
@@ -52,163 +59,292 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     return s;
 }
 
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+// Sums N values over the block.
+template <int N>
+__device__ __forceinline__ void block_sum(int (&v)[N], int (*scratch)[N]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t s = scratch[threadIdx.x & 31];
+    for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, v[k]);
+    if (lane == 0)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int k = 0; k < N; ++k) scratch[warp][k] = v[k];
     __syncthreads();
-    return s;
+    const bool in = lane < int(blockDim.x >> 5);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, in ? scratch[lane][k] : 0);
+    __syncthreads();
 }
 
-// Exclusive prefix sum over the block; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {
+// Exclusive prefix sums of N values over the block; totals[] get the sums.
+template <int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*scratch)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t s = v;
+    int s[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += x;
-    }
-    if (lane == 31) scratch[warp] = s;
-    __syncthreads();
-    int64_t w = scratch[lane];
+    for (int k = 0; k < N; ++k) {
+        s[k] = v[k];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, s[k], o);
+            if (lane >= o) s[k] += x;
+        }
+        if (lane == 31) scratch[warp][k] = s[k];
     }
-    const int64_t before = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
-    *total = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
-    return before + s - v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int w = lane < int(blockDim.x >> 5) ? scratch[lane][k] : 0;
+        const int own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += x;
+        }
+        totals[k] = __shfl_sync(0xffffffffu, w, 31);
+        v[k] = __shfl_sync(0xffffffffu, w - own, warp) + s[k] - v[k];
+    }
+    __syncthreads();
+}
+
+// The row tile `tile` of request r.
+__device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s, int r, int tile, int* tiles) {
+    const int pg = a.tile.pair_groups(), per_block = a.tile.pair_tokens();
+    ChunkItem it = {};
+    it.r = r;
+    it.tok = s.c0 + (pg == 1 ? tile : tile / pg) * per_block;
+    it.ntok = s.c0 + s.n - it.tok;
+    it.pair_group = pg == 1 ? 0 : tile % pg;
+    it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
+    it.ctx = s.ctx;
+    it.slot = -1;
+    *tiles = key_tiles(a, it.seen + min(it.ntok, per_block) - 1);
+    return it;
+}
+
+// The last index in [0, n) with from[i] <= x (from[0] <= x, ascending).
+__device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (from[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
-    __shared__ int64_t scratch[32];
-    __shared__ int64_t item0[kPlanThreads + 1], slot0[kPlanThreads], split0[kPlanThreads];
+    __shared__ int scratch1[32][1], scratch3[32][3], scratch4[32][4], scratch8[32][2 * kCuts];
+    __shared__ int from[kPlanThreads + 1], slot0[kPlanThreads], split0[kPlanThreads];
     __shared__ int pieces[kPlanThreads], piece_tiles[kPlanThreads];
+    // the attention's blocks may set themselves up while the plan runs
+    pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, NT = blockDim.x;
     ChunkHeader* head = reinterpret_cast<ChunkHeader*>(a.ws);
+    int2* ranges = reinterpret_cast<int2*>(a.ws + a.ranges_off);
     ChunkItem* items = reinterpret_cast<ChunkItem*>(a.ws + a.items_off);
     ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(a.ws + a.splits_off);
 
-    // all the row tiles, all their key tiles (a row tile's are about the mean of its request's
-    // first and last), the longest
-    int64_t U = 0, C2 = 0, longest = 0;
-    bool bad = false;
-    for (int r = tid; r < a.B; r += kPlanThreads) {
+    // all the row tiles, all their key tiles in 1/16 (a row tile's are about the mean of its request's first
+    // and last), the longest, whether an even cut is allowed
+    Span mine = {};
+    float C = 0.f;
+    int sums[4] = {0, 0, 0, 0}, longest = 0;
+    for (int r = tid; r < a.B; r += NT) {
         const Span s = span_of(a, r);
-        U += s.u;
-        C2 += int64_t(s.u) * (s.m + (s.n > 0 ? key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())) : 0));
-        if (s.u > 0 && s.m > longest) longest = s.m;
-        bad |= s.bad;
+        if (r == tid) mine = s;
+        sums[0] += s.u;
+        if (s.n > 0) C += 0.5f * float(s.u) * float(s.m + key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())));
+        sums[1] |= s.bad;
+        sums[2] |= s.u > 1 && int64_t(s.ctx) * (kDqk * 2) > kSharedBytes;
+        if (s.u > 0) longest = max(longest, s.m);
     }
-    U = block_sum(U, scratch);
-    const float C = 0.5f * float(block_sum(C2, scratch));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const int64_t x = __shfl_xor_sync(0xffffffffu, longest, o);
-        longest = x > longest ? x : longest;
+    for (int o = 16; o > 0; o >>= 1) C += __shfl_xor_sync(0xffffffffu, C, o);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if ((tid & 31) == 0) {
+        from[tid >> 5] = longest;
+        slot0[tid >> 5] = __float_as_int(C);
     }
-    if ((tid & 31) == 0) scratch[tid >> 5] = longest;
-    bad = __syncthreads_or(bad);
-    for (int i = 0; i < 32; ++i) longest = scratch[i] > longest ? scratch[i] : longest;
-    __syncthreads();
+    block_sum<4>(sums, scratch4);
+    const int U = sums[0];
+    const bool bad = sums[1] != 0;
+    C = 0.f;
+    for (int i = 0; i < (NT >> 5); ++i) {
+        longest = max(longest, from[i]);
+        C += __int_as_float(slot0[i]);
+    }
 
     const float G = float(a.pairs);
     int best_len = INT_MAX;
     float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
-    for (int w = 1; w <= kCuts && U > 0; ++w) {
-        const int len = max(1, int(ceilf(C / (G * float(w)))));
-        if (len >= longest) continue;
-        int64_t n = 0, slots = 0;
-        for (int r = tid; r < a.B; r += kPlanThreads) {
-            const Span s = span_of(a, r);
-            const int np = max(1, (s.m + len - 1) / len);
-            n += int64_t(s.u) * np;
-            if (np > 1) slots += int64_t(s.u) * np;
+    const bool may_cut = a.cap_slots > 0 && U > 0;
+    // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
+    const float even = (C + kItemCost * (float(U) + G)) / G + 2.f * G * kSlotCost + kMergeCost;
+    // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles)
+    const int64_t tiles_most = int64_t(U) * longest;
+    const bool room = tiles_most < (1 << 30) && U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
+                      (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs) <= a.cap_slots;
+    const bool is_even = may_cut && room && U <= NT && a.pairs <= NT && sums[2] == 0 && even < best;
+    if (!is_even && may_cut) {
+        int n[2 * kCuts] = {};
+        for (int r = tid; r < a.B; r += NT) {
+            const Span s = r == tid ? mine : span_of(a, r);
+#pragma unroll
+            for (int w = 0; w < kCuts; ++w) {
+                const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
+                const int np = max(1, (s.m + len - 1) / len);
+                n[w] += s.u * np;
+                if (np > 1) n[kCuts + w] += s.u * np;
+            }
         }
-        n = block_sum(n, scratch);
-        slots = block_sum(slots, scratch);
-        const float cost = fmaxf(float(len) + kItemCost, ceilf(float(n) / G) * (C / float(n) + kItemCost)) +
-                           float(slots) * kSlotCost + kMergeCost;
-        if (slots <= a.cap_slots && cost < best) {
-            best = cost;
-            best_len = len;
+        block_sum<2 * kCuts>(n, scratch8);
+#pragma unroll
+        for (int w = 0; w < kCuts; ++w) {
+            const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
+            const float cost = fmaxf(float(len) + kItemCost, ceilf(float(n[w]) / G) * (C / float(n[w]) + kItemCost)) +
+                               float(n[kCuts + w]) * kSlotCost + kMergeCost;
+            if (len < longest && n[kCuts + w] <= a.cap_slots && cost < best) {
+                best = cost;
+                best_len = len;
+            }
         }
     }
+    __syncthreads();
 
-    int64_t item_base = 0, slot_base = 0, split_base = 0;
-    const int per_block = a.tile.pair_tokens(), pg = a.tile.pair_groups();
-    for (int r0 = 0; r0 < a.B; r0 += kPlanThreads) {
-        const int r = r0 + tid;
-        Span s = {};
-        int np = 1;
-        if (r < a.B) {
-            s = span_of(a, r);
-            np = best_len == INT_MAX ? 1 : max(1, (s.m + best_len - 1) / best_len);
-        }
-        const int64_t n = int64_t(s.u) * np;
-        int64_t all, all_slots, all_splits;
-        const int64_t i0 = block_scan(n, scratch, &all);
-        const int64_t sl0 = block_scan(np > 1 ? n : 0, scratch, &all_slots);
-        const int64_t sp0 = block_scan(np > 1 ? s.u : 0, scratch, &all_splits);
-        item0[tid] = i0;
-        slot0[tid] = slot_base + sl0;
-        split0[tid] = split_base + sp0;
-        pieces[tid] = np;
-        piece_tiles[tid] = (s.m + np - 1) / np;
-        if (tid == kPlanThreads - 1) item0[kPlanThreads] = all;
-        __syncthreads();
-        for (int64_t i = tid; i < all; i += kPlanThreads) {
-            int lo = 0, hi = kPlanThreads;          // the last request with item0 <= i
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (item0[mid] <= i) lo = mid;
-                else hi = mid;
+    int num_items = 0, num_splits = 0;
+    if (is_even) {
+        // one thread per row tile; from[] holds the requests' first row tiles
+        int my_r = 0, my_tile = 0, base = 0;
+        for (int r0 = 0; r0 < a.B; r0 += NT) {
+            const bool in = r0 + tid < a.B;
+            int v[1] = {!in ? 0 : (r0 == 0 ? mine.u : span_of(a, r0 + tid).u)}, tot[1];
+            block_scan<1>(v, tot, scratch1);
+            from[tid] = base + v[0];
+            __syncthreads();
+            if (tid >= base && tid < base + tot[0]) {
+                const int k = last_at_most(from, min(NT, a.B - r0), tid);
+                my_r = r0 + k;
+                my_tile = tid - from[k];
             }
-            const Span q = span_of(a, r0 + lo);
-            const int k = pieces[lo];
-            const int64_t local = i - item0[lo];
-            const int tile = int(local / k), piece = int(local % k);
-            ChunkItem it = {};
-            it.r = r0 + lo;
-            it.tok = q.c0 + tile / pg * per_block;
-            it.ntok = q.c0 + q.n - it.tok;
-            it.pair_group = tile % pg;
-            it.seen = q.ctx - q.n + (it.tok - q.c0) + 1;
-            it.ctx = q.ctx;
+            base += tot[0];
+            __syncthreads();
+        }
+        const bool has = tid < U;
+        ChunkItem it = {};
+        int tiles = 0;
+        if (has) it = row_tile(a, span_of(a, my_r), my_r, my_tile, &tiles);
+        // positions along the sequence in tiles, an item's own cost included: pair j's run is
+        // [j T / P, (j + 1) T / P), and this row tile's tiles lie at [A + own, A + own + tiles)
+        const int own = int(kItemCost);
+        int v[1] = {has ? tiles + own : 0}, W[1];
+        block_scan<1>(v, W, scratch1);
+        const int A = v[0];
+        const int64_t T = W[0], P = a.pairs;
+        int j0 = 0, j1 = -1;
+        if (has) {
+            j0 = int(((int64_t(A) + 1) * P - 1) / T);
+            j1 = int(((int64_t(A) + own + tiles) * P - 1) / T);
+        }
+        auto cut = [&](int j) -> int {            // first tile of pair j's piece
+            if (j <= j0) return 0;
+            if (j > j1) return tiles;
+            const int x = int(int64_t(j) * T / P) - A - own;
+            return x < kLeastPiece ? 0 : (tiles - x < kLeastPiece ? tiles : x);
+        };
+        int np = 0;
+        for (int j = j0; j <= j1; ++j) np += cut(j + 1) > cut(j);
+        if (has && np == 0) np = 1;               // no key in sight: its rows become zeros
+        int c[3] = {np, np > 1 ? np : 0, np > 1 ? 1 : 0}, tot[3];
+        block_scan<3>(c, tot, scratch3);
+        // the items are in the order of their pairs, so a pair's are a range: first in from[], end in slot0[]
+        for (int j = tid; j < a.pairs; j += NT) {
+            from[j] = INT_MAX;
+            slot0[j] = 0;
+        }
+        __syncthreads();
+        if (has) {
             const int t0 = a.tok_lo / kChunkKeys;
-            const int nt = key_tiles(a, it.seen + min(it.ntok, per_block) - 1);
-            it.t_lo = t0 + min(nt, piece * piece_tiles[lo]);
-            it.t_hi = t0 + min(nt, (piece + 1) * piece_tiles[lo]);
-            it.slot = k > 1 ? int(slot0[lo] + local) : -1;
-            if (item_base + i < a.cap_items) items[item_base + i] = it;
-            if (k > 1 && piece == 0) {
+            int k = 0;
+            for (int j = j0; k < np; ++j) {
+                const int lo = cut(j), hi = cut(j + 1);
+                if (hi <= lo && tiles > 0) continue;
+                it.t_lo = t0 + lo;
+                it.t_hi = t0 + hi;
+                it.slot = np > 1 ? c[1] + k : -1;
+                items[c[0] + k] = it;
+                atomicMin(&from[j], c[0] + k);
+                atomicMax(&slot0[j], c[0] + k + 1);
+                ++k;
+            }
+            if (np > 1) {
                 ChunkSplit sp = {};
                 sp.tok = it.tok;
                 sp.ntok = it.ntok;
                 sp.pair_group = it.pair_group;
-                sp.slot = it.slot;
-                sp.pieces = k;
-                splits[split0[lo] + tile] = sp;
+                sp.slot = c[1];
+                sp.pieces = np;
+                splits[c[2]] = sp;
             }
         }
-        item_base += all;
-        slot_base += all_slots;
-        split_base += all_splits;
         __syncthreads();
+        for (int j = tid; j < a.pairs; j += NT) ranges[j] = make_int2(from[j], slot0[j]);
+        num_items = tot[0];
+        num_splits = tot[2];
+    } else {
+        int slot_base = 0;
+        for (int r0 = 0; r0 < a.B; r0 += NT) {
+            const int r = r0 + tid;
+            Span s = {};
+            int np = 1;
+            if (r < a.B) {
+                s = r0 == 0 ? mine : span_of(a, r);
+                np = best_len == INT_MAX ? 1 : max(1, (s.m + best_len - 1) / best_len);
+            }
+            const int n = s.u * np;
+            int c[3] = {n, np > 1 ? n : 0, np > 1 ? s.u : 0}, tot[3];
+            block_scan<3>(c, tot, scratch3);
+            from[tid] = c[0];
+            slot0[tid] = slot_base + c[1];
+            split0[tid] = num_splits + c[2];
+            pieces[tid] = np;
+            piece_tiles[tid] = (s.m + np - 1) / np;
+            __syncthreads();
+            for (int i = tid; i < tot[0]; i += NT) {
+                const int q = last_at_most(from, NT, i);
+                const int k = pieces[q], local = i - from[q];
+                const int tile = k == 1 ? local : local / k, piece = k == 1 ? 0 : local % k;
+                int tiles;
+                ChunkItem it = row_tile(a, span_of(a, r0 + q), r0 + q, tile, &tiles);
+                const int t0 = a.tok_lo / kChunkKeys;
+                it.t_lo = t0 + min(tiles, piece * piece_tiles[q]);
+                it.t_hi = t0 + min(tiles, (piece + 1) * piece_tiles[q]);
+                if (k > 1) it.slot = slot0[q] + local;
+                if (num_items + i < a.cap_items) items[num_items + i] = it;
+                if (k > 1 && piece == 0) {
+                    ChunkSplit sp = {};
+                    sp.tok = it.tok;
+                    sp.ntok = it.ntok;
+                    sp.pair_group = it.pair_group;
+                    sp.slot = it.slot;
+                    sp.pieces = k;
+                    splits[split0[q] + tile] = sp;
+                }
+            }
+            num_items += tot[0];
+            slot_base += tot[1];
+            num_splits += tot[2];
+            __syncthreads();
+        }
+        // offsets that overlap (a bad cu_q) could ask for more than the capacity
+        num_items = int(num_items < a.cap_items ? num_items : a.cap_items);
+        for (int j = tid; j < a.pairs; j += NT) ranges[j] = make_int2(j, num_items);
     }
     if (tid == 0) {
-        // the capacities bound both counts; an item past them would be a fault of theirs
         head->status = bad ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
-        head->num_items = int(item_base < a.cap_items ? item_base : a.cap_items);
-        head->num_splits = int(split_base);
+        head->num_items = num_items;
+        head->num_splits = num_splits;
+        head->stride = is_even ? 1 : a.pairs;
     }
 }
 
@@ -291,7 +427,8 @@ size_t chunk_layout(ChunkArgs& a) {
     const int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles);
     a.cap_slots = int(slots);
     a.cap_items = u + slots;
-    a.items_off = 256;
+    a.ranges_off = 256;
+    a.items_off = align256(a.ranges_off + sizeof(int2) * size_t(a.pairs));
     a.splits_off = align256(a.items_off + sizeof(ChunkItem) * size_t(a.cap_items));
     a.plse_off = align256(a.splits_off + sizeof(ChunkSplit) * size_t(slots));
     a.pout_off = align256(a.plse_off + size_t(slots) * 2 * kChunkRows * sizeof(float));
@@ -299,7 +436,9 @@ size_t chunk_layout(ChunkArgs& a) {
 }
 
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
-    return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+    // few requests and row tiles: a block whose barriers cost less
+    const bool few = a.B <= 256 && a.cap_items - a.cap_slots <= 256;
+    return launch_pdl(chunk_plan_kernel, dim3(1), dim3(few ? 256 : kPlanThreads), 0, stream, a);
 }
 
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int sms, cudaStream_t stream) {

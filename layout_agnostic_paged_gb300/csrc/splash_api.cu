@@ -469,6 +469,7 @@ size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int h
     a->head_lo = head_lo;
     a->Hs = head_hi - head_lo;
     a->P = desc->page_size;
+    a->P_log = a->P == 16 ? 4 : (a->P == 32 ? 5 : (a->P == 64 ? 6 : 7));
     a->num_pages = desc->num_pages;
     a->max_pages = desc->max_pages_per_req;
     a->max_ctx = desc->max_pages_per_req * desc->page_size;
@@ -503,7 +504,7 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     const bool work = desc->num_reqs > 0 && total_q > 0;
     if (work) {
         if (!q || !cu_q || !block_table || !ctx_lens || !out || !lse) return SPLASH_ERR_INVALID_ARG;
-        if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_q, 4) ||
+        if (!aligned(q, 16) || !aligned(out, 32) || !aligned(lse, 4) || !aligned(cu_q, 4) ||
             !aligned(block_table, 4) || !aligned(ctx_lens, 4))
             return SPLASH_ERR_INVALID_ARG;
         if (desc->num_pages > 0 && (!kv_pool || !aligned(kv_pool, 16))) return SPLASH_ERR_INVALID_ARG;

@@ -25,8 +25,9 @@
 // each: a piece of it is loaded again as soon as the MMAs that read it are done, and needed a
 // whole tile later, because S of the next tile is computed before O of this one.
 //
-// Roles (384 threads): warp 0 loads Q and K, warp 2 loads V, the leader's warp 1 issues every
-// MMA, warps 4-11 run the softmax and the epilogue.
+// Roles (512 threads): warp 0 loads Q and K, warp 2 loads V, the leader's warp 1 issues every
+// MMA, warps 4-11 run the softmax, warps 12-15 store the results.  Storing takes as long as two key
+// tiles (a warp's store covers 32 rows), so it has warps of its own, beside the next item's first tiles.
 #include <math.h>
 
 #include "chunk.h"
@@ -46,13 +47,15 @@ constexpr int kVOff = kKOff + 9 * kBlk;          // [2 halves of the keys][pages
 constexpr int kVHalf = 4 * kBlk;
 constexpr int kPOff = kVOff + 2 * kVHalf;        // [2 halves of the keys][64 rows][128 B]
 constexpr int kBarOff = kPOff + 2 * kBlk;
-// barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O free, drain
-constexpr int kNumBars = 2 * kKGroups + 4 + 2 + 2 + 1 + 1 + 1 + 1;
+// barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O full / free,
+// row statistics full / empty, drain
+constexpr int kNumBars = 2 * kKGroups + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 shares of the keys][64]; row sums reuse them
-constexpr int kSmem = kMaxOff + 8 * kChunkRows * 4;
+constexpr int kFinOff = kMaxOff + 8 * kChunkRows * 4;   // an item's final (maximum, sum) of every row
+constexpr int kSmem = kFinOff + kChunkRows * 8;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kSoftThreads = 256;
 constexpr int kOCol = 0, kSCol = 256;            // TMEM: O in columns 0-255, S in 2 x 64
 constexpr int kTmemCols = 512;
@@ -100,20 +103,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* s_full = q_full + 2;               // each CTA's
     uint64_t* p_full = s_full + 2;               // leader's: the softmax warps of both CTAs
     uint64_t* pv_done = p_full + 1;              // each CTA's
-    uint64_t* o_free = pv_done + 1;              // leader's
-    uint64_t* drain = o_free + 1;                // each CTA's
+    uint64_t* o_full = pv_done + 1;              // each CTA's: the item's last PV is done
+    uint64_t* o_free = o_full + 1;               // leader's: the storing warps of both CTAs
+    uint64_t* fin_full = o_free + 1;             // each CTA's own softmax and storing warps
+    uint64_t* fin_empty = fin_full + 1;
+    uint64_t* drain = fin_empty + 1;             // each CTA's
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 8);
     uint32_t* status = reinterpret_cast<uint32_t*>(smem + kMiscOff + 16);
     float* sm_max = reinterpret_cast<float*>(smem + kMaxOff);
+    float2* sm_fin = reinterpret_cast<float2*>(smem + kFinOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        // the pair's 16 softmax warps arrive on P full and O free, one thread on the others
-        for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], &bars[i] == p_full || &bars[i] == o_free ? 16 : 1);
+        // a warp's arrival counts once: 8 softmax and 4 storing warps a CTA, both CTAs' on P full and O free
+        for (int i = 0; i < kNumBars; ++i)
+            mbar_init(&bars[i], &bars[i] == p_full                            ? 16
+                                : &bars[i] == o_free                          ? 8
+                                : &bars[i] == fin_full                        ? 2
+                                : &bars[i] == fin_empty                       ? 4
+                                                                              : 1);
         *abort_flag = 0;
         *status = 0;
         fence_barrier_init();
@@ -317,6 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     vph ^= 1;
                     commit_pair(pv_done, on);
+                    if (t + 1 == nt) commit_pair(o_full, on);
                 }
             }
             commit_pair(drain, on);
@@ -325,8 +338,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         volatile int never = 0;
         mbar_wait(drain, 0, &never, status);
         __syncwarp();
-    } else if (warp >= 4) {
-        // -------------------------------------------------------- softmax and epilogue
+    } else if (warp >= 4 && warp < 12) {
+        // -------------------------------------------------------- softmax
         // Two warps per TMEM lane quadrant, each with 32 of a lane's 64 score columns: a lane
         // is a row (tl & 63) and one half of the tile's keys, so four threads share a row.
         const int quad = warp & 3, part = (warp - 4) >> 2;
@@ -334,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row = tl & 63, half = tl >> 6;
         const int share = half * 2 + part;       // keys [32 share, 32 share + 32) of the tile
         const uint32_t t_lane = tmem + (uint32_t(quad * 32) << 16);
-        const uint32_t bp = map_to_rank(smem_u32(p_full), 0), bo = map_to_rank(smem_u32(o_free), 0);
+        const uint32_t bp = map_to_rank(smem_u32(p_full), 0);
         // scores in the exp2 domain are c * x, c > 0: the maximum is taken over x, so a negative
         // scale moves its sign to x, and a zero one (0 * -inf is NaN) becomes part of x
         const bool odd_scale = a.scale <= 0.f;
@@ -342,9 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float cl = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
         uint8_t* prow = smem + kPOff + half * kBlk + row * 128;
-        float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
-        float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
         uint32_t g = 0;
+        int fph = 0;
         bool ok = true;
         for (int i = range.x; ok && i < range.y; i += stride) {
             const ChunkItem it = items[i];
@@ -413,15 +425,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = part * 128; c < part * 128 + 128; c += 32) {
-                        float o[32];
-                        tmem_ld32(t_lane + kOCol + c, o);
+                    for (int c = part * 128; c < part * 128 + 128; c += 16) {
+                        float o[16];
+                        tmem_ld16(t_lane + kOCol + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            tmem_st16(t_lane + kOCol + c + q * 16, *reinterpret_cast<float(*)[16]>(o + q * 16));
+                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                        tmem_st16(t_lane + kOCol + c, o);
                     }
                     tmem_wait_st();
                 }
@@ -435,73 +445,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_pair(bp);
             }
             if (!ok) break;
-            // ---------------------------------------------------- epilogue
-            const bool worked = it.t_hi > it.t_lo;
-            if (worked && !__all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, abort_flag, status)))
-                ok = false;
+            if (it.t_hi <= it.t_lo) continue;
+            // the rows' sums over the four shares of the keys, and their maxima, to the storing warps
             float* sums = sm_max + (g & 1) * (4 * kChunkRows) + row;   // not the last tile's buffer
             sums[share * kChunkRows] = l;
+            named_barrier_sync(1, kSoftThreads);
+            if (share == 0) {                    // the part 0 warps of lanes 0-63: two whole warps
+                if (!__all_sync(0xffffffffu, mbar_wait(fin_empty, fph ^ 1, abort_flag, status))) ok = false;
+                l = (sums[0] + sums[kChunkRows]) + (sums[2 * kChunkRows] + sums[3 * kChunkRows]);
+                sm_fin[row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(fin_full);
+            }
+            fph ^= 1;
+            // the sums are read before the next tile's maxima take their place
             if (named_barrier_or(1, kSoftThreads, !ok)) break;
-            tc_fence_after();
-            l = (sums[0] + sums[kChunkRows]) + (sums[2 * kChunkRows] + sums[3 * kChunkRows]);
+        }
+    } else if (warp >= 12) {
+        // -------------------------------------------------------- results
+        const int tl = (warp & 3) * 32 + lane;   // TMEM lane: row tl & 63, value dims [256 (tl >> 6), + 256)
+        const int row = tl & 63, half = tl >> 6;
+        const uint32_t t_o = tmem + (uint32_t((warp & 3) * 32) << 16) + kOCol;
+        const uint32_t bo = map_to_rank(smem_u32(o_free), 0);
+        const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
+        float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
+        float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
+        int ph = 0;
+        bool ok = true;
+        for (int i = range.x; ok && i < range.y; i += stride) {
+            const ChunkItem it = items[i];
+            const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
+            const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
+            const bool live = qi_in < a.tile.tokens && qi < it.ntok && hs < a.Hs;
+            const bool worked = it.t_hi > it.t_lo;   // no key tile: zeros
+            float m = 0.f, l = 0.f;
+            if (worked) {
+                if (!__all_sync(0xffffffffu, mbar_wait(fin_full, ph, abort_flag, status))) break;
+                const float2 f = sm_fin[row];
+                m = f.x;
+                l = f.y;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(fin_empty);
+                if (!__all_sync(0xffffffffu, mbar_wait(o_full, ph, abort_flag, status))) break;
+                ph ^= 1;
+                tc_fence_after();
+            }
             const bool none = l == 0.f;
             const float inv = 1.f / l;
             const bool whole = it.slot < 0;
             const int64_t orow = int64_t(it.tok + qi) * a.H + a.head_lo + hs;
-            const int64_t prow_i = int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
-            float* of = whole ? static_cast<float*>(a.out) + orow * kDv : pout + prow_i * kDv;
-            of += half * 256;
-            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
+            const int64_t prow = int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
+            if (live && half == 0)
+                *(whole ? a.lse + orow : plse + prow) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             const bool as_f32 = a.out_f32 || !whole;
+            float* of = (whole ? static_cast<float*>(a.out) + orow * kDv : pout + prow * kDv) + half * 256;
+            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
             if (as_f32) {
 #pragma unroll 1
-                for (int c = part * 128; c < part * 128 + 128; c += 32) {
+                for (int c = 0; c < 256; c += 32) {
                     float o[32];
                     if (worked) {
-                        tmem_ld32(t_lane + kOCol + c, o);
+                        tmem_ld32(t_o + c, o);
                         tmem_wait_ld();
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                    if (worked && c == 224) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(bo);
+                    }
                     if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) store32(of + c + e, reinterpret_cast<const uint32_t*>(o) + e);
                     }
                     __syncwarp();
                 }
-                if (worked) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(bo);
-                }
             } else {
-                // all of this thread's columns into registers first: O is free for the next item's MMAs while
-                // they are stored (the stores, a row of each lane, take longer than the loads)
-                uint32_t packed[64];
+                // the second half of the columns is in registers, and O free, before its stores
+#pragma unroll 1
+                for (int c0 = 0; c0 < 256; c0 += 128) {
+                    uint32_t packed[64];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
-                    if (worked) {
-                        tmem_ld32(t_lane + kOCol + part * 128 + c * 32, o);
-                        tmem_wait_ld();
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        if (worked) {
+                            tmem_ld16(t_o + c0 + c * 16, o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            packed[c * 8 + e] = none ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
                     }
+                    if (worked && c0 == 128) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(bo);
+                    }
+                    if (live) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        packed[c * 16 + e] = none ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-                }
-                if (worked) {
-                    tc_fence_before();
+                        for (int e = 0; e < 64; e += 8) store32(ob + c0 + 2 * e, packed + e);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(bo);
-                }
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 8) store32(ob + part * 128 + 2 * e, packed + e);
                 }
             }
-            if (live && share == 0)
-                *(whole ? a.lse + orow : plse + prow_i) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            named_barrier_sync(1, kSoftThreads);  // the sums are read before the next tile writes there
         }
     }
 

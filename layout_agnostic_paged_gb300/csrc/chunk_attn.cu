@@ -49,7 +49,7 @@ constexpr int kPOff = kVOff + 2 * kVHalf;        // [2 halves of the keys][64 ro
 constexpr int kBarOff = kPOff + 2 * kBlk;
 // barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O full / free,
 // row statistics full / empty, drain
-constexpr int kNumBars = 2 * kKGroups + 4 + 2 + 2 + 1 + 1 + 2 + 2 + 1;
+constexpr int kNumBars = 4 * kKGroups + 4 + 2 + 1 + 1 + 2 + 2 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 shares of the keys][64]; row sums reuse them
 constexpr int kFinOff = kMaxOff + 8 * kChunkRows * 4;   // an item's final (maximum, sum) of every row
@@ -99,8 +99,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* v_full = k_empty + kKGroups;       // leader's
     uint64_t* v_empty = v_full + 2;
     uint64_t* q_full = v_empty + 2;              // leader's
-    uint64_t* q_empty = q_full + 1;
-    uint64_t* s_full = q_full + 2;               // each CTA's
+    uint64_t* q_empty = q_full + kKGroups;       // Q in the groups of K
+    uint64_t* s_full = q_empty + kKGroups;       // each CTA's
     uint64_t* p_full = s_full + 2;               // leader's: the softmax warps of both CTAs
     uint64_t* pv_done = p_full + 1;              // each CTA's
     uint64_t* o_full = pv_done + 1;              // each CTA's: the item's last PV is done
@@ -150,20 +150,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // -------------------------------------------------------- Q and K loads
         const uint32_t sq = smem_u32(smem + kQOff), sk = smem_u32(smem + kKOff);
-        const uint32_t bq = map_to_rank(smem_u32(q_full), 0);
         int ph = 0, qph = 0;
         bool ok = true;
+        ChunkItem it = {}, next = {};
+        if (range.x < range.y) next = items[range.x];
         for (int i = range.x; ok && i < range.y; i += stride) {
-            const ChunkItem it = items[i];
+            it = next;
+            if (i + stride < range.y) next = items[i + stride];
             if (it.t_lo >= it.t_hi) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait(q_empty, qph ^ 1, abort_flag, status))) break;
-            qph ^= 1;
             const int tok = it.tok + (one_group ? int(rank) * a.tile.tokens : 0);
             const int h0 = a.head_lo + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
-            if (rank == 0 && lane == 0)
-                mbar_arrive_expect_tx(q_full, 2 * 9 * a.tile.heads * a.tile.tokens * 128);
-            __syncwarp();
-            if (lane < 9) tma_pair_4d(sq + lane * kBlk, &maps.q, bq, 0, h0, tok, lane);
+            for (int g = 0; g < kKGroups && ok; ++g) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[g], qph ^ 1, abort_flag, status))) { ok = false; break; }
+                const uint32_t bar = map_to_rank(smem_u32(&q_full[g]), 0);
+                if (rank == 0 && lane == 0)
+                    mbar_arrive_expect_tx(&q_full[g], 2 * kKBlks * a.tile.heads * a.tile.tokens * 128);
+                __syncwarp();
+                const int b = g * kKBlks + lane;
+                if (lane < kKBlks) tma_pair_4d(sq + b * kBlk, &maps.q, bar, 0, h0, tok, b);
+            }
+            if (!ok) break;
+            qph ^= 1;
+            // Q of the next item comes from HBM while this one is worked on: its buffer is free only
+            // when the last scores are done, and the next item's first scores wait for it
+            if (i + stride < range.y && next.t_lo < next.t_hi && lane < 9)
+                tma_prefetch_4d(&maps.q, 0, a.head_lo + (one_group ? 0 : (2 * next.pair_group + int(rank)) * a.tile.heads),
+                                next.tok + (one_group ? int(rank) * a.tile.tokens : 0), lane);
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 // lane k < loads looks up the page behind keys [64 c + k R, + R) of the tile
@@ -278,9 +290,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 return w;
             };
-            auto qk = [&](uint32_t buf) -> bool {
+            auto qk = [&](uint32_t buf, bool first, bool last) -> bool {
 #pragma unroll 1
                 for (int j = 0; j < kKGroups; ++j) {
+                    if (first && !wait(&q_full[j], qph)) return false;
                     if (!wait(&k_full[j], kph)) return false;
                     const uint32_t jo = uint32_t(j * kKBlks * kBlk) >> 4;
 #pragma unroll
@@ -291,23 +304,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mma_pair_bf16(tmem + kSCol + buf * 64, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u, on);
                         }
                     commit_pair(&k_empty[j], on);
+                    if (last) commit_pair(&q_empty[j], on);
                 }
                 kph ^= 1;
                 commit_pair(&s_full[buf], on);
                 return true;
             };
+            int2 next = range.x < range.y ? make_int2(items[range.x].t_lo, items[range.x].t_hi) : make_int2(0, 0);
             for (int i = range.x; ok && i < range.y; i += stride) {
-                const int nt = items[i].t_hi - items[i].t_lo;
+                const int nt = next.y - next.x;
+                if (i + stride < range.y) next = make_int2(items[i + stride].t_lo, items[i + stride].t_hi);
                 if (nt <= 0) continue;
-                if (!wait(q_full, qph)) break;
+                if (!qk(g & 1, true, nt == 1)) break;
                 qph ^= 1;
-                if (!qk(g & 1)) break;
                 for (int t = 0; t < nt; ++t, ++g) {
-                    if (t + 1 < nt) {
-                        if (!qk((g + 1) & 1)) { ok = false; break; }
-                    } else {
-                        commit_pair(q_empty, on);
-                    }
+                    if (t + 1 < nt && !qk((g + 1) & 1, false, t + 2 == nt)) { ok = false; break; }
                     if (!wait(p_full, pph)) { ok = false; break; }
                     pph ^= 1;
                     if (t == 0) {

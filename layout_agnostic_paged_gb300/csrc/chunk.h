@@ -34,12 +34,12 @@ inline ChunkTiling chunk_tiling(int Hs) {
 }
 
 // Workspace: header, the pairs' item ranges (int2), work items, split row tiles, partial
-// lse, partial out (256-byte aligned each).
+// lse, partial out (256-byte aligned each).  Pair j works on items [ranges[j].x, ranges[j].y).
 struct ChunkHeader {
     uint32_t status;      // SPLASH_DEVICE_* bits of the last call
     int32_t num_items;
     int32_t num_splits;   // row tiles cut into several items
-    int32_t stride;       // pair j works on items first[j], first[j] + stride, .. below last[j]
+    int32_t pad;
 };
 
 // One pair's work: the rows of one token block and head group pair against key tiles

@@ -138,10 +138,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     pdl_wait();
-    const ChunkHeader* head = reinterpret_cast<const ChunkHeader*>(a.ws);
     const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.items_off);
     const int2 range = reinterpret_cast<const int2*>(a.ws + a.ranges_off)[pair];
-    const int stride = head->stride;
     const int R = min(a.P, kChunkRows);          // rows of one load: pages of 128 come in halves
     const int loads = kChunkRows / R;            // loads for 64 keys
     const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
@@ -154,9 +152,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         ChunkItem it = {}, next = {};
         if (range.x < range.y) next = items[range.x];
-        for (int i = range.x; ok && i < range.y; i += stride) {
+        for (int i = range.x; ok && i < range.y; ++i) {
             it = next;
-            if (i + stride < range.y) next = items[i + stride];
+            if (i + 1 < range.y) next = items[i + 1];
             if (it.t_lo >= it.t_hi) continue;
             const int tok = it.tok + (one_group ? int(rank) * a.tile.tokens : 0);
             const int h0 = a.head_lo + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
@@ -173,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             qph ^= 1;
             // Q of the next item comes from HBM while this one is worked on: its buffer is free only
             // when the last scores are done, and the next item's first scores wait for it
-            if (i + stride < range.y && next.t_lo < next.t_hi && lane < 9)
+            if (i + 1 < range.y && next.t_lo < next.t_hi && lane < 9)
                 tma_prefetch_4d(&maps.q, 0, a.head_lo + (one_group ? 0 : (2 * next.pair_group + int(rank)) * a.tile.heads),
                                 next.tok + (one_group ? int(rank) * a.tile.tokens : 0), lane);
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
@@ -219,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int past = a.past_row;
         int ph = 0;
         bool ok = true;
-        for (int i = range.x; ok && i < range.y; i += stride) {
+        for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
@@ -290,38 +288,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 return w;
             };
-            auto qk = [&](uint32_t buf, bool first, bool last) -> bool {
-#pragma unroll 1
-                for (int j = 0; j < kKGroups; ++j) {
-                    if (first && !wait(&q_full[j], qph)) return false;
-                    if (!wait(&k_full[j], kph)) return false;
-                    const uint32_t jo = uint32_t(j * kKBlks * kBlk) >> 4;
-#pragma unroll
-                    for (int b = 0; b < kKBlks; ++b)
-#pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            const uint32_t o = jo + (uint32_t(b * kBlk + k4 * 32) >> 4);
-                            mma_pair_bf16(tmem + kSCol + buf * 64, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u, on);
-                        }
-                    commit_pair(&k_empty[j], on);
-                    if (last) commit_pair(&q_empty[j], on);
-                }
-                kph ^= 1;
-                commit_pair(&s_full[buf], on);
-                return true;
-            };
             int2 next = range.x < range.y ? make_int2(items[range.x].t_lo, items[range.x].t_hi) : make_int2(0, 0);
-            for (int i = range.x; ok && i < range.y; i += stride) {
+            for (int i = range.x; ok && i < range.y; ++i) {
                 const int nt = next.y - next.x;
-                if (i + stride < range.y) next = make_int2(items[i + stride].t_lo, items[i + stride].t_hi);
-                if (nt <= 0) continue;
-                if (!qk(g & 1, true, nt == 1)) break;
-                qph ^= 1;
-                for (int t = 0; t < nt; ++t, ++g) {
-                    if (t + 1 < nt && !qk((g + 1) & 1, false, t + 2 == nt)) { ok = false; break; }
+                // S of tile t, then O of tile t - 1: the softmax of one tile has the other product's
+                // time.  One copy of each product's code: a second one for an item's first tile, run
+                // once an item, took 5,500 clocks to fetch and issue instead of 1,200.
+                for (int t = 0; ok && t <= nt; ++t) {
+                    if (t < nt) {
+                        const uint32_t s_col = kSCol + (g & 1) * 64;
+#pragma unroll 1
+                        for (int j = 0; j < kKGroups; ++j) {
+                            if (t == 0 && !wait(&q_full[j], qph)) { ok = false; break; }
+                            if (!wait(&k_full[j], kph)) { ok = false; break; }
+                            const uint32_t jo = uint32_t(j * kKBlks * kBlk) >> 4;
+#pragma unroll
+                            for (int b = 0; b < kKBlks; ++b)
+#pragma unroll
+                                for (int k4 = 0; k4 < 4; ++k4) {
+                                    const uint32_t o = jo + (uint32_t(b * kBlk + k4 * 32) >> 4);
+                                    mma_pair_bf16(tmem + s_col, dq + o, dk + o, idesc_qk, (j | b | k4) != 0 ? 1u : 0u, on);
+                                }
+                            commit_pair(&k_empty[j], on);
+                            if (t + 1 == nt) commit_pair(&q_empty[j], on);
+                        }
+                        if (!ok) break;
+                        kph ^= 1;
+                        commit_pair(&s_full[g & 1], on);
+                        ++g;
+                    }
+                    if (t == 0) {                // (loaded while the tensor cores have work)
+                        if (i + 1 < range.y) next = make_int2(items[i + 1].t_lo, items[i + 1].t_hi);
+                        continue;
+                    }
                     if (!wait(p_full, pph)) { ok = false; break; }
                     pph ^= 1;
-                    if (t == 0) {
+                    if (t == 1) {
                         if (!wait(o_free, ofph ^ 1)) { ok = false; break; }
                         ofph ^= 1;
                     }
@@ -334,14 +336,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
                                 mma_pair_bf16(tmem + kOCol + h * 128, dp + (po + uint32_t(s4 * 2)), dv + (ho + vo[s4] + h * vh),
-                                              idesc_pv, (t | hh | s4) != 0 ? 1u : 0u, on);
+                                              idesc_pv, ((t - 1) | hh | s4) != 0 ? 1u : 0u, on);
                         commit_pair(&v_empty[hh], on);
                     }
                     if (!ok) break;
                     vph ^= 1;
                     commit_pair(pv_done, on);
-                    if (t + 1 == nt) commit_pair(o_full, on);
+                    if (t == nt) commit_pair(o_full, on);
                 }
+                if (nt > 0) qph ^= 1;
             }
             commit_pair(drain, on);
         }
@@ -369,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t g = 0;
         int fph = 0;
         bool ok = true;
-        for (int i = range.x; ok && i < range.y; i += stride) {
+        for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
             const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
@@ -483,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
         int ph = 0;
         bool ok = true;
-        for (int i = range.x; ok && i < range.y; i += stride) {
+        for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
             const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);

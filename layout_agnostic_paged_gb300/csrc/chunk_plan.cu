@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     }
 
     const float G = float(a.pairs);
-    int best_len = INT_MAX;
+    int best_len = INT_MAX, dealt = U;            // the items of a dealt plan
     float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
     const bool may_cut = a.cap_slots > 0 && U > 0;
     // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             if (len < longest && n[kCuts + w] <= a.cap_slots && cost < best) {
                 best = cost;
                 best_len = len;
+                dealt = n[w];
             }
         }
     }
@@ -292,6 +293,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         num_items = tot[0];
         num_splits = tot[2];
     } else {
+        // item i is the (i / pairs)-th of pair i mod pairs, whose items lie next to each other
+        const int per_pair = (dealt + a.pairs - 1) / a.pairs;
         int slot_base = 0;
         for (int r0 = 0; r0 < a.B; r0 += NT) {
             const int r = r0 + tid;
@@ -320,7 +323,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 it.t_lo = t0 + min(tiles, piece * piece_tiles[q]);
                 it.t_hi = t0 + min(tiles, (piece + 1) * piece_tiles[q]);
                 if (k > 1) it.slot = slot0[q] + local;
-                if (num_items + i < a.cap_items) items[num_items + i] = it;
+                const int64_t at = int64_t((num_items + i) % a.pairs) * per_pair + (num_items + i) / a.pairs;
+                if (at < a.cap_items) items[at] = it;
                 if (k > 1 && piece == 0) {
                     ChunkSplit sp = {};
                     sp.tok = it.tok;
@@ -336,15 +340,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             num_splits += tot[2];
             __syncthreads();
         }
-        // offsets that overlap (a bad cu_q) could ask for more than the capacity
-        num_items = int(num_items < a.cap_items ? num_items : a.cap_items);
-        for (int j = tid; j < a.pairs; j += NT) ranges[j] = make_int2(j, num_items);
+        // (offsets that overlap, in a bad cu_q, could ask for more than the capacity)
+        for (int j = tid; j < a.pairs; j += NT) {
+            const int64_t x = int64_t(j) * per_pair, y = x + (num_items - j + a.pairs - 1) / a.pairs;
+            ranges[j] = make_int2(int(x < a.cap_items ? x : a.cap_items), int(y < a.cap_items ? y : a.cap_items));
+        }
     }
     if (tid == 0) {
         head->status = bad ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
         head->num_items = num_items;
         head->num_splits = num_splits;
-        head->stride = is_even ? 1 : a.pairs;
     }
 }
 
@@ -426,7 +431,7 @@ size_t chunk_layout(ChunkArgs& a) {
     const int64_t most = int64_t(kChunkSlotsPerPair) * a.pairs;
     const int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles);
     a.cap_slots = int(slots);
-    a.cap_items = u + slots;
+    a.cap_items = u + slots + a.pairs;   // a dealt plan pads the pairs to equal counts
     a.ranges_off = 256;
     a.items_off = align256(a.ranges_off + sizeof(int2) * size_t(a.pairs));
     a.splits_off = align256(a.items_off + sizeof(ChunkItem) * size_t(a.cap_items));
@@ -437,7 +442,7 @@ size_t chunk_layout(ChunkArgs& a) {
 
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
     // few requests and row tiles: a block whose barriers cost less
-    const bool few = a.B <= 256 && a.cap_items - a.cap_slots <= 256;
+    const bool few = a.B <= 256 && a.cap_items - a.cap_slots - a.pairs <= 256;
     return launch_pdl(chunk_plan_kernel, dim3(1), dim3(few ? 256 : kPlanThreads), 0, stream, a);
 }
 

@@ -84,9 +84,9 @@ struct ChunkArgs {
 
 struct ChunkMaps {
     CUtensorMap q;        // [9][total_q][H][64] box {64, heads, tokens, 1}
-    CUtensorMap k;        // pool as [9][rows][64], box {64, 64, 3} (pages of 64 and more)
+    CUtensorMap k;        // pool as [9][rows][64]: box {64, 64, 3}, or {64, P, 1} for pages below 64
     CUtensorMap v;        // box {64, min(P, 64), 4}
-    CUtensorMap rows[6];  // box {64, 2^i, 1}
+    CUtensorMap rows[3];  // box {64, 4^i, 1}
 };
 
 // Capacities for the shape (cap_items, cap_slots), and the offsets; returns the bytes.

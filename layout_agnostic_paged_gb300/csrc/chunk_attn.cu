@@ -195,12 +195,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (R == kChunkRows) {
                         if (lane == 0) tma_pair_3d(sk + g * kKBlks * kBlk, &maps.k, bar, 0, row, g * kKBlks);
                     } else {
-                        const CUtensorMap* m = &maps.rows[R == 32 ? 5 : 4];
                         for (int j = lane; j < (kKBlks * loads + 31) / 32 * 32; j += 32) {
                             const int b = j / loads, p = j % loads;
                             const int y = __shfl_sync(0xffffffffu, row, p);
                             if (b < kKBlks)
-                                tma_pair_3d(sk + (g * kKBlks + b) * kBlk + p * R * 128, m, bar, 0, y, g * kKBlks + b);
+                                tma_pair_3d(sk + (g * kKBlks + b) * kBlk + p * R * 128, &maps.k, bar, 0, y, g * kKBlks + b);
                         }
                     }
                 }
@@ -212,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // this CTA's 256 value dims (blocks 4 c .. 4 c + 3) of all 128 keys, in two halves.  Rows
         // past the context must be zero, whatever their slots hold (0 * NaN is NaN): whole absent pages
         // are loaded from past the pool, and the page in which the context ends is loaded in
-        // runs of 2^i rows, the valid ones from the pool and the others from past it.
+        // runs of 4^i rows, the valid ones from the pool and the others from past it.
         const uint32_t sv = smem_u32(smem + kVOff);
         const int past = a.past_row;
         int ph = 0;
@@ -247,17 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int n = it.ctx - (t * kChunkKeys + src * R);   // valid rows, 0 < n < R
                         if (lane < 4) {
                             const uint32_t d0 = sv + src * R * 512 + lane * R * 128;
-                            int o = 0;
-                            for (int b = 5; b >= 0; --b)
-                                if (n >> b & 1) {
-                                    tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, y + o, 4 * int(rank) + lane);
-                                    o += 1 << b;
-                                }
-                            for (int b = 0; b < 6; ++b)
-                                if ((R - n) >> b & 1) {
-                                    tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, past, 4 * int(rank) + lane);
-                                    o += 1 << b;
-                                }
+                            for (int o = 0, b = 2; o < R;) {        // runs of 16, 4 and 1 rows
+                                const int end = o < n ? n : R;
+                                while (o + (1 << 2 * b) > end) --b;
+                                tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, o < n ? y + o : past, 4 * int(rank) + lane);
+                                o += 1 << 2 * b;
+                                if (o == n) b = 2;
+                            }
                         }
                         __syncwarp();
                     }

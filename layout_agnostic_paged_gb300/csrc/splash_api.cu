@@ -534,9 +534,10 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     const void* kv = desc->num_pages > 0 ? kv_pool : workspace;
     const uint64_t rows = uint64_t(a.past_row);
     const uint32_t R = uint32_t(a.P < kChunkRows ? a.P : kChunkRows);
-    bool ok = encode_blocks(&maps.q, q, 4, qd, qs, qb) && encode_pool(&maps.k, kv, rows, kChunkRows, kChunkKBlocks) &&
+    bool ok = encode_blocks(&maps.q, q, 4, qd, qs, qb) &&
+              encode_pool(&maps.k, kv, rows, R, R == uint32_t(kChunkRows) ? kChunkKBlocks : 1) &&
               encode_pool(&maps.v, kv, rows, R, 4);
-    for (int i = 0; ok && i < 6; ++i) ok = encode_pool(&maps.rows[i], kv, rows, 1u << i, 1);
+    for (int i = 0; ok && i < 3; ++i) ok = encode_pool(&maps.rows[i], kv, rows, 1u << (2 * i), 1);
     if (!ok) return SPLASH_ERR_CUDA;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (launch_chunk_plan(a, stream) != cudaSuccess || launch_chunk_attn(a, maps, stream) != cudaSuccess ||

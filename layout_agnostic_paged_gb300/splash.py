@@ -7,8 +7,8 @@ missing or the tensors are not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -306,27 +306,45 @@ def splash_kv_migrate(src_pool: torch.Tensor, dst_pool: torch.Tensor, src_ids: t
         raise SplashError(rc, "splash_kv_migrate")
 
 
-def _on(device: torch.device):
-    """Context in which `device` is current (none is entered where it is already)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The functions below serve single decode steps, whose kernels take a few microseconds: they
+# look each attribute up once and ask for the raw stream handle.
+
+def _call(dev: int, stream, where: str, fn, *args):
+    """fn(*args, stream) with device `dev` current; stream None is the device's current stream."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if rc != SPLASH_OK:
+        raise SplashError(rc, where)
 
 
-def _same_device(where: str, *ts):
+def _device_of(where: str, *ts) -> int:
+    """Index of the CUDA device that all the tensors live on."""
+    dev = ts[0].get_device()
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError(f"{where}: tensors must live on a CUDA device")
-        if t.device != ts[0].device:
-            raise ValueError(f"{where}: tensors must live on one device")
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{where}: tensors must live on one CUDA device")
+    return dev
 
 
-def _index_arrays(where: str, B: int, cu_q, block_table, ctx_lens):
-    for t in (cu_q, block_table, ctx_lens):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{where}: cu_q, block_table and ctx_lens must be contiguous int32")
-    if cu_q.shape != (B + 1,) or block_table.dim() != 2 or block_table.shape[0] != B or ctx_lens.shape != (B,):
+def _index_arrays(where: str, cu_q, block_table, ctx_lens) -> tuple[int, int]:
+    """(requests, pages per request) of the three arrays of a ragged batch."""
+    i32 = torch.int32
+    if cu_q.dtype != i32 or block_table.dtype != i32 or ctx_lens.dtype != i32 or not (
+            cu_q.is_contiguous() and block_table.is_contiguous() and ctx_lens.is_contiguous()):
+        raise ValueError(f"{where}: cu_q, block_table and ctx_lens must be contiguous int32")
+    shape, n = block_table.shape, ctx_lens.shape
+    if len(shape) != 2 or n != shape[:1] or cu_q.dim() != 1 or cu_q.numel() != shape[0] + 1:
         raise ValueError(f"{where}: cu_q [B + 1], block_table [B][max_pages] and ctx_lens [B] disagree")
+    return shape[0], shape[1]
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_desc(B: int, H: int, P: int, num_pages: int, max_pages: int, scale: float) -> SplashAttnDesc:
+    """The description of a shape (read-only; the library reads it during the call)."""
+    return SplashAttnDesc(B, H, 576, 512, P, num_pages, max_pages, scale)
 
 
 def make_rope_desc(dims: int, base: float = 10000.0, interleaved: bool = True, scaling: str = "none",
@@ -345,19 +363,19 @@ def splash_rope(x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor, rop
     """out [T][H][d] <- x [T][H][d] rotated by positions int32 [T] (d = rope.dims).  Both are
     views with dense head rows and any token and head strides, e.g. q[..., 512:]; out may
     be x, and elements outside the views are not touched."""
-    _same_device("splash_rope", x, positions, out)
-    if x.dtype not in _DTYPES or out.dtype != x.dtype or positions.dtype != torch.int32:
+    dev = _device_of("splash_rope", x, positions, out)
+    dtype, shape = _DTYPES.get(x.dtype), x.shape
+    if dtype is None or out.dtype != x.dtype or positions.dtype != torch.int32:
         raise ValueError("splash_rope: x and out must share bfloat16, float16 or float32; positions int32")
-    if x.dim() != 3 or x.shape != out.shape or x.shape[2] != rope.dims or positions.shape != (x.shape[0],):
+    if len(shape) != 3 or out.shape != shape or shape[2] != rope.dims or positions.shape != shape[:1]:
         raise ValueError("splash_rope: x and out must be [T][H][rope.dims], positions [T]")
-    if x.numel() and (x.stride(2) != 1 or out.stride(2) != 1 or not positions.is_contiguous()):
+    T, H, _ = shape
+    xt, xh, x1 = x.stride()
+    yt, yh, y1 = out.stride()
+    if (x1 != 1 or y1 != 1 or not positions.is_contiguous()) and T and H:
         raise ValueError("splash_rope: head rows and positions must be dense")
-    with _on(x.device):
-        rc = load_library().splash_rope(
-            ctypes.byref(rope), _DTYPES[x.dtype], x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(),
-            out.stride(0), out.stride(1), positions.data_ptr(), x.shape[0], x.shape[1], _stream(stream))
-    if rc != SPLASH_OK:
-        raise SplashError(rc, "splash_rope")
+    _call(dev, stream, "splash_rope", (_lib or load_library()).splash_rope, rope, dtype, x.data_ptr(), xt, xh,
+          out.data_ptr(), yt, yh, positions.data_ptr(), T, H)
 
 
 def splash_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, cu_q: torch.Tensor,
@@ -366,69 +384,75 @@ def splash_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, cu_q: torch.Ten
     """Writes new tokens (latent [N][512] and k_rope [N][64], bf16 with dense rows) to their slots
     of kv_pool: bf16 [num_pages][P][576], or uint8 [num_pages][P][656] for MXFP8.  cu_q, block_table and
     ctx_lens (the new tokens included) say where; rope rotates k_rope by the tokens' positions."""
-    _same_device("splash_kv_append", latent, k_rope, cu_q, block_table, ctx_lens, kv_pool)
-    N, B = latent.shape[0], ctx_lens.shape[0]
+    where = "splash_kv_append"
+    dev = _device_of(where, latent, k_rope, cu_q, block_table, ctx_lens, kv_pool)
     if latent.dtype != torch.bfloat16 or k_rope.dtype != torch.bfloat16:
         raise ValueError("splash_kv_append: latent and k_rope must be bfloat16")
-    if latent.shape != (N, 512) or k_rope.shape != (N, 64) or (N and (latent.stride(1) != 1 or k_rope.stride(1) != 1)):
-        raise ValueError("splash_kv_append: latent [N][512] and k_rope [N][64] with dense rows")
+    lat, kr = latent.shape, k_rope.shape
+    if len(lat) != 2 or lat[1] != 512 or kr != (lat[0], 64):
+        raise ValueError("splash_kv_append: latent [N][512] and k_rope [N][64]")
+    N = lat[0]
+    lt, l1 = latent.stride()
+    kt, k1 = k_rope.stride()
+    if N and (l1 != 1 or k1 != 1):
+        raise ValueError("splash_kv_append: latent and k_rope must have dense rows")
     if kv_pool.dtype == torch.bfloat16:
         fmt, width = SPLASH_KV_BF16, 576
     elif kv_pool.dtype == torch.uint8:
         fmt, width = SPLASH_KV_MXFP8, MXFP8_ROW_BYTES
     else:
         raise ValueError("splash_kv_append: kv_pool must be bfloat16 or uint8 (MXFP8)")
-    if kv_pool.dim() != 3 or kv_pool.shape[2] != width or not kv_pool.is_contiguous():
+    pool = kv_pool.shape
+    if len(pool) != 3 or pool[2] != width or not kv_pool.is_contiguous():
         raise ValueError(f"splash_kv_append: kv_pool must be contiguous [num_pages][P][{width}]")
-    _index_arrays("splash_kv_append", B, cu_q, block_table, ctx_lens)
-    desc = SplashAttnDesc(B, 1, 576, 512, kv_pool.shape[1], kv_pool.shape[0], block_table.shape[1], 1.0)
-    with _on(kv_pool.device):
-        rc = load_library().splash_kv_append(
-            ctypes.byref(desc), ctypes.byref(rope) if rope is not None else None, fmt, latent.data_ptr(),
-            latent.stride(0), k_rope.data_ptr(), k_rope.stride(0), cu_q.data_ptr(), N, block_table.data_ptr(),
-            ctx_lens.data_ptr(), kv_pool.data_ptr(), _stream(stream))
-    if rc != SPLASH_OK:
-        raise SplashError(rc, "splash_kv_append")
+    B, pages = _index_arrays(where, cu_q, block_table, ctx_lens)
+    _call(dev, stream, where, (_lib or load_library()).splash_kv_append,
+          _shape_desc(B, 1, pool[1], pool[0], pages, 1.0), rope, fmt, latent.data_ptr(), lt, k_rope.data_ptr(), kt,
+          cu_q.data_ptr(), N, block_table.data_ptr(), ctx_lens.data_ptr(), kv_pool.data_ptr())
 
 
 def splash_kv_unpack(src_pool: torch.Tensor, dst_pool: torch.Tensor, src_ids: torch.Tensor,
                      dst_ids: torch.Tensor, stream=None) -> None:
     """bf16 dst_pool[dst_ids[i]] <- the values of MXFP8 src_pool[src_ids[i]] (uint8 [num_pages][P][656])."""
-    _same_device("splash_kv_unpack", src_pool, dst_pool, src_ids, dst_ids)
-    _check_cuda(src_pool, dst_pool, src_ids, dst_ids)
+    where = "splash_kv_unpack"
+    dev = _device_of(where, src_pool, dst_pool, src_ids, dst_ids)
     if src_ids.dtype != torch.int32 or dst_ids.dtype != torch.int32 or src_ids.shape != dst_ids.shape:
         raise ValueError("splash_kv_unpack: ids must be int32 of equal length")
-    if (src_pool.dtype != torch.uint8 or dst_pool.dtype != torch.bfloat16 or src_pool.dim() != 3
-            or dst_pool.dim() != 3 or src_pool.shape[2] != MXFP8_ROW_BYTES or dst_pool.shape[2] != 576
-            or src_pool.shape[1] != dst_pool.shape[1]):
+    s, d = src_pool.shape, dst_pool.shape
+    if (src_pool.dtype != torch.uint8 or dst_pool.dtype != torch.bfloat16 or len(s) != 3 or len(d) != 3
+            or s[2] != MXFP8_ROW_BYTES or d[2] != 576 or s[1] != d[1]):
         raise ValueError("splash_kv_unpack: src uint8 [num_pages][P][656], dst bfloat16 [num_pages][P][576]")
-    with _on(dst_pool.device):
-        rc = load_library().splash_kv_unpack(
-            src_pool.data_ptr(), dst_pool.data_ptr(), src_pool.shape[1], src_ids.data_ptr(), dst_ids.data_ptr(),
-            src_ids.numel(), src_pool.shape[0], dst_pool.shape[0], _stream(stream))
-    if rc != SPLASH_OK:
-        raise SplashError(rc, "splash_kv_unpack")
+    if not (src_pool.is_contiguous() and dst_pool.is_contiguous() and src_ids.is_contiguous() and dst_ids.is_contiguous()):
+        raise ValueError("splash_kv_unpack: tensors must be contiguous")
+    if not d[1]:
+        return
+    _call(dev, stream, where, (_lib or load_library()).splash_kv_unpack, src_pool.data_ptr(), dst_pool.data_ptr(),
+          s[1], src_ids.data_ptr(), dst_ids.data_ptr(), src_ids.numel(), s[0], d[0])
 
 
-def _chunk_desc(q, kv_pool, block_table, scale) -> SplashAttnDesc:
-    if q.dim() != 3 or kv_pool.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("splash_chunk_attn: q [N][H][576], kv_pool [num_pages][P][576], block_table [B][max_pages]")
-    desc = make_desc(q, kv_pool, block_table, scale)
-    desc.num_reqs = block_table.shape[0]
-    return desc
+def _chunk_desc(where: str, q, kv_pool, B: int, pages: int, scale) -> SplashAttnDesc:
+    shape, pool = q.shape, kv_pool.shape
+    if q.dtype != torch.bfloat16 or kv_pool.dtype != torch.bfloat16:
+        raise ValueError(f"{where}: q and kv_pool must be bfloat16")
+    if len(shape) != 3 or len(pool) != 3 or shape[2] != 576 or pool[2] != 576:
+        raise ValueError(f"{where}: q [N][H][576] and kv_pool [num_pages][P][576]")
+    return _shape_desc(B, shape[1], pool[1], pool[0], pages, float(scale))
 
 
 def chunk_workspace(q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor, scale: float,
                     head_lo: int = 0, head_hi: int | None = None) -> torch.Tensor:
     """Allocates (with torch, on q's device) a workspace for splash_chunk_attn on q's rows; it serves
     every later call with no more new tokens, requests and pages per request."""
-    desc = _chunk_desc(q, kv_pool, block_table, scale)
+    where = "splash_chunk_workspace_size"
+    dev = _device_of(where, q, kv_pool, block_table)
+    if block_table.dim() != 2:
+        raise ValueError(f"{where}: block_table must be [B][max_pages]")
+    desc = _chunk_desc(where, q, kv_pool, *block_table.shape, scale)
     head_hi = q.shape[1] if head_hi is None else head_hi
-    with _on(q.device):
-        n = int(load_library().splash_chunk_workspace_size(ctypes.byref(desc), q.shape[0], int(head_lo),
-                                                           int(head_hi)))
+    with torch.cuda.device(dev):
+        n = int(load_library().splash_chunk_workspace_size(desc, q.shape[0], int(head_lo), int(head_hi)))
     if n == 0:
-        raise SplashError(SPLASH_ERR_UNSUPPORTED, "splash_chunk_workspace_size")
+        raise SplashError(SPLASH_ERR_UNSUPPORTED, where)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
@@ -438,26 +462,23 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
                       stream=None) -> None:
     """Causal attention of new tokens q [N][H][576] over the paged cache that holds them (see
     splash.h); writes heads [head_lo, head_hi) of out [N][H][512] (bf16 or fp32) and lse [N][H]."""
-    _same_device("splash_chunk_attn", q, kv_pool, cu_q, block_table, ctx_lens, out, lse, workspace)
-    for t in (q, kv_pool, out, lse, workspace):
-        if not t.is_contiguous():
-            raise ValueError("splash_chunk_attn: tensors must be contiguous")
-    if (q.dtype != torch.bfloat16 or kv_pool.dtype != torch.bfloat16 or lse.dtype != torch.float32
-            or out.dtype not in (torch.bfloat16, torch.float32)):
-        raise ValueError("splash_chunk_attn: dtype mismatch")
-    desc = _chunk_desc(q, kv_pool, block_table, scale)
+    where = "splash_chunk_attn"
+    dev = _device_of(where, q, kv_pool, cu_q, block_table, ctx_lens, out, lse, workspace)
+    B, pages = _index_arrays(where, cu_q, block_table, ctx_lens)
+    desc = _chunk_desc(where, q, kv_pool, B, pages, scale)
     N, H, _ = q.shape
+    out_dtype = _DTYPES.get(out.dtype)
+    if out_dtype not in (SPLASH_BF16, SPLASH_F32) or lse.dtype != torch.float32:
+        raise ValueError("splash_chunk_attn: out must be bfloat16 or float32, lse float32")
     if out.shape != (N, H, 512) or lse.shape != (N, H):
-        raise ValueError("splash_chunk_attn: shape mismatch")
-    _index_arrays("splash_chunk_attn", desc.num_reqs, cu_q, block_table, ctx_lens)
-    with _on(q.device):
-        rc = load_library().splash_chunk_attn(
-            ctypes.byref(desc), q.data_ptr(), kv_pool.data_ptr(), cu_q.data_ptr(), N, block_table.data_ptr(),
-            ctx_lens.data_ptr(), int(head_lo), int(head_hi), int(tok_lo), int(tok_hi), _DTYPES[out.dtype],
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream(stream))
-    if rc != SPLASH_OK:
-        raise SplashError(rc, "splash_chunk_attn")
+        raise ValueError("splash_chunk_attn: out must be [N][H][512], lse [N][H]")
+    if not (q.is_contiguous() and kv_pool.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
+            and workspace.is_contiguous()):
+        raise ValueError("splash_chunk_attn: tensors must be contiguous")
+    _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn, desc, q.data_ptr(), kv_pool.data_ptr(),
+          cu_q.data_ptr(), N, block_table.data_ptr(), ctx_lens.data_ptr(), int(head_lo), int(head_hi), int(tok_lo),
+          int(tok_hi), out_dtype, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
 
 
 def splash_workspace_status(workspace: torch.Tensor, stream=None) -> int:

@@ -29,7 +29,8 @@
  *     that returns an error has enqueued nothing.  Launch failures are reported
  *     as SPLASH_ERR_CUDA (the CUDA error is not cleared from the device).
  *   - Calls are thread-safe; the only library state is a per-device cache of
- *     the SM count and of the dynamic shared memory opt-in.
+ *     the SM count and of the dynamic shared memory opt-in, and each thread's
+ *     frequency table of the last splash_rope_desc it passed (compared by value).
  *   - The calling thread's current CUDA device must be the device that owns
  *     the pointers and the stream.
  */

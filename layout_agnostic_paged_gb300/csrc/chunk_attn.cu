@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "pair.cuh"
+#include "vec32.cuh"
 
 namespace splash {
 namespace {
@@ -70,13 +71,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// One 32-byte store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
 }
 
 // The page id behind a key, or -1 where there is none (past the context, or a bad id).

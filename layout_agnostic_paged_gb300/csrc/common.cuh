@@ -13,7 +13,6 @@ namespace splash {
 
 constexpr int kDqk = 576;        // 512 latent + 64 rope dims of the one shared KV head
 constexpr int kDv = 512;         // values are the latent prefix of the key
-constexpr int kMxRowBytes = 656; // MXFP8 cache row: 512 e4m3, 16 scale bytes, 64 bf16
 constexpr int kTileTokens = 128; // token tile of every decode kernel (the MMA M)
 
 // ---------------------------------------------------------------------------

@@ -63,11 +63,12 @@ cudaError_t launch_kv_migrate(const void* src, void* dst, size_t page_bytes, con
                               const int32_t* dst_ids, int n, int src_np, int dst_np, int sm_count,
                               cudaStream_t stream);
 
+constexpr int kMxRowBytes = 656;   // MXFP8 cache row: 512 e4m3, 16 scale bytes, 64 bf16
 struct RopeTable;
 struct RopeTable32;
-// Rotary positions of T x H head rows (dtype: SPLASH_BF16 / F16 / F32); `vec`: pointers, strides
-// and dims allow 16-byte vectors.
-cudaError_t launch_rope(const RopeTable& table, int dtype, int dims, bool interleaved, bool vec,
+// Rotary positions of T x H head rows (dtype: SPLASH_BF16 / F16 / F32); vec_bytes: the vectors that
+// pointers, strides and dims allow (32, 16, or 0 for single elements).
+cudaError_t launch_rope(const RopeTable& table, int dtype, int dims, bool interleaved, int vec_bytes,
                         const void* x, int64_t xt, int64_t xh, void* y, int64_t yt, int64_t yh,
                         const int32_t* positions, int T, int H, int sms, cudaStream_t stream);
 // New tokens' keys into the cache (table null: the rope dims are not rotated).

@@ -136,8 +136,17 @@ bool encode_pool(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_r
 
 // The frequencies of a rope description as 64-bit fractions of a turn per position.
 // Returns SPLASH_OK or the argument error.
-int rope_turns(const splash_rope_desc* d, uint64_t* turns, float* amplitude) {
+int rope_turns(const splash_rope_desc* d, RopeTable* table) {
+    // a model has one description: each thread keeps the table of the last one it saw (its 64 bytes)
+    thread_local splash_rope_desc last;
+    thread_local RopeTable last_table;
+    thread_local bool valid = false;
     if (!d) return SPLASH_ERR_INVALID_ARG;
+    if (valid && memcmp(d, &last, sizeof(last)) == 0) {
+        *table = last_table;
+        return SPLASH_OK;
+    }
+    valid = false;
     if (d->dims < 2 || d->dims % 2 != 0) return SPLASH_ERR_INVALID_ARG;
     if (d->dims > 2 * kMaxRopePairs) return SPLASH_ERR_UNSUPPORTED;
     if (d->scaling < SPLASH_ROPE_PLAIN || d->scaling > SPLASH_ROPE_YARN) return SPLASH_ERR_INVALID_ARG;
@@ -165,9 +174,12 @@ int rope_turns(const splash_rope_desc* d, uint64_t* turns, float* amplitude) {
             f = f * (1 - g) + f * g / d->factor;
         }
         // f <= 1 radian, so the fraction of a turn is below 1 / 6
-        turns[i] = uint64_t(ldexp(f * 0.15915494309189533577, 64) + 0.5);
+        last_table.turns[i] = uint64_t(ldexp(f * 0.15915494309189533577, 64) + 0.5);
     }
-    *amplitude = float(d->amplitude);
+    last_table.amplitude = float(d->amplitude);
+    last = *d;
+    valid = true;
+    *table = last_table;
     return SPLASH_OK;
 }
 
@@ -372,7 +384,7 @@ int splash_rope(const splash_rope_desc* rope, int dtype, const void* x, int64_t 
                 int64_t x_head_stride, void* y, int64_t y_token_stride, int64_t y_head_stride,
                 const int32_t* positions, int T, int H, splash_stream_t stream) {
     RopeTable table;
-    const int st = rope_turns(rope, table.turns, &table.amplitude);
+    const int st = rope_turns(rope, &table);
     if (st != SPLASH_OK) return st;
     if (dtype != SPLASH_BF16 && dtype != SPLASH_F16 && dtype != SPLASH_F32) return SPLASH_ERR_UNSUPPORTED;
     if (T < 0 || H < 0 || x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0)
@@ -386,16 +398,19 @@ int splash_rope(const splash_rope_desc* rope, int dtype, const void* x, int64_t 
     const int size = dtype == SPLASH_F32 ? 4 : 2;
     if (!aligned(x, size) || !aligned(y, size)) return SPLASH_ERR_INVALID_ARG;
     if (int64_t(T) * H >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
-    // 16-byte vectors where every head row allows them: the interleaved layout takes 8 (fp32: 4)
-    // consecutive dims, the half layout as many of each half
-    const int ve = 16 / size;
-    const bool vec = aligned(x, 16) && aligned(y, 16) && x_token_stride % ve == 0 && x_head_stride % ve == 0 &&
-                     yt % ve == 0 && yh % ve == 0 && (rope->interleaved ? d : d / 2) % ve == 0;
+    // the widest vectors that every head row allows: the interleaved layout takes them from the d dims, the
+    // half layout from each half
+    auto fits = [&](int bytes) {
+        const int ve = bytes / size;
+        return aligned(x, bytes) && aligned(y, bytes) && x_token_stride % ve == 0 && x_head_stride % ve == 0 &&
+               yt % ve == 0 && yh % ve == 0 && (rope->interleaved ? d : d / 2) % ve == 0;
+    };
+    const int vec_bytes = fits(32) ? 32 : (fits(16) ? 16 : 0);
     int dev = 0;
     if (current_device(&dev) != 0) return SPLASH_ERR_CUDA;
     const int sms = sm_count(dev);
     if (sms <= 0) return SPLASH_ERR_CUDA;
-    if (launch_rope(table, dtype, rope->dims, rope->interleaved != 0, vec, x, x_token_stride, x_head_stride, y, yt,
+    if (launch_rope(table, dtype, rope->dims, rope->interleaved != 0, vec_bytes, x, x_token_stride, x_head_stride, y, yt,
                     yh, positions, T, H, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SPLASH_ERR_CUDA;
     return SPLASH_OK;
@@ -411,8 +426,9 @@ int splash_kv_append(const splash_attn_desc* desc, const splash_rope_desc* rope,
     RopeTable wide;
     RopeTable32 table;
     if (rope) {
-        st = rope_turns(rope, wide.turns, &table.amplitude);
+        st = rope_turns(rope, &wide);
         if (st != SPLASH_OK) return st;
+        table.amplitude = wide.amplitude;
         if (rope->dims != kDqk - kDv) return SPLASH_ERR_UNSUPPORTED;
         for (int i = 0; i < 32; ++i) table.turns[i] = wide.turns[i];
     }

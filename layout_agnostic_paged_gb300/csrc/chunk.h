@@ -53,7 +53,8 @@ struct alignas(16) ChunkItem {
     int32_t t_lo, t_hi;   // key tiles
     int32_t slot;         // partial slot, or -1: the result goes to out
     int32_t ctx;          // context length (keys at or past it do not exist)
-    int32_t pad[3];
+    int32_t alone;        // few row tiles share these keys: they are prefetched into L2
+    int32_t pad[2];
 };
 static_assert(sizeof(ChunkItem) == 48, "ChunkItem layout");
 

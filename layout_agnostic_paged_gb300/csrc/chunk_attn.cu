@@ -197,6 +197,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                // keys that no other pair has brought into L2 come from HBM, in more than a tile's time: two
+                // tiles ahead into L2 (drafted tokens of a 16-head shard: 60 -> 57 us; where pairs share the
+                // keys it costs 2%)
+                if (it.alone && t + 2 < it.t_hi && R == kChunkRows && lane < 9 && lane % kKBlks == 0) {
+                    const int id = page_of(a, table, (t + 2) * kChunkKeys + int(rank) * kChunkRows, it.ctx);
+                    if (id >= 0)
+                        tma_prefetch_3d(&maps.k, 0, (id << a.P_log) + (int(rank) * kChunkRows & (a.P - 1)), lane);
+                }
                 ph ^= 1;
             }
         }

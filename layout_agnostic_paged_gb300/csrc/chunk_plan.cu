@@ -30,6 +30,7 @@ constexpr float kItemCost = 3.0f;
 constexpr float kSlotCost = 0.04f;
 constexpr float kMergeCost = 1.5f;
 constexpr int kLeastPiece = 2;            // an even cut leaves no piece of fewer tiles
+constexpr int kAlone = 4;                 // row tiles of a request whose keys come from HBM, not from L2
 // Contexts (bytes) whose row tiles may be swept out of step: what stays in the 129 MB L2.
 constexpr int64_t kSharedBytes = 96ll << 20;
 
@@ -59,19 +60,28 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     return s;
 }
 
-// Sums N values over the block.
+// Over the whole block: sums of N ints and a float, and a maximum.
 template <int N>
-__device__ __forceinline__ void block_sum(int (&v)[N], int (*scratch)[N]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Totals {
+    int v[N];
+    float f;
+    int most;
+};
+template <int N>
+__device__ __forceinline__ void block_totals(Totals<N>& x, Totals<N>* scratch) {
+    const int lane = threadIdx.x & 31;
+    auto warp = [&]() {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, v[k]);
-    if (lane == 0)
+        for (int k = 0; k < N; ++k) x.v[k] = __reduce_add_sync(0xffffffffu, x.v[k]);
+        x.most = __reduce_max_sync(0xffffffffu, x.most);
 #pragma unroll
-        for (int k = 0; k < N; ++k) scratch[warp][k] = v[k];
+        for (int o = 16; o > 0; o >>= 1) x.f += __shfl_xor_sync(0xffffffffu, x.f, o);
+    };
+    warp();
+    if (lane == 0) scratch[threadIdx.x >> 5] = x;
     __syncthreads();
-    const bool in = lane < int(blockDim.x >> 5);
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = __reduce_add_sync(0xffffffffu, in ? scratch[lane][k] : 0);
+    x = lane < int(blockDim.x >> 5) ? scratch[lane] : Totals<N>{};
+    warp();
     __syncthreads();
 }
 
@@ -116,6 +126,7 @@ __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s,
     it.pair_group = pg == 1 ? 0 : tile % pg;
     it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
     it.ctx = s.ctx;
+    it.alone = s.u <= kAlone;
     it.slot = -1;
     *tiles = key_tiles(a, it.seen + min(it.ntok, per_block) - 1);
     return it;
@@ -133,9 +144,12 @@ __device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
-    __shared__ int scratch1[32][1], scratch3[32][3], scratch4[32][4], scratch8[32][2 * kCuts];
-    __shared__ int from[kPlanThreads + 1], slot0[kPlanThreads], split0[kPlanThreads];
+    __shared__ Totals<3> scratch_a[32];
+    __shared__ Totals<2 * kCuts> scratch_b[32];
+    __shared__ int scratch1[32][1], scratch3[32][3];
+    __shared__ int from[kPlanThreads], slot0[kPlanThreads], split0[kPlanThreads];
     __shared__ int pieces[kPlanThreads], piece_tiles[kPlanThreads];
+    __shared__ Span spans[kPlanThreads];
     // the attention's blocks may set themselves up while the plan runs
     pdl_trigger();
     pdl_wait();
@@ -145,119 +159,109 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     ChunkItem* items = reinterpret_cast<ChunkItem*>(a.ws + a.items_off);
     ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(a.ws + a.splits_off);
 
-    // all the row tiles, all their key tiles in 1/16 (a row tile's are about the mean of its request's first
-    // and last), the longest, whether an even cut is allowed
+    // all the row tiles, all their key tiles (a row tile's are about the mean of its request's first and
+    // last), the longest, whether an even cut is allowed
     Span mine = {};
-    float C = 0.f;
-    int sums[4] = {0, 0, 0, 0}, longest = 0;
+    Totals<3> sum = {};
     for (int r = tid; r < a.B; r += NT) {
         const Span s = span_of(a, r);
         if (r == tid) mine = s;
-        sums[0] += s.u;
-        if (s.n > 0) C += 0.5f * float(s.u) * float(s.m + key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())));
-        sums[1] |= s.bad;
-        sums[2] |= s.u > 1 && int64_t(s.ctx) * (kDqk * 2) > kSharedBytes;
-        if (s.u > 0) longest = max(longest, s.m);
+        sum.v[0] += s.u;
+        if (s.n > 0) sum.f += 0.5f * float(s.u) * float(s.m + key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())));
+        sum.v[1] |= s.bad;
+        sum.v[2] |= s.u > 1 && int64_t(s.ctx) * (kDqk * 2) > kSharedBytes;
+        if (s.u > 0) sum.most = max(sum.most, s.m);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) C += __shfl_xor_sync(0xffffffffu, C, o);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if ((tid & 31) == 0) {
-        from[tid >> 5] = longest;
-        slot0[tid >> 5] = __float_as_int(C);
-    }
-    block_sum<4>(sums, scratch4);
-    const int U = sums[0];
-    const bool bad = sums[1] != 0;
-    C = 0.f;
-    for (int i = 0; i < (NT >> 5); ++i) {
-        longest = max(longest, from[i]);
-        C += __int_as_float(slot0[i]);
-    }
+    block_totals(sum, scratch_a);
+    const int U = sum.v[0], longest = sum.most;
+    const float C = sum.f;
 
     const float G = float(a.pairs);
+    const float ideal = (C + kItemCost * float(U)) / G;
     int best_len = INT_MAX, dealt = U;            // the items of a dealt plan
     float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
-    const bool may_cut = a.cap_slots > 0 && U > 0;
+    const bool may_cut = a.cap_slots > 0 && U > 0 && best > 1.02f * ideal + kMergeCost;
     // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
-    const float even = (C + kItemCost * (float(U) + G)) / G + 2.f * G * kSlotCost + kMergeCost;
-    // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles)
+    const float even = ideal + kItemCost + 2.f * G * kSlotCost + kMergeCost;
+    // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles;
+    // positions times pairs stay below 2^31)
     const int64_t tiles_most = int64_t(U) * longest;
-    const bool room = tiles_most < (1 << 30) && U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
-                      (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs) <= a.cap_slots;
-    const bool is_even = may_cut && room && U <= NT && a.pairs <= NT && sums[2] == 0 && even < best;
+    const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
+                      (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs) <= a.cap_slots &&
+                      tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
+    const bool is_even = may_cut && room && U <= NT && a.pairs <= 256 && a.pairs <= NT && sum.v[2] == 0 && even < best;
     if (!is_even && may_cut) {
-        int n[2 * kCuts] = {};
+        Totals<2 * kCuts> n = {};
         for (int r = tid; r < a.B; r += NT) {
             const Span s = r == tid ? mine : span_of(a, r);
 #pragma unroll
             for (int w = 0; w < kCuts; ++w) {
                 const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
                 const int np = max(1, (s.m + len - 1) / len);
-                n[w] += s.u * np;
-                if (np > 1) n[kCuts + w] += s.u * np;
+                n.v[w] += s.u * np;
+                if (np > 1) n.v[kCuts + w] += s.u * np;
             }
         }
-        block_sum<2 * kCuts>(n, scratch8);
+        block_totals(n, scratch_b);
 #pragma unroll
         for (int w = 0; w < kCuts; ++w) {
             const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
-            const float cost = fmaxf(float(len) + kItemCost, ceilf(float(n[w]) / G) * (C / float(n[w]) + kItemCost)) +
-                               float(n[kCuts + w]) * kSlotCost + kMergeCost;
-            if (len < longest && n[kCuts + w] <= a.cap_slots && cost < best) {
+            const float cost = fmaxf(float(len) + kItemCost, ceilf(float(n.v[w]) / G) * (C / float(n.v[w]) + kItemCost)) +
+                               float(n.v[kCuts + w]) * kSlotCost + kMergeCost;
+            if (len < longest && n.v[kCuts + w] <= a.cap_slots && cost < best) {
                 best = cost;
                 best_len = len;
-                dealt = n[w];
+                dealt = n.v[w];
             }
         }
     }
-    __syncthreads();
 
     int num_items = 0, num_splits = 0;
     if (is_even) {
         // one thread per row tile; from[] holds the requests' first row tiles
-        int my_r = 0, my_tile = 0, base = 0;
+        ChunkItem it = {};
+        int tiles = 0, base = 0;
         for (int r0 = 0; r0 < a.B; r0 += NT) {
-            const bool in = r0 + tid < a.B;
-            int v[1] = {!in ? 0 : (r0 == 0 ? mine.u : span_of(a, r0 + tid).u)}, tot[1];
+            const Span s = r0 + tid >= a.B ? Span{} : (r0 == 0 ? mine : span_of(a, r0 + tid));
+            int v[1] = {s.u}, tot[1];
             block_scan<1>(v, tot, scratch1);
             from[tid] = base + v[0];
+            spans[tid] = s;
             __syncthreads();
             if (tid >= base && tid < base + tot[0]) {
                 const int k = last_at_most(from, min(NT, a.B - r0), tid);
-                my_r = r0 + k;
-                my_tile = tid - from[k];
+                it = row_tile(a, spans[k], r0 + k, tid - from[k], &tiles);
             }
             base += tot[0];
             __syncthreads();
         }
         const bool has = tid < U;
-        ChunkItem it = {};
-        int tiles = 0;
-        if (has) it = row_tile(a, span_of(a, my_r), my_r, my_tile, &tiles);
         // positions along the sequence in tiles, an item's own cost included: pair j's run is
         // [j T / P, (j + 1) T / P), and this row tile's tiles lie at [A + own, A + own + tiles)
         const int own = int(kItemCost);
         int v[1] = {has ? tiles + own : 0}, W[1];
         block_scan<1>(v, W, scratch1);
         const int A = v[0];
-        const int64_t T = W[0], P = a.pairs;
+        const uint32_t T = uint32_t(W[0]), P = uint32_t(a.pairs);
         int j0 = 0, j1 = -1;
         if (has) {
-            j0 = int(((int64_t(A) + 1) * P - 1) / T);
-            j1 = int(((int64_t(A) + own + tiles) * P - 1) / T);
+            j0 = int((uint32_t(A + 1) * P - 1) / T);
+            j1 = int((uint32_t(A + own + tiles) * P - 1) / T);
         }
         auto cut = [&](int j) -> int {            // first tile of pair j's piece
             if (j <= j0) return 0;
             if (j > j1) return tiles;
-            const int x = int(int64_t(j) * T / P) - A - own;
+            const int x = int(uint32_t(j) * T / P) - A - own;
             return x < kLeastPiece ? 0 : (tiles - x < kLeastPiece ? tiles : x);
         };
         int np = 0;
         for (int j = j0; j <= j1; ++j) np += cut(j + 1) > cut(j);
         if (has && np == 0) np = 1;               // no key in sight: its rows become zeros
-        int c[3] = {np, np > 1 ? np : 0, np > 1 ? 1 : 0}, tot[3];
-        block_scan<3>(c, tot, scratch3);
+        // items, partials and split row tiles before this one's: at most 1,024 + pairs, 2 pairs, pairs
+        int packed[1] = {np | (np > 1 ? np : 0) << 12 | (np > 1 ? 1 : 0) << 22}, packed_tot[1];
+        block_scan<1>(packed, packed_tot, scratch1);
+        const int c[3] = {packed[0] & 0xfff, packed[0] >> 12 & 0x3ff, packed[0] >> 22};
+        const int tot[3] = {packed_tot[0] & 0xfff, 0, packed_tot[0] >> 22};
         // the items are in the order of their pairs, so a pair's are a range: first in from[], end in slot0[]
         for (int j = tid; j < a.pairs; j += NT) {
             from[j] = INT_MAX;
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             int np = 1;
             if (r < a.B) {
                 s = r0 == 0 ? mine : span_of(a, r);
+                spans[tid] = s;
                 np = best_len == INT_MAX ? 1 : max(1, (s.m + best_len - 1) / best_len);
             }
             const int n = s.u * np;
@@ -318,12 +323,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 const int k = pieces[q], local = i - from[q];
                 const int tile = k == 1 ? local : local / k, piece = k == 1 ? 0 : local % k;
                 int tiles;
-                ChunkItem it = row_tile(a, span_of(a, r0 + q), r0 + q, tile, &tiles);
+                ChunkItem it = row_tile(a, spans[q], r0 + q, tile, &tiles);
                 const int t0 = a.tok_lo / kChunkKeys;
                 it.t_lo = t0 + min(tiles, piece * piece_tiles[q]);
                 it.t_hi = t0 + min(tiles, (piece + 1) * piece_tiles[q]);
                 if (k > 1) it.slot = slot0[q] + local;
-                const int64_t at = int64_t((num_items + i) % a.pairs) * per_pair + (num_items + i) / a.pairs;
+                const uint32_t x = uint32_t(num_items + i), y = x / uint32_t(a.pairs);
+                const int64_t at = int64_t(x - y * a.pairs) * per_pair + y;
                 if (at < a.cap_items) items[at] = it;
                 if (k > 1 && piece == 0) {
                     ChunkSplit sp = {};
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
     }
     if (tid == 0) {
-        head->status = bad ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
+        head->status = sum.v[1] ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
         head->num_items = num_items;
         head->num_splits = num_splits;
     }
@@ -363,39 +369,56 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     const float* plse = reinterpret_cast<const float*>(a.ws + a.plse_off);
     const float* pout = reinterpret_cast<const float*>(a.ws + a.pout_off);
     const int lane = threadIdx.x & 31;
-    const int64_t rows = int64_t(head->num_splits) * (2 * kChunkRows);
     const int64_t warps = int64_t(gridDim.x) * 8;
-    for (int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); w < rows; w += warps) {
-        const ChunkSplit sp = splits[w / (2 * kChunkRows)];
+    int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    // (the first split is read with the count: their round trips overlap; the array has room for it)
+    ChunkSplit sp = splits[w / (2 * kChunkRows) < a.cap_slots ? w / (2 * kChunkRows) : 0];
+    const int64_t rows = int64_t(head->num_splits) * (2 * kChunkRows);
+    for (bool first = true; w < rows; w += warps, first = false) {
+        if (!first) sp = splits[w / (2 * kChunkRows)];
         const int row = int(w % (2 * kChunkRows)), c = row / kChunkRows, i = row % kChunkRows;
         const int qi = i / a.tile.heads + (a.tile.groups == 1 ? c * a.tile.tokens : 0);
         const int hs = (a.tile.groups == 1 ? 0 : (2 * sp.pair_group + c) * a.tile.heads) + i % a.tile.heads;
         if (i >= a.tile.heads * a.tile.tokens || qi >= sp.ntok || hs >= a.Hs) continue;
+        const float* lse = plse + int64_t(sp.slot) * (2 * kChunkRows) + row;
+        // lane s reads piece s; a NaN stays
         float m = -INFINITY;
-        for (int s = 0; s < sp.pieces; ++s) {
-            const float x = plse[(int64_t(sp.slot) + s) * (2 * kChunkRows) + row];
-            m = x != x ? x : fmaxf(m, x);          // a NaN stays
-            if (m != m) break;
+        bool nan = false;
+        for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
+            const float x = s0 + lane < sp.pieces ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+            nan |= __any_sync(0xffffffffu, x != x);
+            m = fmaxf(m, x);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (nan) m = __int_as_float(0x7fc00000);
         float acc[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
         float l = 0.f;
         if (m != -INFINITY)
-            for (int s = 0; s < sp.pieces; ++s) {
-                const int64_t p = (int64_t(sp.slot) + s) * (2 * kChunkRows) + row;
-                const float x = plse[p];
-                if (x == -INFINITY) continue;
-                const float wt = expf(x - m);
-                l += wt;
-                const float4* src = reinterpret_cast<const float4*>(pout + p * kDv) + lane * 2;
+            for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
+                const int n = min(32, sp.pieces - s0);
+                const float x = lane < n ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+                const float mine = x == -INFINITY ? 0.f : expf(x - m);
+                float t = mine;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 v = __ldcs(src + (j >> 1) * 64 + (j & 1));
-                    acc[4 * j] += wt * v.x;
-                    acc[4 * j + 1] += wt * v.y;
-                    acc[4 * j + 2] += wt * v.z;
-                    acc[4 * j + 3] += wt * v.w;
+                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                l += t;
+#pragma unroll 2
+                for (int s = 0; s < n; ++s) {
+                    const float wt = __shfl_sync(0xffffffffu, mine, s);
+                    if (wt == 0.f) continue;      // an empty piece
+                    const float4* src = reinterpret_cast<const float4*>(
+                                            pout + ((int64_t(sp.slot) + s0 + s) * (2 * kChunkRows) + row) * kDv) + lane * 2;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 v = __ldcs(src + (j >> 1) * 64 + (j & 1));
+                        acc[4 * j] += wt * v.x;
+                        acc[4 * j + 1] += wt * v.y;
+                        acc[4 * j + 2] += wt * v.z;
+                        acc[4 * j + 3] += wt * v.w;
+                    }
                 }
             }
         const float inv = l == 0.f ? 0.f : 1.f / l;

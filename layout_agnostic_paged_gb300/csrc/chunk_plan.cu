@@ -150,9 +150,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     __shared__ int from[kPlanThreads], slot0[kPlanThreads], split0[kPlanThreads];
     __shared__ int pieces[kPlanThreads], piece_tiles[kPlanThreads];
     __shared__ Span spans[kPlanThreads];
-    // the attention's blocks may set themselves up while the plan runs
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                                // the attention's blocks set themselves up while the plan runs
     const int tid = threadIdx.x, NT = blockDim.x;
     ChunkHeader* head = reinterpret_cast<ChunkHeader*>(a.ws);
     int2* ranges = reinterpret_cast<int2*>(a.ws + a.ranges_off);

@@ -1,6 +1,7 @@
 """Causal attention of a chunk of new tokens over the paged cache (marked gpu), against the
 64-bit form of tests/serving_reference.py."""
 import math
+import random
 
 import pytest
 import torch
@@ -225,3 +226,58 @@ def test_single_tokens_agree_with_the_decode():
     ws = S.decode_workspace(b.q, b.pool, b.table, b.scale)
     S.splash_decode_attn(b.q, b.pool, b.table, b.ctx_t, 0, 128, 0, -1, do, dl, ws, b.scale)
     assert_chunk(b, do, dl, chunk_reference(b, 0, 128), 0, 128, "decode")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    r = random.Random(seed)
+    heads = r.choice([1, 3, 8, 16, 24, 40, 64, 72, 128])
+    lo = r.randrange(heads)
+    hi = r.randint(lo + 1, heads)
+    B = r.choice([1, 2, 5, 40])
+    q = [r.choice([0, 1, 1, 2, r.randint(1, 200 // B + 1)]) for _ in range(B)]
+    ctx = [n + r.choice([0, 0, 1, r.randint(0, 127), r.randint(0, 6000 // B)]) for n in q]
+    b = Batch(q, ctx, heads, r.choice([16, 32, 64, 128]), 200 + seed, DEV, pad_rows=r.choice([0, 1, 9]),
+              scale=r.choice([1 / math.sqrt(192.0), 0.3]))
+    if b.rows == 0:
+        pytest.skip("no rows drawn")
+    tok_lo = r.choice([0, 0, r.randint(0, 300)])
+    tok_hi = r.choice([-1, -1, tok_lo + r.randint(0, 3000)])
+    check(b, f"seed {seed}", lo, hi, tok_lo, tok_hi, r.choice([torch.bfloat16, torch.float32]))
+
+
+def test_an_infinite_or_nan_slot_past_the_context_never_shows():
+    for bad in (math.nan, math.inf, -math.inf):
+        for ctx in (1, 63, 65, 129, 200):
+            b = Batch([min(ctx, 5)], [ctx], 16, 64, 300 + ctx, DEV)
+            page, off = (ctx - 1) // 64, (ctx - 1) % 64
+            b.pool[b.table[0, page].item(), off + 1:] = bad
+            spare = sorted(set(range(b.pool.shape[0])) - set(b.table.flatten().tolist()))
+            b.pool[spare] = bad
+            check(b, f"{bad} past {ctx}")
+
+
+def test_refusals():
+    b = Batch([2], [70], 16, 64, 400, DEV)
+    ws = S.chunk_workspace(b.q, b.pool, b.table, b.scale)
+    out, lse = torch.empty(2, 16, 512, device=DEV), torch.empty(2, 16, device=DEV)
+
+    def call(q=b.q, pool=b.pool, cu=b.cu, table=b.table, ctx=b.ctx_t, lo=0, hi=16, out=out, lse=lse, ws=ws):
+        S.splash_chunk_attn(q, pool, cu, table, ctx, lo, hi, 0, -1, out, lse, ws, b.scale)
+    call()
+    for kw in (dict(q=b.q.float()), dict(pool=b.pool.float()), dict(out=out.half()), dict(lse=lse.half()),
+               dict(cu=b.cu.long()), dict(table=b.table[0]), dict(ctx=b.ctx_t[:0]), dict(out=out[:1]),
+               dict(q=b.q[..., :575]), dict(pool=b.pool[None]), dict(q=b.q.transpose(0, 1).contiguous().transpose(0, 1)),
+               dict(ctx=b.ctx_t.cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(S.SplashError) as e:
+        call(ws=ws[:256])
+    assert e.value.code == S.SPLASH_ERR_WORKSPACE
+    with pytest.raises(S.SplashError) as e:
+        call(lo=8, hi=17)
+    assert e.value.code == S.SPLASH_ERR_INVALID_ARG
+    wide = torch.empty(2 * 16 * 512 + 8, dtype=torch.bfloat16, device=DEV)[8:].view(2, 16, 512)
+    with pytest.raises(S.SplashError) as e:      # 16-byte aligned only
+        call(out=wide)
+    assert e.value.code == S.SPLASH_ERR_INVALID_ARG

@@ -80,6 +80,31 @@ def test_rope_empty():
         S.splash_rope(x, torch.empty(T, dtype=torch.int32, device=DEV), x, desc)
 
 
+def test_rope_refusals():
+    desc = S.make_rope_desc(64)
+    x = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    pos = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for args in ((x, pos.long(), x), (x, pos[:2], x), (x.double(), pos, x.double()), (x, pos, x.float()),
+                 (x[..., :32], pos, x[..., :32]), (x[0], pos, x[0]), (x.transpose(1, 2), pos, x.transpose(1, 2)),
+                 (x, pos.cpu(), x), (x, pos, x[:, :2])):
+        with pytest.raises(ValueError):
+            S.splash_rope(*args, desc)
+    with pytest.raises(S.SplashError) as e:      # every token writes the same rows
+        S.splash_rope(x, pos, x[:1].expand(3, 4, 64), desc)
+    assert e.value.code == S.SPLASH_ERR_INVALID_ARG
+
+
+def test_rope_many_heads_on_another_stream():
+    x = torch.randn(17, 4099, 64, generator=gen(9)).to(torch.float16).to(DEV)
+    pos = torch.arange(17, dtype=torch.int32, device=DEV)
+    y = torch.empty_like(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    S.splash_rope(x, pos, y, S.make_rope_desc(64, interleaved=False), stream=s)
+    s.synchronize()
+    check_rope(x, y, pos, False, NONE)
+
+
 # ------------------------------------------------------------------ the cache
 
 def lengths(kind):
@@ -220,6 +245,37 @@ def test_unpack_every_code_and_scale(page):
     nan = torch.isnan(want.float())
     assert torch.equal(torch.isnan(got.float()), nan)
     assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
+
+
+def test_cache_refusals():
+    b = batch("mixed", 64, 13, pad=0)
+    n = b.rows
+    lat, kr = torch.zeros(n, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(n, 64, dtype=torch.bfloat16, device=DEV)
+    ok = dict(latent=lat, k_rope=kr, cu_q=b.cu, block_table=b.table, ctx_lens=b.ctx_t, kv_pool=b.pool)
+    for kw in (dict(latent=lat.float()), dict(k_rope=kr[:-1]), dict(latent=lat[:, :511]), dict(cu_q=b.cu[:-1]),
+               dict(cu_q=b.cu.long()), dict(block_table=b.table[0]), dict(kv_pool=b.pool.float()),
+               dict(kv_pool=b.pool[..., :575]), dict(kv_pool=b.pool.view(torch.uint8)), dict(ctx_lens=b.ctx_t.cpu())):
+        with pytest.raises(ValueError):
+            S.splash_kv_append(**{**ok, **kw})
+    with pytest.raises(S.SplashError):
+        S.splash_kv_append(**{**ok, "kv_pool": torch.zeros(3, 48, 576, dtype=torch.bfloat16, device=DEV)})
+    src = torch.zeros(2, 64, 656, dtype=torch.uint8, device=DEV)
+    dst = torch.zeros(2, 64, 576, dtype=torch.bfloat16, device=DEV)
+    ids = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for args in ((src, dst, ids.long(), ids), (src, dst, ids, ids[:0]), (dst, dst, ids, ids), (src, src, ids, ids),
+                 (src, dst[:, :32], ids, ids), (src, dst.cpu(), ids, ids)):
+        with pytest.raises(ValueError):
+            S.splash_kv_unpack(*args)
+
+
+def test_unaligned_unpack_target():
+    src = torch.randint(0, 256, (3, 16, 656), generator=gen(4), dtype=torch.uint8).to(DEV)
+    raw = torch.zeros(3 * 16 * 576 + 8, dtype=torch.bfloat16, device=DEV)
+    ids = torch.arange(3, dtype=torch.int32, device=DEV)
+    a, c = raw[8:].view(3, 16, 576), torch.zeros(3, 16, 576, dtype=torch.bfloat16, device=DEV)   # 16 bytes off
+    S.splash_kv_unpack(src, a, ids, ids)
+    S.splash_kv_unpack(src, c, ids, ids)
+    assert torch.equal(a.view(torch.int16), c.view(torch.int16)) and (raw[:8] == 0).all()
 
 
 def test_pools_past_two_to_the_31_bytes():

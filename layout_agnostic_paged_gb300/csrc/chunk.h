@@ -33,13 +33,15 @@ inline ChunkTiling chunk_tiling(int Hs) {
     return t;
 }
 
-// Workspace: header, the pairs' item ranges (int2), work items, split row tiles, partial
-// lse, partial out (256-byte aligned each).  Pair j works on items [ranges[j].x, ranges[j].y).
+// Workspace: header, a status word per CTA, work items, split row tiles, partial lse,
+// partial out (256-byte aligned each).
+constexpr uint32_t kChunkMagic = 0x4b4e4843u;   // tells the header from a decode plan's (whose second word is a small count)
+constexpr size_t kChunkWordsOff = 256;
 struct ChunkHeader {
-    uint32_t status;      // SPLASH_DEVICE_* bits of the last call
-    int32_t num_items;
+    uint32_t status;      // SPLASH_DEVICE_* bits that the plan set; the CTAs' words hold the others
+    uint32_t magic;
     int32_t num_splits;   // row tiles cut into several items
-    int32_t pad;
+    int32_t words;        // status words
 };
 
 // One pair's work: the rows of one token block and head group pair against key tiles
@@ -70,7 +72,7 @@ struct ChunkArgs {
     void* out;
     float* lse;
     uint8_t* ws;
-    size_t ranges_off, items_off, splits_off, plse_off, pout_off;
+    size_t words_off, items_off, splits_off, plse_off, pout_off;
     int64_t cap_items;
     int cap_slots;
     int B, total_q, H, head_lo, Hs;
@@ -92,7 +94,6 @@ struct ChunkMaps {
 
 // Capacities for the shape (cap_items, cap_slots), and the offsets; returns the bytes.
 size_t chunk_layout(ChunkArgs& a);
-cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream);
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int sms, cudaStream_t stream);
 

@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "chunk.h"
+#include "chunk_plan.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "pair.cuh"
@@ -56,7 +57,7 @@ constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 share
 constexpr int kFinOff = kMaxOff + 8 * kChunkRows * 4;   // an item's final (maximum, sum) of every row
 constexpr int kSmem = kFinOff + kChunkRows * 8;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kThreads = 512;
+constexpr int kThreads = kPlanThreads;
 constexpr int kSoftThreads = 256;
 constexpr int kOCol = 0, kSCol = 256;            // TMEM: O in columns 0-255, S in 2 x 64
 constexpr int kTmemCols = 512;
@@ -84,7 +85,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {                 // no room is left to align it here
-        if (threadIdx.x == 0) atomicOr(&reinterpret_cast<ChunkHeader*>(a.ws)->status, uint32_t(SPLASH_DEVICE_TIMEOUT));
+        if (threadIdx.x == 0) {
+            ChunkHeader* h = reinterpret_cast<ChunkHeader*>(a.ws);
+            reinterpret_cast<uint32_t*>(a.ws + a.words_off)[blockIdx.x] = SPLASH_DEVICE_TIMEOUT;
+            if (blockIdx.x == 0) *h = ChunkHeader{SPLASH_DEVICE_TIMEOUT, kChunkMagic, 0, 2 * a.pairs};
+        }
         return;
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
@@ -132,8 +137,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     pdl_wait();
+    // the plan: this pair's items (its scratch lies in buffers that the copies below fill)
+    static_assert(sizeof(PlanScratch) <= 9 * kBlk, "the plan's scratch fits in K's buffer");
+    int2* planned = reinterpret_cast<int2*>(smem + kMiscOff + 24);
+    {
+        const int2 r = plan_items(a, pair, blockIdx.x == 0, *reinterpret_cast<PlanScratch*>(smem + kKOff));
+        if (threadIdx.x == 0) *planned = r;
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    // Read back from one address, so that the compiler knows it to be the same in all threads: the MMA
+    // issue is only fast in control flow that it can prove uniform (see mma_pair_bf16).
+    const int2 range = *planned;
     const ChunkItem* items = reinterpret_cast<const ChunkItem*>(a.ws + a.items_off);
-    const int2 range = reinterpret_cast<const int2*>(a.ws + a.ranges_off)[pair];
     const int R = min(a.P, kChunkRows);          // rows of one load: pages of 128 come in halves
     const int loads = kChunkRows / R;            // loads for 64 keys
     const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
@@ -504,14 +520,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool none = l == 0.f;
             const float inv = 1.f / l;
             const bool whole = it.slot < 0;
-            const int64_t orow = int64_t(it.tok + qi) * a.H + a.head_lo + hs;
-            const int64_t prow = int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
+            const int64_t to = whole ? int64_t(it.tok + qi) * a.H + a.head_lo + hs
+                                     : int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
             if (live && half == 0)
-                *(whole ? a.lse + orow : plse + prow) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            const bool as_f32 = a.out_f32 || !whole;
-            float* of = (whole ? static_cast<float*>(a.out) + orow * kDv : pout + prow * kDv) + half * 256;
-            __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kDv + half * 256;
-            if (as_f32) {
+                *((whole ? a.lse : plse) + to) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            if (a.out_f32 || !whole) {
+                float* of = (whole ? static_cast<float*>(a.out) : pout) + to * kDv + half * 256;
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     float o[32];
@@ -534,6 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // the second half of the columns is in registers, and O free, before its stores
+                __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + to * kDv + half * 256;
 #pragma unroll 1
                 for (int c0 = 0; c0 < 256; c0 += 128) {
                     uint32_t packed[64];
@@ -567,8 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && *status)
-        atomicOr(&reinterpret_cast<ChunkHeader*>(a.ws)->status, *status);
+    if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(a.ws + a.words_off)[blockIdx.x] = *status;
     cluster_sync();                              // no CTA leaves while the other may still reach its memory
     if (warp == 1) {
         tc_fence_after();

@@ -556,8 +556,7 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     for (int i = 0; ok && i < 3; ++i) ok = encode_pool(&maps.rows[i], kv, rows, 1u << (2 * i), 1);
     if (!ok) return SPLASH_ERR_CUDA;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (launch_chunk_plan(a, stream) != cudaSuccess || launch_chunk_attn(a, maps, stream) != cudaSuccess ||
-        launch_chunk_combine(a, sms, stream) != cudaSuccess)
+    if (launch_chunk_attn(a, maps, stream) != cudaSuccess || launch_chunk_combine(a, sms, stream) != cudaSuccess)
         return SPLASH_ERR_CUDA;
     return SPLASH_OK;
 }
@@ -566,8 +565,19 @@ int splash_workspace_status(const void* workspace, uint32_t* flags, splash_strea
     if (!workspace || !flags) return SPLASH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return SPLASH_ERR_CUDA;
-    if (cudaMemcpy(flags, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return SPLASH_ERR_CUDA;
+    uint32_t head[4];
+    if (cudaMemcpy(head, workspace, sizeof(head), cudaMemcpyDeviceToHost) != cudaSuccess) return SPLASH_ERR_CUDA;
+    uint32_t bits = head[0];
+    if (head[1] == kChunkMagic) {   // a chunk call: its CTAs' words hold the rest
+        constexpr uint32_t kMost = 4096;
+        uint32_t words[kMost];
+        const uint32_t n = head[3] < kMost ? head[3] : kMost;
+        if (cudaMemcpy(words, static_cast<const uint8_t*>(workspace) + kChunkWordsOff, n * sizeof(uint32_t),
+                       cudaMemcpyDeviceToHost) != cudaSuccess)
+            return SPLASH_ERR_CUDA;
+        for (uint32_t i = 0; i < n; ++i) bits |= words[i];
+    }
+    *flags = bits;
     return SPLASH_OK;
 }
 

@@ -153,37 +153,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int R = min(a.P, kChunkRows);          // rows of one load: pages of 128 come in halves
     const int loads = kChunkRows / R;            // loads for 64 keys
     const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
-    const bool one_group = a.tile.groups == 1;
 
-    if (warp == 0) {
+    if (warp == 0 || (warp == 3 && R < kChunkRows)) {
         // -------------------------------------------------------- Q and K loads
+        // One warp issues a copy in some 90 clocks.  Pages of 16 tokens take 36 of 2 KB for a tile's keys, more
+        // than the tile's time, so for pages below 64 a second warp issues every other one.
+        const bool second = warp == 3;
         const uint32_t sq = smem_u32(smem + kQOff), sk = smem_u32(smem + kKOff);
         int ph = 0, qph = 0;
         bool ok = true;
+        // q's box of this CTA: head and token, or the flat row
+        auto q_at = [&](const ChunkItem& x) -> int2 {
+            if (a.tile.flat) return make_int2(x.tok * a.H + x.row0 + int(rank) * kChunkRows, 0);
+            const bool one = a.tile.groups == 1;
+            return make_int2(a.head_lo + (one ? 0 : (2 * x.pair_group + int(rank)) * a.tile.heads),
+                             x.tok + (one ? int(rank) * a.tile.tokens : 0));
+        };
         ChunkItem it = {}, next = {};
         if (range.x < range.y) next = items[range.x];
         for (int i = range.x; ok && i < range.y; ++i) {
             it = next;
             if (i + 1 < range.y) next = items[i + 1];
             if (it.t_lo >= it.t_hi) continue;
-            const int tok = it.tok + (one_group ? int(rank) * a.tile.tokens : 0);
-            const int h0 = a.head_lo + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
-            for (int g = 0; g < kKGroups && ok; ++g) {
+            const int2 at = q_at(it);
+            for (int g = 0; g < kKGroups && ok && !second; ++g) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[g], qph ^ 1, abort_flag, status))) { ok = false; break; }
                 const uint32_t bar = map_to_rank(smem_u32(&q_full[g]), 0);
                 if (rank == 0 && lane == 0)
-                    mbar_arrive_expect_tx(&q_full[g], 2 * kKBlks * a.tile.heads * a.tile.tokens * 128);
+                    mbar_arrive_expect_tx(&q_full[g], 2 * kKBlks * a.tile.box_rows() * 128);
                 __syncwarp();
                 const int b = g * kKBlks + lane;
-                if (lane < kKBlks) tma_pair_4d(sq + b * kBlk, &maps.q, bar, 0, h0, tok, b);
+                if (lane < kKBlks) tma_pair_4d(sq + b * kBlk, &maps.q, bar, 0, at.x, at.y, b);
             }
             if (!ok) break;
             qph ^= 1;
             // Q of the next item comes from HBM while this one is worked on: its buffer is free only
             // when the last scores are done, and the next item's first scores wait for it
-            if (i + 1 < range.y && next.t_lo < next.t_hi && lane < 9)
-                tma_prefetch_4d(&maps.q, 0, a.head_lo + (one_group ? 0 : (2 * next.pair_group + int(rank)) * a.tile.heads),
-                                next.tok + (one_group ? int(rank) * a.tile.tokens : 0), lane);
+            if (i + 1 < range.y && next.t_lo < next.t_hi && lane < 9 && !second) {
+                const int2 to = q_at(next);
+                tma_prefetch_4d(&maps.q, 0, to.x, to.y, lane);
+            }
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 // lane k < loads looks up the page behind keys [64 c + k R, + R) of the tile
@@ -192,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane < loads) {
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
-                    else if (key < it.ctx) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
+                    else if (key < it.ctx && !second) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
                 for (int g = 0; g < kKGroups; ++g) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[g], ph ^ 1, abort_flag, status))) {
@@ -200,15 +209,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t bar = map_to_rank(smem_u32(&k_full[g]), 0);
-                    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kKBlks * kBlk);
+                    if (rank == 0 && lane == 0 && !second) mbar_arrive_expect_tx(&k_full[g], 2 * kKBlks * kBlk);
                     __syncwarp();
                     if (R == kChunkRows) {
                         if (lane == 0) tma_pair_3d(sk + g * kKBlks * kBlk, &maps.k, bar, 0, row, g * kKBlks);
                     } else {
-                        for (int j = lane; j < (kKBlks * loads + 31) / 32 * 32; j += 32) {
-                            const int b = j / loads, p = j % loads;
+                        static_assert(kKBlks * 4 <= 32, "a lane per copy");
+                        {
+                            const int b = lane >> (6 - rlog), p = lane & (loads - 1);
                             const int y = __shfl_sync(0xffffffffu, row, p);
-                            if (b < kKBlks)
+                            if (b < kKBlks && (lane & 1) == int(second))
                                 tma_pair_3d(sk + (g * kKBlks + b) * kBlk + p * R * 128, &maps.k, bar, 0, y, g * kKBlks + b);
                         }
                     }
@@ -380,17 +390,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool odd_scale = a.scale <= 0.f;
         const float sign = a.scale < 0.f ? -1.f : 0.f;
         const float cl = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
-        const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
         uint8_t* prow = smem + kPOff + half * kBlk + row * 128;
         uint32_t g = 0;
         int fph = 0;
         bool ok = true;
         for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
-            const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
-            const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
-            const bool live = qi_in < a.tile.tokens && qi < it.ntok && hs < a.Hs;
-            const int lim = live ? min(it.seen + qi, a.tok_hi) : 0;      // keys [tok_lo, lim)
+            const ChunkRow at = chunk_row(a.tile, a.Hs, it.row0, it.ntok, it.pair_group, int(rank), row);
+            const int lim = at.live ? min(it.seen + at.token, a.tok_hi) : 0;      // keys [tok_lo, lim)
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             float m = -INFINITY, l = 0.f;        // maximum and sum (this thread's keys) of c * x
             for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
@@ -494,16 +501,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row = tl & 63, half = tl >> 6;
         const uint32_t t_o = tmem + (uint32_t((warp & 3) * 32) << 16) + kOCol;
         const uint32_t bo = map_to_rank(smem_u32(o_free), 0);
-        const int qi_in = row / a.tile.heads, hd_in = row % a.tile.heads;
         float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
         float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
         int ph = 0;
         bool ok = true;
         for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
-            const int qi = qi_in + (one_group ? int(rank) * a.tile.tokens : 0);
-            const int hs = hd_in + (one_group ? 0 : (2 * it.pair_group + int(rank)) * a.tile.heads);
-            const bool live = qi_in < a.tile.tokens && qi < it.ntok && hs < a.Hs;
+            const ChunkRow at = chunk_row(a.tile, a.Hs, it.row0, it.ntok, it.pair_group, int(rank), row);
+            const bool live = at.live;
             const bool worked = it.t_hi > it.t_lo;   // no key tile: zeros
             float m = 0.f, l = 0.f;
             if (worked) {
@@ -520,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool none = l == 0.f;
             const float inv = 1.f / l;
             const bool whole = it.slot < 0;
-            const int64_t to = whole ? int64_t(it.tok + qi) * a.H + a.head_lo + hs
+            const int64_t to = whole ? int64_t(it.tok + at.token) * a.H + a.head_lo + at.head
                                      : int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
             if (live && half == 0)
                 *((whole ? a.lse : plse) + to) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;

@@ -29,9 +29,8 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     for (bool first = true; w < rows; w += warps, first = false) {
         if (!first) sp = splits[w / (2 * kChunkRows)];
         const int row = int(w % (2 * kChunkRows)), c = row / kChunkRows, i = row % kChunkRows;
-        const int qi = i / a.tile.heads + (a.tile.groups == 1 ? c * a.tile.tokens : 0);
-        const int hs = (a.tile.groups == 1 ? 0 : (2 * sp.pair_group + c) * a.tile.heads) + i % a.tile.heads;
-        if (i >= a.tile.heads * a.tile.tokens || qi >= sp.ntok || hs >= a.Hs) continue;
+        const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, c, i);
+        if (!at.live) continue;
         const float* lse = plse + int64_t(sp.slot) * (2 * kChunkRows) + row;
         // lane s reads piece s; a NaN stays
         float m = -INFINITY;
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
                 }
             }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t o = int64_t(sp.tok + qi) * a.H + a.head_lo + hs;
+        const int64_t o = int64_t(sp.tok + at.token) * a.H + a.head_lo + at.head;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (F32) {
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
 
 size_t chunk_layout(ChunkArgs& a) {
     const int64_t tiles = (int64_t(a.max_ctx) + kChunkKeys - 1) / kChunkKeys;
-    const int64_t u = (int64_t(a.total_q) / a.tile.pair_tokens() + a.B) * a.tile.pair_groups();
+    const int64_t u = a.tile.row_tiles(a.total_q) + int64_t(a.B) * a.tile.pair_groups();   // each request rounds up
     const int64_t most = int64_t(kChunkSlotsPerPair) * a.pairs;
     const int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles);
     a.cap_slots = int(slots);

@@ -54,8 +54,7 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     s.n = min(max(c1, s.c0), a.total_q) - s.c0;
     s.ctx = min(max(ctx, 0), a.max_ctx);
     s.bad = s.c0 != c0 || c1 != s.c0 + s.n || s.ctx != ctx;
-    const int pt = a.tile.pair_tokens();
-    s.u = (s.n + pt - 1) / pt * a.tile.pair_groups();
+    s.u = int(a.tile.row_tiles(s.n));
     s.m = key_tiles(a, s.ctx);
     return s;
 }
@@ -118,17 +117,25 @@ __device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*
 
 // The row tile `tile` of request r.
 __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s, int r, int tile, int* tiles) {
-    const int pg = a.tile.pair_groups(), per_block = a.tile.pair_tokens();
     ChunkItem it = {};
     it.r = r;
-    it.tok = s.c0 + (pg == 1 ? tile : tile / pg) * per_block;
-    it.ntok = s.c0 + s.n - it.tok;
-    it.pair_group = pg == 1 ? 0 : tile % pg;
-    it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
     it.ctx = s.ctx;
     it.alone = s.u <= kAlone;
     it.slot = -1;
-    *tiles = key_tiles(a, it.seen + min(it.ntok, per_block) - 1);
+    int last;                                     // the tile's last token, from `tok` on
+    if (a.tile.flat) {
+        it.row0 = tile * (2 * kChunkRows);
+        it.tok = s.c0;
+        last = min(s.n - 1, (it.row0 + 2 * kChunkRows - 1) / a.Hs);
+    } else {
+        const int pg = a.tile.pair_groups(), per_block = a.tile.pair_tokens();
+        it.tok = s.c0 + (pg == 1 ? tile : tile / pg) * per_block;
+        it.pair_group = pg == 1 ? 0 : tile % pg;
+        last = min(s.c0 + s.n - it.tok, per_block) - 1;
+    }
+    it.ntok = s.c0 + s.n - it.tok;
+    it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
+    *tiles = key_tiles(a, it.seen + last);
     return it;
 }
 
@@ -305,6 +312,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                     ChunkSplit sp = {};
                     sp.tok = it[e].tok;
                     sp.ntok = it[e].ntok;
+                    sp.row0 = it[e].row0;
                     sp.pair_group = it[e].pair_group;
                     sp.slot = slot;
                     sp.pieces = np[e];
@@ -364,6 +372,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                     ChunkSplit sp = {};
                     sp.tok = it.tok;
                     sp.ntok = it.ntok;
+                    sp.row0 = it.row0;
                     sp.pair_group = it.pair_group;
                     sp.slot = sh.slot0[q] + (i - sh.split0[q]) * sh.pieces[q];
                     sp.pieces = sh.pieces[q];

@@ -491,7 +491,7 @@ size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int h
     a->max_ctx = desc->max_pages_per_req * desc->page_size;
     a->past_row = desc->num_pages > 0 ? desc->num_pages * desc->page_size : 1;
     a->pairs = *sms / 2;
-    a->tile = chunk_tiling(a->Hs);
+    a->tile = chunk_tiling(a->H, a->Hs);
     a->scale = desc->scale;
     const size_t bytes = chunk_layout(*a);
     if (a->cap_items >= (int64_t(1) << 31)) return 0;
@@ -544,8 +544,9 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     a.out_f32 = out_dtype == SPLASH_F32;
     ChunkMaps maps;
     const uint64_t row = uint64_t(kDqk) * 2;
-    const uint64_t qd[3] = {uint64_t(a.H), uint64_t(total_q), 9}, qs[3] = {row, row * a.H, 128};
-    const uint32_t qb[3] = {uint32_t(a.tile.heads), uint32_t(a.tile.tokens), 1};
+    const uint64_t qd[3] = {a.tile.flat ? uint64_t(a.H) * total_q : uint64_t(a.H), a.tile.flat ? uint64_t(1) : uint64_t(total_q), 9};
+    const uint64_t qs[3] = {row, row * a.H, 128};
+    const uint32_t qb[3] = {a.tile.flat ? uint32_t(kChunkRows) : uint32_t(a.tile.heads), a.tile.flat ? 1u : uint32_t(a.tile.tokens), 1};
     // an empty pool still needs a valid map: one row of the workspace, which no copy reads
     const void* kv = desc->num_pages > 0 ? kv_pool : workspace;
     const uint64_t rows = uint64_t(a.past_row);

@@ -11,8 +11,9 @@
 namespace splash {
 namespace {
 
-// One warp per row of a split row tile: out = sum_s w_s part_s / sum_s w_s, as in the
-// split combine of the decode.
+// out = sum_s w_s part_s / sum_s w_s over the pieces of a split row tile, as in the split combine of the
+// decode.  A warp has one row and a quarter of its value dims: one token over a long context is one row
+// tile of up to one piece per CTA pair, whose merge is then spread over 512 warps.
 template <bool F32>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
     pdl_wait();
@@ -21,14 +22,15 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     const float* plse = reinterpret_cast<const float*>(a.ws + a.plse_off);
     const float* pout = reinterpret_cast<const float*>(a.ws + a.pout_off);
     const int lane = threadIdx.x & 31;
+    constexpr int kWarps = 2 * kChunkRows * 4;   // of a split
     const int64_t warps = int64_t(gridDim.x) * 8;
     int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     // (the first split is read with the count: their round trips overlap; the array has room for it)
-    ChunkSplit sp = splits[w / (2 * kChunkRows) < a.cap_slots ? w / (2 * kChunkRows) : 0];
-    const int64_t rows = int64_t(head->num_splits) * (2 * kChunkRows);
-    for (bool first = true; w < rows; w += warps, first = false) {
-        if (!first) sp = splits[w / (2 * kChunkRows)];
-        const int row = int(w % (2 * kChunkRows)), c = row / kChunkRows, i = row % kChunkRows;
+    ChunkSplit sp = splits[w / kWarps < a.cap_slots ? w / kWarps : 0];
+    const int64_t all = int64_t(head->num_splits) * kWarps;
+    for (bool first = true; w < all; w += warps, first = false) {
+        if (!first) sp = splits[w / kWarps];
+        const int row = int(w % kWarps) >> 2, quarter = int(w) & 3, c = row / kChunkRows, i = row % kChunkRows;
         const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, c, i);
         if (!at.live) continue;
         const float* lse = plse + int64_t(sp.slot) * (2 * kChunkRows) + row;
@@ -43,9 +45,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (nan) m = __int_as_float(0x7fc00000);
-        float acc[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
         float l = 0.f;
         if (m != -INFINITY)
             for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
@@ -56,44 +56,31 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
                 l += t;
-#pragma unroll 2
+                const float4* src = reinterpret_cast<const float4*>(
+                                        pout + ((int64_t(sp.slot) + s0) * (2 * kChunkRows) + row) * kDv) + quarter * 32 + lane;
+#pragma unroll 8
                 for (int s = 0; s < n; ++s) {
                     const float wt = __shfl_sync(0xffffffffu, mine, s);
-                    if (wt == 0.f) continue;      // an empty piece
-                    const float4* src = reinterpret_cast<const float4*>(
-                                            pout + ((int64_t(sp.slot) + s0 + s) * (2 * kChunkRows) + row) * kDv) + lane * 2;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 v = __ldcs(src + (j >> 1) * 64 + (j & 1));
-                        acc[4 * j] += wt * v.x;
-                        acc[4 * j + 1] += wt * v.y;
-                        acc[4 * j + 2] += wt * v.z;
-                        acc[4 * j + 3] += wt * v.w;
-                    }
+                    const float4 v = __ldcs(src + int64_t(s) * (2 * kChunkRows * kDv / 4));
+                    acc[0] += wt * v.x;           // (an empty piece holds zeros)
+                    acc[1] += wt * v.y;
+                    acc[2] += wt * v.z;
+                    acc[3] += wt * v.w;
                 }
             }
         const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] *= inv;
         const int64_t o = int64_t(sp.tok + at.token) * a.H + a.head_lo + at.head;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (F32) {
-                float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o * kDv) + j * 64 + lane * 2;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    d[k] = make_float4(acc[8 * j + 4 * k] * inv, acc[8 * j + 4 * k + 1] * inv,
-                                       acc[8 * j + 4 * k + 2] * inv, acc[8 * j + 4 * k + 3] * inv);
-            } else {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[8 * j + 2 * k] * inv, acc[8 * j + 2 * k + 1] * inv);
-                    v[k] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o * kDv)[j * 32 + lane] =
-                    make_uint4(v[0], v[1], v[2], v[3]);
-            }
+        if (F32) {
+            reinterpret_cast<float4*>(static_cast<float*>(a.out) + o * kDv)[quarter * 32 + lane] =
+                make_float4(acc[0], acc[1], acc[2], acc[3]);
+        } else {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0], acc[1]), y = __floats2bfloat162_rn(acc[2], acc[3]);
+            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o * kDv)[quarter * 32 + lane] =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
         }
-        if (lane == 0) a.lse[o] = l == 0.f ? -INFINITY : m + logf(l);
+        if (quarter == 0 && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : m + logf(l);
     }
 }
 
@@ -116,9 +103,9 @@ size_t chunk_layout(ChunkArgs& a) {
 
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int sms, cudaStream_t stream) {
     if (a.cap_slots == 0) return cudaSuccess;
-    // a warp per row: enough blocks for every split of a small call, eight a SM at most
-    const int64_t rows = int64_t(a.cap_slots) * (2 * kChunkRows) / 16;
-    const int blocks = int(rows < int64_t(sms) * 8 ? (rows > 0 ? rows : 1) : int64_t(sms) * 8);
+    // enough blocks for every split of a small call (two slots each at least), eight a SM at most
+    const int64_t want = int64_t(a.cap_slots + 1) / 2 * (2 * kChunkRows * 4 / 8);
+    const int blocks = int(want < int64_t(sms) * 8 ? want : int64_t(sms) * 8);
     if (a.out_f32) return launch_pdl(chunk_combine_kernel<true>, dim3(blocks), dim3(256), 0, stream, a);
     return launch_pdl(chunk_combine_kernel<false>, dim3(blocks), dim3(256), 0, stream, a);
 }

@@ -258,15 +258,19 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
 #pragma unroll
         for (int e = 0; e < kEvenTiles; ++e) v[0] += tid * kEvenTiles + e < U ? tiles[e] + own : 0;
         block_scan<1>(v, W, sh.scan1);
-        const uint32_t T = uint32_t(W[0]), P = uint32_t(a.pairs);
-        // pieces of a row tile at position A: the first tile of pair j's
-        auto cut = [&](int A, int n, int j, int j0, int j1) -> int {
-            if (j <= j0) return 0;
-            if (j > j1) return n;
-            const int x = int(uint32_t(j) * T / P) - A - own;
-            return x < kLeastPiece ? 0 : (n - x < kLeastPiece ? n : x);
+        // Runs are own + kLeastPiece long at least, so that only one boundary can fall on a row tile's own
+        // cost and first tiles, and one on its last: only its first and last piece can come out too
+        // short, and then go to their neighbours.
+        const uint32_t T = uint32_t(W[0]);
+        const uint32_t P = max(1u, min(uint32_t(a.pairs), T / uint32_t(own + kLeastPiece)));
+        int np[kEvenTiles] = {}, j0[kEvenTiles] = {}, j1[kEvenTiles] = {}, A[kEvenTiles] = {};
+        bool no_first[kEvenTiles] = {};
+        auto cut = [&](int e, int j) -> int {     // first tile of pair j's piece
+            if (j <= j0[e]) return 0;
+            if (j > j1[e]) return tiles[e];
+            const int x = int(uint32_t(j) * T / P) - A[e] - own;
+            return x < kLeastPiece ? 0 : (tiles[e] - x < kLeastPiece ? tiles[e] : x);
         };
-        int np[kEvenTiles] = {}, j0[kEvenTiles] = {}, j1[kEvenTiles] = {}, A[kEvenTiles];
         int packed[1] = {0}, packed_tot[1];
         int at = v[0];
 #pragma unroll
@@ -275,9 +279,13 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             if (tid * kEvenTiles + e >= U) continue;
             j0[e] = int((uint32_t(at + 1) * P - 1) / T);
             j1[e] = int((uint32_t(at + own + tiles[e]) * P - 1) / T);
-            for (int j = j0[e]; j <= j1[e]; ++j)
-                np[e] += cut(at, tiles[e], j + 1, j0[e], j1[e]) > cut(at, tiles[e], j, j0[e], j1[e]);
-            if (np[e] == 0) np[e] = 1;            // no key in sight: its rows become zeros
+            np[e] = j1[e] - j0[e] + 1;
+            if (np[e] > 1 && tiles[e] > 0) {
+                no_first[e] = cut(e, j0[e] + 1) == 0;
+                np[e] -= no_first[e] + (cut(e, j1[e]) == tiles[e]);
+            } else {
+                np[e] = 1;                        // (no key in sight: its rows become zeros)
+            }
             // items, partials and split row tiles: at most 1,024 + pairs, 2 pairs, pairs
             packed[0] += np[e] | (np[e] > 1 ? np[e] : 0) << 12 | (np[e] > 1 ? 1 : 0) << 22;
             at += tiles[e] + own;
@@ -292,20 +300,19 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         int item = packed[0] & 0xfff, slot = packed[0] >> 12 & 0x3ff, split = packed[0] >> 22;
 #pragma unroll
         for (int e = 0; e < kEvenTiles; ++e) {
-            int k = 0;
-            for (int j = j0[e]; k < np[e]; ++j) {
-                const int lo = cut(A[e], tiles[e], j, j0[e], j1[e]), hi = cut(A[e], tiles[e], j + 1, j0[e], j1[e]);
-                if (hi <= lo && tiles[e] > 0) continue;
-                if (j == pair) {
+            if (np[e] > 0 && pair >= j0[e] && pair <= j1[e]) {
+                const int lo = cut(e, pair), hi = cut(e, pair + 1);
+                const bool empty = tiles[e] == 0;
+                if (empty ? pair == j0[e] : hi > lo) {
+                    const int k = empty ? 0 : pair - j0[e] - no_first[e];
                     ChunkItem o = it[e];
-                    o.t_lo = t0 + lo;
-                    o.t_hi = t0 + hi;
+                    o.t_lo = t0 + (empty ? 0 : lo);
+                    o.t_hi = t0 + (empty ? 0 : hi);
                     o.slot = np[e] > 1 ? slot + k : -1;
                     items[item + k] = o;
                     atomicMin(&sh.first, item + k);
                     atomicMax(&sh.last, item + k + 1);
                 }
-                ++k;
             }
             if (np[e] > 1) {
                 if (writer) {

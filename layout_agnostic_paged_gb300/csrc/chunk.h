@@ -102,6 +102,7 @@ struct alignas(16) ChunkSplit {
 static_assert(sizeof(ChunkSplit) == 32, "ChunkSplit layout");
 
 struct ChunkArgs {
+    const uint8_t* kv;    // the pool
     const int32_t* cu_q;
     const int32_t* block_table;
     const int32_t* ctx_lens;

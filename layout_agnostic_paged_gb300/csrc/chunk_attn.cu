@@ -223,13 +223,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // keys that no other pair has brought into L2 come from HBM, in more than a tile's time: two
-                // tiles ahead into L2 (drafted tokens of a 16-head shard: 60 -> 57 us; where pairs share the
-                // keys it costs 2%)
-                if (it.alone && t + 2 < it.t_hi && R == kChunkRows && lane < 9 && lane % kKBlks == 0) {
-                    const int id = page_of(a, table, (t + 2) * kChunkKeys + int(rank) * kChunkRows, it.ctx);
+                // Keys that no other pair has brought into L2 come from HBM, in more than a tile's time: the
+                // next tile's into L2, each page's rows as one run (35 requests of 3-9 tokens and 16 heads
+                // over some 10,000 keys: 117 -> 106 us; further ahead is slower, and where pairs share
+                // the keys it costs 2%).
+                const int ahead = key + kChunkKeys;
+                if (it.alone && t + 1 < it.t_hi && lane < loads && !second) {
+                    const int id = page_of(a, table, ahead, it.ctx);
                     if (id >= 0)
-                        tma_prefetch_3d(&maps.k, 0, (id << a.P_log) + (int(rank) * kChunkRows & (a.P - 1)), lane);
+                        prefetch_l2(a.kv + ((int64_t(id) << a.P_log) + (ahead & (a.P - 1))) * (kDqk * 2),
+                                    min(R, it.ctx - ahead) * (kDqk * 2));
                 }
                 ph ^= 1;
             }

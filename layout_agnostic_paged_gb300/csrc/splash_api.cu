@@ -533,6 +533,7 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     if (!work) return SPLASH_OK;
 
     const int64_t most = (int64_t(1) << 31) - 1;
+    a.kv = static_cast<const uint8_t*>(kv_pool);
     a.cu_q = cu_q;
     a.block_table = block_table;
     a.ctx_lens = ctx_lens;

@@ -11,76 +11,87 @@
 namespace splash {
 namespace {
 
-// out = sum_s w_s part_s / sum_s w_s over the pieces of a split row tile, as in the split combine of the
-// decode.  A warp has one row and a quarter of its value dims: one token over a long context is one row
-// tile of up to one piece per CTA pair, whose merge is then spread over 512 warps.
+// One row of a split row tile and Q quarters of its value dims from `quarter` on, by a warp:
+// out = sum_s w_s part_s / sum_s w_s over the pieces, as in the split combine of the decode.
+template <bool F32, int Q>
+__device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& sp, const ChunkRow& at, int row,
+                                          int quarter, int lane) {
+    const float* lse = reinterpret_cast<const float*>(a.ws + a.plse_off) + int64_t(sp.slot) * (2 * kChunkRows) + row;
+    const float4* part = reinterpret_cast<const float4*>(a.ws + a.pout_off) +
+                         (int64_t(sp.slot) * (2 * kChunkRows) + row) * (kDv / 4) + quarter * 32 + lane;
+    // lane s reads piece s; a NaN stays
+    float m = -INFINITY;
+    bool nan = false;
+    for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
+        const float x = s0 + lane < sp.pieces ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+        nan |= __any_sync(0xffffffffu, x != x);
+        m = fmaxf(m, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (nan) m = __int_as_float(0x7fc00000);
+    float acc[Q][4] = {};
+    float l = 0.f;
+    if (m != -INFINITY)
+        for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
+            const int n = min(32, sp.pieces - s0);
+            const float x = lane < n ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+            const float mine = x == -INFINITY ? 0.f : expf(x - m);
+            float t = mine;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            l += t;
+#pragma unroll(8 / Q)
+            for (int s = 0; s < n; ++s) {
+                const float wt = __shfl_sync(0xffffffffu, mine, s);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float4 v = __ldcs(part + int64_t(s0 + s) * (2 * kChunkRows * kDv / 4) + q * 32);
+                    acc[q][0] += wt * v.x;        // (an empty piece holds zeros)
+                    acc[q][1] += wt * v.y;
+                    acc[q][2] += wt * v.z;
+                    acc[q][3] += wt * v.w;
+                }
+            }
+        }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t o = int64_t(sp.tok + at.token) * a.H + a.head_lo + at.head;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const float4 v = make_float4(acc[q][0] * inv, acc[q][1] * inv, acc[q][2] * inv, acc[q][3] * inv);
+        const int64_t to = o * (kDv / 4) + (quarter + q) * 32 + lane;
+        if (F32) {
+            reinterpret_cast<float4*>(a.out)[to] = v;
+        } else {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+            reinterpret_cast<uint2*>(a.out)[to] =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        }
+    }
+    if (quarter == 0 && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// A warp per row, or per row and quarter of its dims when the rows alone would leave three quarters of the
+// warps idle (one token over a long context: one row tile of up to a piece per pair).  Its time is
+// a chain of loads (count and split, weights, partials), so one pass of the resident warps over the rows
+// is what counts: with quarters always, the 64 splits of drafted tokens take 10.6 us instead of 6.
 template <bool F32>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
     pdl_wait();
     const ChunkHeader* head = reinterpret_cast<const ChunkHeader*>(a.ws);
     const ChunkSplit* splits = reinterpret_cast<const ChunkSplit*>(a.ws + a.splits_off);
-    const float* plse = reinterpret_cast<const float*>(a.ws + a.plse_off);
-    const float* pout = reinterpret_cast<const float*>(a.ws + a.pout_off);
     const int lane = threadIdx.x & 31;
-    constexpr int kWarps = 2 * kChunkRows * 4;   // of a split
-    const int64_t warps = int64_t(gridDim.x) * 8;
-    int64_t w = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    // (the first split is read with the count: their round trips overlap; the array has room for it)
-    ChunkSplit sp = splits[w / kWarps < a.cap_slots ? w / kWarps : 0];
-    const int64_t all = int64_t(head->num_splits) * kWarps;
-    for (bool first = true; w < all; w += warps, first = false) {
-        if (!first) sp = splits[w / kWarps];
-        const int row = int(w % kWarps) >> 2, quarter = int(w) & 3, c = row / kChunkRows, i = row % kChunkRows;
-        const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, c, i);
+    const int64_t warps = int64_t(gridDim.x) * 8, first = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t rows = int64_t(head->num_splits) * (2 * kChunkRows);
+    const int parts = rows * 4 <= warps ? 4 : 1;
+    for (int64_t w = first; w < rows * parts; w += warps) {
+        const int64_t r = parts == 4 ? w >> 2 : w;
+        const ChunkSplit sp = splits[r / (2 * kChunkRows)];
+        const int row = int(r % (2 * kChunkRows));
+        const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, row / kChunkRows, row % kChunkRows);
         if (!at.live) continue;
-        const float* lse = plse + int64_t(sp.slot) * (2 * kChunkRows) + row;
-        // lane s reads piece s; a NaN stays
-        float m = -INFINITY;
-        bool nan = false;
-        for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
-            const float x = s0 + lane < sp.pieces ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
-            nan |= __any_sync(0xffffffffu, x != x);
-            m = fmaxf(m, x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (nan) m = __int_as_float(0x7fc00000);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        float l = 0.f;
-        if (m != -INFINITY)
-            for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
-                const int n = min(32, sp.pieces - s0);
-                const float x = lane < n ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
-                const float mine = x == -INFINITY ? 0.f : expf(x - m);
-                float t = mine;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                l += t;
-                const float4* src = reinterpret_cast<const float4*>(
-                                        pout + ((int64_t(sp.slot) + s0) * (2 * kChunkRows) + row) * kDv) + quarter * 32 + lane;
-#pragma unroll 8
-                for (int s = 0; s < n; ++s) {
-                    const float wt = __shfl_sync(0xffffffffu, mine, s);
-                    const float4 v = __ldcs(src + int64_t(s) * (2 * kChunkRows * kDv / 4));
-                    acc[0] += wt * v.x;           // (an empty piece holds zeros)
-                    acc[1] += wt * v.y;
-                    acc[2] += wt * v.z;
-                    acc[3] += wt * v.w;
-                }
-            }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] *= inv;
-        const int64_t o = int64_t(sp.tok + at.token) * a.H + a.head_lo + at.head;
-        if (F32) {
-            reinterpret_cast<float4*>(static_cast<float*>(a.out) + o * kDv)[quarter * 32 + lane] =
-                make_float4(acc[0], acc[1], acc[2], acc[3]);
-        } else {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0], acc[1]), y = __floats2bfloat162_rn(acc[2], acc[3]);
-            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o * kDv)[quarter * 32 + lane] =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-        }
-        if (quarter == 0 && lane == 0) a.lse[o] = l == 0.f ? -INFINITY : m + logf(l);
+        if (parts == 4) merge_row<F32, 1>(a, sp, at, row, int(w) & 3, lane);
+        else merge_row<F32, 4>(a, sp, at, row, 0, lane);
     }
 }
 

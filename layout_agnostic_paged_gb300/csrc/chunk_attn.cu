@@ -481,12 +481,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(bp);
             }
-            if (!ok) break;
             if (it.t_hi <= it.t_lo) continue;
             // the rows' sums over the four shares of the keys, and their maxima, to the storing warps
             float* sums = sm_max + (g & 1) * (4 * kChunkRows) + row;   // not the last tile's buffer
             sums[share * kChunkRows] = l;
-            named_barrier_sync(1, kSoftThreads);
+            // (a wait can give up in one warp alone: all of them leave here, or none)
+            if (named_barrier_or(1, kSoftThreads, !ok)) break;
             if (share == 0) {                    // the part 0 warps of lanes 0-63: two whole warps
                 if (!__all_sync(0xffffffffu, mbar_wait(fin_empty, fph ^ 1, abort_flag, status))) ok = false;
                 l = (sums[0] + sums[kChunkRows]) + (sums[2 * kChunkRows] + sums[3 * kChunkRows]);
@@ -590,7 +590,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(a.ws + a.words_off)[blockIdx.x] = *status;
+    if (threadIdx.x == 0) {
+        reinterpret_cast<uint32_t*>(a.ws + a.words_off)[blockIdx.x] = *status;
+        if (*abort_flag)                         // copies that nobody waited for land before the CTA goes
+            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {}
+    }
     cluster_sync();                              // no CTA leaves while the other may still reach its memory
     if (warp == 1) {
         tc_fence_after();

@@ -397,11 +397,11 @@ SPLASH_API size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int 
  * row never depend on another row.  Slots past a context may hold any bits; a token within a
  * context whose latent is not finite can make NaN of every new row of that request, also of
  * those that precede it.
- * A cu_q that descends or leaves [0, total_q] is clamped into order; it, a context length
+ * A cu_q that descends or leaves [0, total_q] (no row is written then), a context length
  * outside [0, max_pages_per_req * P] (clamped) and a needed page id outside [0, num_pages) (its
  * tokens are left out) set SPLASH_DEVICE_BAD_INPUT, read with splash_workspace_status.
- * The result does not depend on how the work is cut over the GPU's SMs by chance: the
- * same call on the same device gives the same bits.
+ * max_pages_per_req * P may be 2^31 - 1024 at most.  The same call on the same device gives the
+ * same bits.
  */
 SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool,
                                  const int32_t* cu_q, int total_q, const int32_t* block_table,
@@ -410,9 +410,9 @@ SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, co
                                  void* workspace, size_t ws_bytes, splash_stream_t stream);
 
 /*
- * Reads the device status word of a decode workspace (SPLASH_DEVICE_* bits set
- * by the most recent splash_decode_attn that used it): synchronises `stream`,
- * then copies 4 bytes to *flags (host pointer).  Returns SPLASH_OK or an error.
+ * Reads the device status of a decode or chunk workspace (SPLASH_DEVICE_* bits set
+ * by the most recent splash_decode_attn or splash_chunk_attn that used it): synchronises
+ * `stream`, then copies the bits to *flags (host pointer).  Returns SPLASH_OK or an error.
  */
 SPLASH_API int splash_workspace_status(const void* workspace, uint32_t* flags, splash_stream_t stream);
 

@@ -39,7 +39,8 @@ struct Span {
     int ctx;
     int u;            // row tiles
     int m;            // key tiles of the last token, the request's most
-    bool bad;
+    bool bad;         // the length or the offsets
+    bool bad_order;   // the offsets
 };
 
 __device__ __forceinline__ int key_tiles(const ChunkArgs& a, int seen) {
@@ -53,7 +54,8 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     s.c0 = min(max(c0, 0), a.total_q);
     s.n = min(max(c1, s.c0), a.total_q) - s.c0;
     s.ctx = min(max(ctx, 0), a.max_ctx);
-    s.bad = s.c0 != c0 || c1 != s.c0 + s.n || s.ctx != ctx;
+    s.bad_order = s.c0 != c0 || c1 != s.c0 + s.n;
+    s.bad = s.bad_order || s.ctx != ctx;
     s.u = int(a.tile.row_tiles(s.n));
     s.m = key_tiles(a, s.ctx);
     return s;
@@ -152,7 +154,7 @@ __device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
 
 // Shared memory of the plan (its buffers are not in use yet).
 struct PlanScratch {
-    Totals<3> totals[32];
+    Totals<4> totals[32];
     Totals<2 * kCuts> cuts[32];
     int scan1[32][1], scan3[32][3];
     int from[kPlanThreads], slot0[kPlanThreads], split0[kPlanThreads];
@@ -170,9 +172,9 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(a.ws + a.splits_off);
 
     // all the row tiles, all their key tiles (a row tile's are about the mean of its request's first and
-    // last), the longest, whether an even cut is allowed
+    // last), the longest, whether an even cut is allowed; requests with bad values, and with bad offsets
     Span mine = {};
-    Totals<3> sum = {};
+    Totals<4> sum = {};
     for (int r = tid; r < a.B; r += NT) {
         const Span s = span_of(a, r);
         if (r == tid) mine = s;
@@ -180,9 +182,17 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         if (s.n > 0) sum.f += 0.5f * float(s.u) * float(s.m + key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())));
         sum.v[1] |= s.bad;
         sum.v[2] |= s.u > 1 && int64_t(s.ctx) * (kDqk * 2) > kSharedBytes;
+        sum.v[3] |= s.bad_order;
         if (s.u > 0) sum.most = max(sum.most, s.m);
     }
     block_totals(sum, sh.totals);
+    // Requests whose rows overlap could ask for more items than there is room for, so offsets out of order
+    // leave the whole call without work.
+    if (sum.v[3]) {
+        if (writer && tid == 0)
+            *reinterpret_cast<ChunkHeader*>(a.ws) = ChunkHeader{SPLASH_DEVICE_BAD_INPUT, kChunkMagic, 0, 2 * a.pairs};
+        return make_int2(0, 0);
+    }
     const int U = sum.v[0], longest = sum.most;
     const float C = sum.f;
 
@@ -369,7 +379,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 it.t_lo = t0 + min(tiles, piece * sh.piece_tiles[q]);
                 it.t_hi = t0 + min(tiles, (piece + 1) * sh.piece_tiles[q]);
                 if (pc > 1) it.slot = sh.slot0[q] + local;
-                if (x0 + k < a.cap_items) items[x0 + k] = it;
+                items[x0 + k] = it;
             }
             if (writer)
                 for (int i = tid; i < tot[2]; i += NT) {
@@ -390,9 +400,8 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             num_splits += tot[2];
             __syncthreads();
         }
-        // (offsets that overlap, in a bad cu_q, could ask for more than the capacity)
         const int64_t y0 = x0 + (base - pair + a.pairs - 1) / a.pairs;
-        range = make_int2(int(x0 < a.cap_items ? x0 : a.cap_items), int(y0 < a.cap_items ? y0 : a.cap_items));
+        range = make_int2(int(x0), int(y0));
     }
     if (writer && tid == 0) {
         ChunkHeader* head = reinterpret_cast<ChunkHeader*>(a.ws);

@@ -471,9 +471,14 @@ int splash_kv_unpack(const void* src_pool, void* dst_pool, int page_size, const 
 
 namespace {
 
+// Positions rounded up to whole tiles, and a tile ahead, stay below 2^31.
+bool chunk_too_long(const splash_attn_desc* d) {
+    return int64_t(d->max_pages_per_req) * d->page_size > (int64_t(1) << 31) - 1024;
+}
+
 // Shape, tiling and workspace layout of a chunk call; returns its workspace bytes, 0 for a bad shape.
 size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi, ChunkArgs* a, int* sms) {
-    if (validate_desc(desc) != SPLASH_OK || total_q < 0) return 0;
+    if (validate_desc(desc) != SPLASH_OK || chunk_too_long(desc) || total_q < 0) return 0;
     if (head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return 0;
     int dev = 0;
     if (current_device(&dev) != 0) return 0;
@@ -515,7 +520,7 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     if (total_q < 0 || head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return SPLASH_ERR_INVALID_ARG;
     if (tok_lo < 0 || (tok_hi >= 0 && tok_hi < tok_lo)) return SPLASH_ERR_INVALID_ARG;
     if (out_dtype != SPLASH_BF16 && out_dtype != SPLASH_F32) return SPLASH_ERR_UNSUPPORTED;
-    if (int64_t(total_q) * desc->num_heads >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
+    if (int64_t(total_q) * desc->num_heads >= (int64_t(1) << 31) || chunk_too_long(desc)) return SPLASH_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, 256)) return SPLASH_ERR_INVALID_ARG;
     const bool work = desc->num_reqs > 0 && total_q > 0;
     if (work) {
@@ -571,9 +576,12 @@ int splash_workspace_status(const void* workspace, uint32_t* flags, splash_strea
     if (cudaMemcpy(head, workspace, sizeof(head), cudaMemcpyDeviceToHost) != cudaSuccess) return SPLASH_ERR_CUDA;
     uint32_t bits = head[0];
     if (head[1] == kChunkMagic) {   // a chunk call: its CTAs' words hold the rest
-        constexpr uint32_t kMost = 4096;
+        int dev = 0;
+        if (current_device(&dev) != 0) return SPLASH_ERR_CUDA;
+        constexpr uint32_t kMost = 1024;
         uint32_t words[kMost];
-        const uint32_t n = head[3] < kMost ? head[3] : kMost;
+        const uint32_t sms = uint32_t(sm_count(dev));            // a word per CTA, a CTA per SM at most
+        const uint32_t n = min(head[3], min(sms, kMost));
         if (cudaMemcpy(words, static_cast<const uint8_t*>(workspace) + kChunkWordsOff, n * sizeof(uint32_t),
                        cudaMemcpyDeviceToHost) != cudaSuccess)
             return SPLASH_ERR_CUDA;

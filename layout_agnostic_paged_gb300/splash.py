@@ -482,7 +482,7 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
 
 
 def splash_workspace_status(workspace: torch.Tensor, stream=None) -> int:
-    """Synchronises the stream and returns the SPLASH_DEVICE_* bits of the last decode call."""
+    """Synchronises the stream and returns the SPLASH_DEVICE_* bits of the workspace's last decode or chunk call."""
     flags = ctypes.c_uint32(0)
     with torch.cuda.device(workspace.device):
         rc = load_library().splash_workspace_status(_ptr(workspace), ctypes.byref(flags),

@@ -152,6 +152,15 @@ def test_bad_lengths_and_offsets_are_flagged():
         assert S.splash_workspace_status(ws) & S.SPLASH_DEVICE_BAD_INPUT, cu
 
 
+@pytest.mark.parametrize("cu", [[0, 9, 5], [0, 2, 50], [-3, 2, 5], [4, 1, 5], [0, 5, 0]])
+def test_offsets_out_of_order_leave_every_row_alone(cu):
+    b = Batch([2, 3], [100, 90], 16, 64, 65, DEV)
+    b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    out, lse, ws = run(b)
+    assert S.splash_workspace_status(ws) == S.SPLASH_DEVICE_BAD_INPUT
+    assert (out == 7).all() and (lse == 7).all()
+
+
 def test_empty_pool_and_empty_calls():
     b = Batch([1, 2], [1, 2], 16, 64, 66, DEV)
     b.pool = b.pool[:0]

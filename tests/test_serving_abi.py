@@ -135,7 +135,8 @@ def test_chunk_rejects_bad_arguments(lib, kw, code):
 def test_chunk_rejects_bad_shapes(lib):
     assert chunk(lib, None) == INVALID
     for kw, code in ((dict(d_qk=512), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED), (dict(num_heads=0), INVALID),
-                     (dict(scale=float("nan")), INVALID), (dict(num_pages=1 << 28), UNSUPPORTED)):
+                     (dict(scale=float("nan")), INVALID), (dict(num_pages=1 << 28), UNSUPPORTED),
+                     (dict(page_size=16, max_pages_per_req=(1 << 27) - 63), UNSUPPORTED)):
         assert chunk(lib, desc(**kw)) == code
         assert lib.splash_chunk_workspace_size(desc(**kw), 6, 0, 1) == 0
     assert lib.splash_chunk_workspace_size(None, 6, 0, 8) == 0

@@ -18,16 +18,25 @@
 // softmax needs no exchange beyond its own CTA.  The hardware splits B between the CTAs: for
 // S each holds 64 of the 128 keys, for O each holds its 256 of the 512 value dims of all
 // 128 keys.  These are different cuts of the cache, so K and V are loaded separately (the V
-// bytes come from L2).  Measured MMA rates at M = 128 in a pair: 64.7 clocks at N = 256 (the
-// full rate), 50.6 at N = 128 (32 at the full rate).
+// bytes come from L2).  Issued in uniform control flow a tile's 52 MMAs take 2,178 clocks, the full
+// rate (2,988 from a branch that one lane takes).
 //
 // Shared memory of each CTA: Q 72 KB, K 72 KB, V 64 KB, P 16 KB.  K and V have one buffer
 // each: a piece of it is loaded again as soon as the MMAs that read it are done, and needed a
 // whole tile later, because S of the next tile is computed before O of this one.
 //
-// Roles (512 threads): warp 0 loads Q and K, warp 2 loads V, the leader's warp 1 issues every
-// MMA, warps 4-11 run the softmax, warps 12-15 store the results.  Storing takes as long as two key
-// tiles (a warp's store covers 32 rows), so it has warps of its own, beside the next item's first tiles.
+// Roles (512 threads): warp 0 loads Q and K (and warp 3 every other copy of K for pages below 64),
+// warp 2 loads V, the leader's warp 1 issues every MMA, warps 4-11 run the softmax, warps 12-15
+// store the results beside the next item's first tiles.
+//
+// Measured.  The last 1,024 tokens of a 16K-token prompt, 128 heads (4.53 TFLOP): 2.6 ms, 1,740 TF/s,
+// 90% of the library's burst rate for matrix products and as much as its sustained one: the SMs run at
+// 1.6 GHz there, held by power.  16 requests of 1-256 tokens over up to 3,840: 1.02 ms
+// (85%).  Four whole prompts of 257-1,024 tokens: 0.26 ms (50%), an item being three tiles long on average
+// and the causal edge half of one; what is left is the chain from an item's last scores over
+// their softmax and O to the next item's first (6,400 clocks for an item of one tile).  64 requests of 4
+// drafted tokens, 16 heads, over 512-4,096 (173 MB): 55 us, 3.1 TB/s: 15 tiles a pair, each held
+// by the latency of its keys, between the start (5 us) and the merge (6 us).
 #include <math.h>
 
 #include "chunk.h"
@@ -51,7 +60,7 @@ constexpr int kPOff = kVOff + 2 * kVHalf;        // [2 halves of the keys][64 ro
 constexpr int kBarOff = kPOff + 2 * kBlk;
 // barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O full / free,
 // row statistics full / empty, drain
-constexpr int kNumBars = 4 * kKGroups + 4 + 2 + 1 + 1 + 2 + 2 + 1;
+constexpr int kNumBars = 4 * kKGroups + 4 + 2 + 1 + 1 + 4 + 2 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 shares of the keys][64]; row sums reuse them
 constexpr int kFinOff = kMaxOff + 8 * kChunkRows * 4;   // an item's final (maximum, sum) of every row
@@ -59,8 +68,15 @@ constexpr int kSmem = kFinOff + kChunkRows * 8;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kThreads = kPlanThreads;
 constexpr int kSoftThreads = 256;
-constexpr int kOCol = 0, kSCol = 256;            // TMEM: O in columns 0-255, S in 2 x 64
+constexpr int kSCol = 384;                       // TMEM: halves of O in columns 0, 128 and 256, S in 2 x 64
 constexpr int kTmemCols = 512;
+
+// O takes 256 columns, and 384 are left beside S: three buffers of half an O (value dims 0-127 and
+// 128-255 of each CTA).  An item's halves are in the buffers `o` and the one after it, the next
+// item's begin two on, so that the next item waits for the results of the first half only.
+__device__ __forceinline__ uint32_t o_second(uint32_t o) { return o == 2 ? 0 : o + 1; }
+__device__ __forceinline__ uint32_t o_next(uint32_t o) { return o == 0 ? 2 : o - 1; }
+
 constexpr float kTau = 8.0f;                     // rescale O when a score beats the maximum by 2^8
 
 __device__ __forceinline__ float ex2(float x) {
@@ -103,8 +119,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* p_full = s_full + 2;               // leader's: the softmax warps of both CTAs
     uint64_t* pv_done = p_full + 1;              // each CTA's
     uint64_t* o_full = pv_done + 1;              // each CTA's: the item's last PV is done
-    uint64_t* o_free = o_full + 1;               // leader's: the storing warps of both CTAs
-    uint64_t* fin_full = o_free + 1;             // each CTA's own softmax and storing warps
+    uint64_t* o_free = o_full + 1;               // leader's, of each buffer: the storing warps of both CTAs
+    uint64_t* fin_full = o_free + 3;             // each CTA's own softmax and storing warps
     uint64_t* fin_empty = fin_full + 1;
     uint64_t* drain = fin_empty + 1;             // each CTA's
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
@@ -121,7 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a warp's arrival counts once: 8 softmax and 4 storing warps a CTA, both CTAs' on P full and O free
         for (int i = 0; i < kNumBars; ++i)
             mbar_init(&bars[i], &bars[i] == p_full                            ? 16
-                                : &bars[i] == o_free                          ? 8
+                                : &bars[i] >= o_free && &bars[i] < o_free + 3 ? 8
                                 : &bars[i] == fin_full                        ? 2
                                 : &bars[i] == fin_empty                       ? 4
                                                                               : 1);
@@ -306,7 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t vo[4];                      // 16-key steps of a V half
             for (int s = 0; s < 4; ++s) vo[s] = uint32_t((s * 16 >> rlog) * (R * 512) + (s * 16 & (R - 1)) * 128) >> 4;
             const uint32_t vh = uint32_t(R) * 256 >> 4;              // two 64-dim blocks on
-            int kph = 0, vph = 0, qph = 0, pph = 0, ofph = 0;
+            int kph = 0, vph = 0, qph = 0, pph = 0;
+            uint32_t ob = 0, used = 0;           // first buffer of the item's O; parity of the buffers' uses
             uint32_t g = 0;                      // tiles so far: S of tile g is in buffer g & 1
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -350,8 +367,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!wait(p_full, pph)) { ok = false; break; }
                     pph ^= 1;
                     if (t == 1) {
-                        if (!wait(o_free, ofph ^ 1)) { ok = false; break; }
-                        ofph ^= 1;
+                        const uint32_t o2 = o_second(ob);
+                        if (!wait(&o_free[ob], (used >> ob & 1) ^ 1)) { ok = false; break; }
+                        if (!wait(&o_free[o2], (used >> o2 & 1) ^ 1)) { ok = false; break; }
+                        used ^= 1u << ob | 1u << o2;
                     }
 #pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
@@ -361,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                mma_pair_bf16(tmem + kOCol + h * 128, dp + (po + uint32_t(s4 * 2)), dv + (ho + vo[s4] + h * vh),
+                                mma_pair_bf16(tmem + (h ? o_second(ob) : ob) * 128, dp + (po + uint32_t(s4 * 2)), dv + (ho + vo[s4] + h * vh),
                                               idesc_pv, ((t - 1) | hh | s4) != 0 ? 1u : 0u, on);
                         commit_pair(&v_empty[hh], on);
                     }
@@ -370,7 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     commit_pair(pv_done, on);
                     if (t == nt) commit_pair(o_full, on);
                 }
-                if (nt > 0) qph ^= 1;
+                if (nt > 0) {
+                    qph ^= 1;
+                    ob = o_next(ob);
+                }
             }
             commit_pair(drain, on);
         }
@@ -394,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float sign = a.scale < 0.f ? -1.f : 0.f;
         const float cl = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         uint8_t* prow = smem + kPOff + half * kBlk + row * 128;
-        uint32_t g = 0;
+        uint32_t g = 0, ob = 0;
         int fph = 0;
         bool ok = true;
         for (int i = range.x; ok && i < range.y; ++i) {
@@ -462,13 +484,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = part * 128; c < part * 128 + 128; c += 16) {
+                    for (int c = 0; c < 128; c += 16) {
                         float o[16];
-                        tmem_ld16(t_lane + kOCol + c, o);
+                        const uint32_t at_o = t_lane + (part ? o_second(ob) : ob) * 128 + c;
+                        tmem_ld16(at_o, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                        tmem_st16(t_lane + kOCol + c, o);
+                        tmem_st16(at_o, o);
                     }
                     tmem_wait_st();
                 }
@@ -495,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(fin_full);
             }
             fph ^= 1;
+            ob = o_next(ob);
             // the sums are read before the next tile's maxima take their place
             if (named_barrier_or(1, kSoftThreads, !ok)) break;
         }
@@ -502,13 +526,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------- results
         const int tl = (warp & 3) * 32 + lane;   // TMEM lane: row tl & 63, value dims [256 (tl >> 6), + 256)
         const int row = tl & 63, half = tl >> 6;
-        const uint32_t t_o = tmem + (uint32_t((warp & 3) * 32) << 16) + kOCol;
+        const uint32_t t_o = tmem + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t bo = map_to_rank(smem_u32(o_free), 0);
         float* plse = reinterpret_cast<float*>(a.ws + a.plse_off);
         float* pout = reinterpret_cast<float*>(a.ws + a.pout_off);
         int ph = 0;
-        bool ok = true;
-        for (int i = range.x; ok && i < range.y; ++i) {
+        uint32_t ob = 0;
+        for (int i = range.x; i < range.y; ++i) {
             const ChunkItem it = items[i];
             const ChunkRow at = chunk_row(a.tile, a.Hs, it.row0, it.ntok, it.pair_group, int(rank), row);
             const bool live = at.live;
@@ -526,63 +550,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const bool none = l == 0.f;
-            const float inv = 1.f / l;
+            const float inv = none ? 0.f : 1.f / l;
             const bool whole = it.slot < 0;
             const int64_t to = whole ? int64_t(it.tok + at.token) * a.H + a.head_lo + at.head
                                      : int64_t(it.slot) * (2 * kChunkRows) + int(rank) * kChunkRows + row;
             if (live && half == 0)
                 *((whole ? a.lse : plse) + to) = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            if (a.out_f32 || !whole) {
-                float* of = (whole ? static_cast<float*>(a.out) : pout) + to * kDv + half * 256;
+            // 16 rows x 64 columns a round, four threads to a row, which trade their columns so that each
+            // stores 32 bytes of a 128-byte line.  (A thread storing its own row, a line per 32
+            // bytes, held O for 5,000 clocks.)
+            const bool f32 = a.out_f32 || !whole;
+            const int mine = live ? int(to) : -1;
+            char* base = reinterpret_cast<char*>(whole ? a.out : static_cast<void*>(pout));
+            const bool no_rows = __any_sync(0xffffffffu, none);
+            const uint32_t alive = __ballot_sync(0xffffffffu, live);
+            auto release = [&](uint32_t buf) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(bo + buf * 8);
+            };
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
+            for (int k = 0; k < 4; ++k) {            // 128 columns of rows [16 rr, + 16) of the warp's 32
+                const int oh = k >> 1, rr = k & 1;
+                const uint32_t buf = oh ? o_second(ob) : ob;
+                if ((alive >> (16 * rr) & 0xffff) == 0) {
+                    if (worked && rr == 1) release(buf);
+                    continue;
+                }
+                const int from = rr * 16 + (lane >> 2);
+                const int to0 = __shfl_sync(0xffffffffu, mine, from), to1 = __shfl_sync(0xffffffffu, mine, from + 8);
+                const float inv0 = __shfl_sync(0xffffffffu, inv, from), inv1 = __shfl_sync(0xffffffffu, inv, from + 8);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
                     float o[32];
                     if (worked) {
-                        tmem_ld32(t_o + c, o);
+                        tmem_ld_rows16(t_o + (uint32_t(rr * 16) << 16) + buf * 128 + c, o);
                         tmem_wait_ld();
+                        if (rr == 1 && c == 64) release(buf);
                     }
+                    if (no_rows) {                   // zeros, whatever O holds
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                    if (worked && c == 224) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_pair(bo);
+                        for (int e = 0; e < 32; ++e) o[e] = (e & 2 ? inv1 : inv0) == 0.f ? 0.f : o[e];
                     }
-                    if (live) {
+                    const int col = half * 256 + oh * 128 + c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) store32(of + c + e, reinterpret_cast<const uint32_t*>(o) + e);
-                    }
-                    __syncwarp();
-                }
-            } else {
-                // the second half of the columns is in registers, and O free, before its stores
-                __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + to * kDv + half * 256;
-#pragma unroll 1
-                for (int c0 = 0; c0 < 256; c0 += 128) {
-                    uint32_t packed[64];
+                    for (int h = 0; h < 2; ++h) {    // rows lane / 4 + 8 h
+                        const int dst = h ? to1 : to0;
+                        const float s = h ? inv1 : inv0;
+                        float x[16];                 // 2 columns of each run of 8
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
-                        if (worked) {
-                            tmem_ld16(t_o + c0 + c * 16, o);
-                            tmem_wait_ld();
+                        for (int e = 0; e < 16; ++e) x[e] = o[4 * (e >> 1) + 2 * h + (e & 1)] * s;
+                        if (f32) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {        // 32 columns each
+                                uint32_t w[4][2];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) w[e >> 1][e & 1] = __float_as_uint(x[8 * g + e]);
+                                quad_trade(w, lane);
+                                if (dst >= 0) store32(base + (int64_t(dst) * kDv + col + g * 32 + 8 * (lane & 3)) * 4, &w[0][0]);
+                            }
+                        } else {
+                            uint32_t w[4][2], v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e >> 1][e & 1] = pack2(x[2 * e], x[2 * e + 1]);
+                            quad_trade(w, lane);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = w[e & 3][e >> 2];
+                            if (dst >= 0) store32(base + (int64_t(dst) * kDv + col + 16 * (lane & 3)) * 2, v);
                         }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            packed[c * 8 + e] = none ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
                     }
-                    if (worked && c0 == 128) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_pair(bo);
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 64; e += 8) store32(ob + c0 + 2 * e, packed + e);
-                    }
-                    __syncwarp();
                 }
             }
+            if (worked) ob = o_next(ob);
         }
     }
 

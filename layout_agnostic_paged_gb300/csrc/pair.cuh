@@ -131,4 +131,40 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 lanes (taddr's lane: 0 or 16 of the warp's 32) x 64 consecutive columns.  A thread gets, of each run of 8
+// columns g, columns 2 (lane % 4) and the next one of rows lane / 4 (v[4 g], v[4 g + 1]) and
+// lane / 4 + 8 (v[4 g + 2], v[4 g + 3]): four threads hold a row's run.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four neighbouring threads trade: thread j gives w[i] to thread i, and gets in w[s] what thread s
+// held for it.
+__device__ __forceinline__ void quad_trade(uint32_t (&w)[4][2], int lane) {
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((i & bit) == 0)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t x = w[i][k], y = w[i + bit][k];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, bit);
+                    w[i][k] = up ? got : x;
+                    w[i + bit][k] = up ? y : got;
+                }
+    }
+}
+
 }  // namespace splash

@@ -183,6 +183,29 @@ def test_same_bits_again_and_workspace_reuse():
         assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def test_requests_that_share_their_first_pages():
+    b = Batch([40, 3, 1], [500, 400, 300], 128, 64, 77, DEV)
+    for r in (1, 2):
+        b.table[r, :3] = b.table[0, :3]
+        b.keys[r][:192] = b.keys[0][:192]
+    check(b, "shared prefix")
+
+
+def test_one_workspace_for_decode_and_chunk_in_turn():
+    b = Batch([1, 1], [900, 2500], 128, 64, 78, DEV)
+    sizes = [S.chunk_workspace(b.q, b.pool, b.table, b.scale), S.decode_workspace(b.q, b.pool, b.table, b.scale)]
+    ws = torch.full((max(x.numel() for x in sizes),), 0xFF, dtype=torch.uint8, device=DEV)
+    ref = chunk_reference(b, 0, 128)
+    out, lse = torch.empty(2, 128, 512, device=DEV), torch.empty(2, 128, device=DEV)
+    for _ in range(2):
+        run(b, ws=ws, out=out, lse=lse)
+        assert S.splash_workspace_status(ws) == 0
+        assert_chunk(b, out, lse, ref, 0, 128, "chunk")
+        S.splash_decode_attn(b.q, b.pool, b.table, b.ctx_t, 0, 128, 0, -1, out, lse, ws, b.scale)
+        assert S.splash_workspace_status(ws) == 0
+        assert_chunk(b, out, lse, ref, 0, 128, "decode")
+
+
 def test_two_calls_at_once_on_two_streams():
     bs = [Batch([50, 1], [600, 3000], 128, 64, 72 + i, DEV) for i in range(2)]
     refs = [chunk_reference(b, 0, 128) for b in bs]

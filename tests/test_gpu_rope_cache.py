@@ -268,6 +268,17 @@ def test_cache_refusals():
             S.splash_kv_unpack(*args)
 
 
+def test_unpack_one_source_page_twice_and_bad_ids():
+    src = torch.randint(0, 256, (4, 16, 656), generator=gen(5), dtype=torch.uint8).to(DEV)
+    dst = torch.full((6, 16, 576), 5.0, dtype=torch.bfloat16, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    S.splash_kv_unpack(src, dst, torch.tensor([2, 2, -1, 4, 1, 0], **i32), torch.tensor([5, 0, 1, 2, 6, -1], **i32))
+    want = torch.from_numpy(R.unpack_rows(src[2])).float().to(torch.bfloat16)
+    for page in (0, 5):
+        assert torch.equal(dst[page].cpu().nan_to_num(nan=1.0), want.nan_to_num(nan=1.0))
+    assert (dst[1:5] == 5).all()
+
+
 def test_unaligned_unpack_target():
     src = torch.randint(0, 256, (3, 16, 656), generator=gen(4), dtype=torch.uint8).to(DEV)
     raw = torch.zeros(3 * 16 * 576 + 8, dtype=torch.bfloat16, device=DEV)

@@ -58,9 +58,9 @@ constexpr int kVOff = kKOff + 9 * kBlk;          // [2 halves of the keys][pages
 constexpr int kVHalf = 4 * kBlk;
 constexpr int kPOff = kVOff + 2 * kVHalf;        // [2 halves of the keys][64 rows][128 B]
 constexpr int kBarOff = kPOff + 2 * kBlk;
-// barriers: K full / empty, V full / empty, Q full / empty, S full, P full, PV done, O full / free,
+// barriers: K full / empty, V full / empty, Q full / empty, S full, P full, O full / free,
 // row statistics full / empty, drain
-constexpr int kNumBars = 4 * kKGroups + 4 + 2 + 1 + 1 + 4 + 2 + 1;
+constexpr int kNumBars = 4 * kKGroups + 4 + 2 + 2 + 4 + 2 + 1;
 constexpr int kMiscOff = kBarOff + kNumBars * 8;
 constexpr int kMaxOff = kMiscOff + 32;           // row maxima [2 tiles][4 shares of the keys][64]; row sums reuse them
 constexpr int kFinOff = kMaxOff + 8 * kChunkRows * 4;   // an item's final (maximum, sum) of every row
@@ -116,9 +116,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* q_full = v_empty + 2;              // leader's
     uint64_t* q_empty = q_full + kKGroups;       // Q in the groups of K
     uint64_t* s_full = q_empty + kKGroups;       // each CTA's
-    uint64_t* p_full = s_full + 2;               // leader's: the softmax warps of both CTAs
-    uint64_t* pv_done = p_full + 1;              // each CTA's
-    uint64_t* o_full = pv_done + 1;              // each CTA's: the item's last PV is done
+    uint64_t* p_full = s_full + 2;               // leader's, of each half of the keys: the softmax warps of both CTAs
+    uint64_t* o_full = p_full + 2;               // each CTA's: the item's last PV is done
     uint64_t* o_free = o_full + 1;               // leader's, of each buffer: the storing warps of both CTAs
     uint64_t* fin_full = o_free + 3;             // each CTA's own softmax and storing warps
     uint64_t* fin_empty = fin_full + 1;
@@ -136,7 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         // a warp's arrival counts once: 8 softmax and 4 storing warps a CTA, both CTAs' on P full and O free
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(&bars[i], &bars[i] == p_full                            ? 16
+            mbar_init(&bars[i], &bars[i] >= p_full && &bars[i] < p_full + 2 ? 16
                                 : &bars[i] >= o_free && &bars[i] < o_free + 3 ? 8
                                 : &bars[i] == fin_full                        ? 2
                                 : &bars[i] == fin_empty                       ? 4
@@ -322,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t vo[4];                      // 16-key steps of a V half
             for (int s = 0; s < 4; ++s) vo[s] = uint32_t((s * 16 >> rlog) * (R * 512) + (s * 16 & (R - 1)) * 128) >> 4;
             const uint32_t vh = uint32_t(R) * 256 >> 4;              // two 64-dim blocks on
-            int kph = 0, vph = 0, qph = 0, pph = 0;
+            int kph = 0, vph = 0, qph = 0;
             uint32_t ob = 0, used = 0;           // first buffer of the item's O; parity of the buffers' uses
             uint32_t g = 0;                      // tiles so far: S of tile g is in buffer g & 1
             bool ok = true;
@@ -364,8 +363,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (i + 1 < range.y) next = make_int2(items[i + 1].t_lo, items[i + 1].t_hi);
                         continue;
                     }
-                    if (!wait(p_full, pph)) { ok = false; break; }
-                    pph ^= 1;
                     if (t == 1) {
                         const uint32_t o2 = o_second(ob);
                         if (!wait(&o_free[ob], (used >> ob & 1) ^ 1)) { ok = false; break; }
@@ -375,6 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
                         if (!wait(&v_full[hh], vph)) { ok = false; break; }
+                        if (!wait(&p_full[hh], vph)) { ok = false; break; }
                         const uint32_t ho = uint32_t(hh * kVHalf) >> 4, po = uint32_t(hh * kBlk) >> 4;
 #pragma unroll
                         for (int s4 = 0; s4 < 4; ++s4)
@@ -386,7 +384,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                     vph ^= 1;
-                    commit_pair(pv_done, on);
                     if (t == nt) commit_pair(o_full, on);
                 }
                 if (nt > 0) {
@@ -465,23 +462,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     m = top;
                     l *= alpha;
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                uint32_t pk[16];
-                float ls[2] = {0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float p0 = ex2(fmaf(x[e], cl, -base)), p1 = ex2(fmaf(x[e + 1], cl, -base));
-                    ls[0] += p0;                 // the sum takes P before its rounding to bf16
-                    ls[1] += p1;
-                    pk[e >> 1] = pack2(p0, p1);
-                }
-                l += ls[0] + ls[1];
-                // P's buffer is free and O is at rest once the previous tile's MMAs are done
-                if (g > 0) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (g - 1) & 1, abort_flag, status)))
-                        ok = false;
-                }
+                // O is at rest once the previous tile's MMAs are done
                 if (t > it.t_lo && __any_sync(0xffffffffu, up)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[1], (g - 1) & 1, abort_flag, status)))
+                        ok = false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 16) {
@@ -495,14 +479,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                 }
+                const float base = m == -INFINITY ? 0.f : m;
+                uint32_t pk[16];
+                float ls[2] = {0.f, 0.f};
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-                    *reinterpret_cast<uint4*>(prow + (((part * 4 + ch) ^ (row & 7)) << 4)) =
-                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(bp);
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2(fmaf(x[e], cl, -base)), p1 = ex2(fmaf(x[e + 1], cl, -base));
+                    ls[0] += p0;                 // the sum takes P before its rounding to bf16
+                    ls[1] += p1;
+                    pk[e >> 1] = pack2(p0, p1);
+                }
+                l += ls[0] + ls[1];
+                // Each half of the keys has its product, which needs its half of P and every warp's O at rest:
+                // a half of P's buffer is free, and its barrier's phase over, when the previous tile's
+                // product of that half is done.
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (g > 0) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[h], (g - 1) & 1, abort_flag, status)))
+                            ok = false;
+                    }
+                    if (half == h) {
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch)
+                            *reinterpret_cast<uint4*>(prow + (((part * 4 + ch) ^ (row & 7)) << 4)) =
+                                make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                        fence_proxy_async_smem();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bp + h * 8);
+                }
             }
             if (it.t_hi <= it.t_lo) continue;
             // the rows' sums over the four shares of the keys, and their maxima, to the storing warps

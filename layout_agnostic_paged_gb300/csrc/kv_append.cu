@@ -5,8 +5,8 @@
 // latents are 16 consecutive ones per lane, so that an MXFP8 group of 32 is a pair of
 // lanes, and the 64 rope dims are one pair per lane.  An append's warp is a chain of two to three
 // dependent loads (the owner of the row, its page, the stores), so many warps with one row each
-// beat fewer with more: 36,600 rows to MXFP8 (66 MB) in 15.4 us (64% of the copy bandwidth; four rows a
-// warp: 24 us); one row of each of 256 requests in 2.2 us.
+// beat fewer with more: 36,600 rows to MXFP8 (66 MB) in 12.4 us (78% of the copy bandwidth; four rows a
+// warp took half as long again); one row of each of 256 requests in 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const __nv_bfloat16* kp = a.k_rope + int64_t(t) * a.rope_stride;
     const int ia = a.interleaved ? 2 * lane : lane, ib = a.interleaved ? 2 * lane + 1 : lane + 32;
     __nv_bfloat16 ra = kp[ia], rb = kp[ib];
+    const uint64_t F = a.rotate ? generic_table(a.table.turns)[lane] : 0;
 
     const Owner o = find_owner(a.cu_q, a.ctx_lens, a.B, t, lane);
     const int pos = o.ctx - (o.c1 - t);
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 
     if (a.rotate) {
         const float2 y = rope_rotate(__bfloat162float(ra), __bfloat162float(rb),
-                                     rope_cos_sin(a.table.turns[lane], pos, a.table.amplitude));
+                                     rope_cos_sin(F, pos, a.table.amplitude));
         ra = __float2bfloat16_rn(y.x);
         rb = __float2bfloat16_rn(y.y);
     }

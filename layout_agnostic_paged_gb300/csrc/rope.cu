@@ -5,8 +5,8 @@
 // run of its heads.  The cos / sin of the token's d / 2 pairs are computed once per block
 // into shared memory, behind the block's first loads, and serve all of its heads.  Threads move
 // 32 bytes at a time, so that a sector is written by one store.  8,191 tokens x 64 heads x 128
-// dims of fp16 (268 MB): 46 us, 86% of the copy bandwidth (16-byte vectors: 62 us); 256 tokens x 128
-// heads x 64 dims inside wider rows (8.4 MB): 2.8 us.
+// dims of fp16 (268 MB): 39.5 us, the copy bandwidth; 256 tokens x 128 heads x 64 dims inside wider
+// rows (8.4 MB): 2.3 us (16-byte vectors: 2.9 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,7 +18,7 @@
 namespace splash {
 namespace {
 
-constexpr int kRopeThreads = 128;   // small blocks: 256 threads take 52 us for the case above, 64 take 51
+constexpr int kRopeThreads = 128;   // (64 and 256 take the same time, within 2%)
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     constexpr int W = INTER && VE == 1 ? 2 : VE;       // elements of one load group
     constexpr int NP = INTER ? W / 2 : VE;             // pairs of a work item
     constexpr int U = kRopeUnroll<T, NP>;
-    __shared__ float2 cs[kMaxRopePairs];
+    // runs of NP pairs, 16 bytes apart: threads at different runs of a head read different banks (without
+    // the gap four of them met in one, and the large case took 46 us)
+    constexpr int kRun = NP >= 4 ? NP + 2 : NP;
+    __shared__ alignas(16) float2 cs[kMaxRopePairs / NP * kRun];
     pdl_wait();
     const int t = blockIdx.x / a.chunks;
     const int h0 = (blockIdx.x % a.chunks) * a.heads_per_block;
@@ -72,6 +75,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int items = nh * per_head;
     const T* x = static_cast<const T*>(a.x) + int64_t(t) * a.xt + int64_t(h0) * a.xh;
     T* y = static_cast<T*>(a.y) + int64_t(t) * a.yt + int64_t(h0) * a.yh;
+    const uint64_t* turns = generic_table(a.table.turns);
     bool ready = false;
     for (int i0 = threadIdx.x; !ready || i0 < items; i0 += kRopeThreads * U) {
         alignas(32) T in[U][2 * NP];                     // the pairs' elements, as loaded
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         if (!ready) {
             const int32_t pos = a.positions[t];
             for (int j = threadIdx.x; j < half; j += kRopeThreads)
-                cs[j] = rope_cos_sin(a.table.turns[j], pos, a.table.amplitude);
+                cs[j / NP * kRun + j % NP] = rope_cos_sin(turns[j], pos, a.table.amplitude);
             __syncthreads();
             ready = true;
         }
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 for (int e = 0; e < NP; ++e) {
                     T& ea = in[u][INTER ? 2 * e : e];
                     T& eb = in[u][INTER ? 2 * e + 1 : NP + e];
-                    const float2 r = rope_rotate(to_f32(ea), to_f32(eb), cs[k * NP + e]);
+                    const float2 r = rope_rotate(to_f32(ea), to_f32(eb), cs[k * kRun + e]);
                     from_f32(ea, r.x);
                     from_f32(eb, r.y);
                 }

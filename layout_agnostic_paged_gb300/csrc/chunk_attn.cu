@@ -29,13 +29,13 @@
 // warp 2 loads V, the leader's warp 1 issues every MMA, warps 4-11 run the softmax, warps 12-15
 // store the results beside the next item's first tiles.
 //
-// Measured.  The last 1,024 tokens of a 16K-token prompt, 128 heads (4.53 TFLOP): 2.6 ms, 1,740 TF/s,
-// 90% of the library's burst rate for matrix products and as much as its sustained one: the SMs run at
-// 1.6 GHz there, held by power.  16 requests of 1-256 tokens over up to 3,840: 1.02 ms
-// (85%).  Four whole prompts of 257-1,024 tokens: 0.26 ms (50%), an item being three tiles long on average
+// Measured.  The last 1,024 tokens of a 16K-token prompt, 128 heads (4.53 TFLOP): 2.52 ms, 1,795 TF/s,
+// 93% of the library's burst rate for matrix products and more than its sustained one: the SMs run at
+// 1.6 GHz there, held by power.  16 requests of 1-256 tokens over up to 3,840: 0.975 ms
+// (89%).  Four whole prompts of 257-1,024 tokens: 0.26 ms (51%), an item being three tiles long on average
 // and the causal edge half of one; what is left is the chain from an item's last scores over
 // their softmax and O to the next item's first (6,400 clocks for an item of one tile).  64 requests of 4
-// drafted tokens, 16 heads, over 512-4,096 (173 MB): 55 us, 3.1 TB/s: 15 tiles a pair, each held
+// drafted tokens, 16 heads, over 512-4,096 (173 MB): 53 us, 3.2 TB/s: 15 tiles a pair, each held
 // by the latency of its keys, between the start (5 us) and the merge (6 us).
 #include <math.h>
 

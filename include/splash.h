@@ -317,7 +317,7 @@ typedef struct {
  *   positions   int32 [T]; negative positions turn the other way (amplitude 1: they undo
  *               the rotation)
  * Elements of y outside the d dims are not written.  Any alignment of the elements' own
- * size is taken; 16-byte aligned pointers and strides run fastest.
+ * size is taken; 32-byte aligned pointers and strides run fastest.
  */
 SPLASH_API int splash_rope(const splash_rope_desc* rope, int dtype, const void* x,
                            int64_t x_token_stride, int64_t x_head_stride, void* y,

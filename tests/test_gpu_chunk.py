@@ -115,6 +115,17 @@ def test_growing_scores_rescale():
     check(b, "rescale", dtype=torch.float32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_growing_scores_in_every_one_of_many_items(dtype):
+    n = 320                               # several items for every pair of SMs, of three to five key tiles
+    b = Batch([1] * n, [300 + (i * 29) % 260 for i in range(n)], 128, 64, 79, DEV)
+    for r in range(n):
+        for j, t in enumerate(range(135 + r % 7, b.ctx[r], 130)):
+            b.keys[r][t] = (b.q[r, (r + 37 * j) % 128].float().cpu() * (0.5 + 0.25 * j)).to(torch.bfloat16)
+            b.pool[b.table[r, t // 64].item(), t % 64] = b.keys[r][t].to(DEV)
+    check(b, "rescale in every item", dtype=dtype)
+
+
 def test_negative_and_zero_scale():
     for scale in (-0.1, 0.0):
         check(Batch([3], [200], 16, 64, 62, DEV, scale=scale), f"scale {scale}", dtype=torch.float32)

@@ -61,6 +61,19 @@ def test_rope_in_place_in_a_wider_head(T, H):
     assert torch.equal(q[..., :512], q0[..., :512])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("T,H,dims,width", [(3001, 1, 64, 576), (5000, 5, 6, 7), (2500, 2, 256, 256), (70001, 1, 32, 32)])
+def test_rope_of_many_tokens_with_few_heads(dtype, interleaved, T, H, dims, width):
+    x = torch.randn(T, H, width, generator=gen(T)).to(dtype).to(DEV)
+    x0 = x.clone()
+    pos = torch.randint(-1000, 200000, (T,), generator=gen(H), dtype=torch.int32).to(DEV)
+    v = x[..., width - dims:]
+    S.splash_rope(v, pos, v, S.make_rope_desc(dims, interleaved=interleaved, **YARN))
+    check_rope(x0[..., width - dims:], v, pos, interleaved, YARN)
+    assert torch.equal(x[..., :width - dims], x0[..., :width - dims])
+
+
 def test_rope_head_major_and_undone():
     x = torch.randn(5, 40, 128, generator=gen(3)).to(DEV).transpose(0, 1)     # [40 tokens][5 heads], heads outermost
     pos = torch.arange(40, dtype=torch.int32, device=DEV) * 30011

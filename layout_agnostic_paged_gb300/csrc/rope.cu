@@ -7,7 +7,7 @@
 // serve all of its heads.  Threads move
 // 32 bytes at a time, so that a sector is written by one store.  8,191 tokens x 64 heads x 128
 // dims of fp16 (268 MB): 39.5 us, the copy bandwidth; 256 tokens x 128 heads x 64 dims inside wider
-// rows (8.4 MB): 2.3 us (16-byte vectors: 2.9 us).
+// rows (8.4 MB): 2.4 us (16-byte vectors: 2.9 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -5,8 +5,9 @@
 // of its fraction for far positions, and fp64 is slow on this GPU.  So the host turns f_i
 // into turns per position in 64-bit fixed point, F_i = round(f_i / (2 pi) * 2^64): the
 // low 64 bits of the integer product p * F_i are then the fraction of a turn, whole turns
-// dropped by the wrap itself, with an error of |p| / 2 units of 2^-64 turns.  One integer
-// multiply per pair, the same accuracy at every position.
+// dropped by the wrap itself, with an error of |p| / 2 units of 2^-64 turns (F_i is rounded once,
+// see rope_table.h): 2^-34 turns at the farthest position, far below fp32's share.  One integer multiply
+// per pair, the same accuracy at every position.
 #pragma once
 
 #include <stdint.h>

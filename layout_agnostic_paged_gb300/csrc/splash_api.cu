@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "rope.cuh"
+#include "rope_table.h"
 
 namespace splash {
 namespace {
@@ -151,31 +152,13 @@ int rope_turns(const splash_rope_desc* d, RopeTable* table) {
     if (d->dims > 2 * kMaxRopePairs) return SPLASH_ERR_UNSUPPORTED;
     if (d->scaling < SPLASH_ROPE_PLAIN || d->scaling > SPLASH_ROPE_YARN) return SPLASH_ERR_INVALID_ARG;
     if (!(d->base >= 1.0) || !isfinite(d->base) || !isfinite(d->amplitude)) return SPLASH_ERR_INVALID_ARG;
-    double lo = 0, hi = 0;
     if (d->scaling != SPLASH_ROPE_PLAIN && (!(d->factor >= 1.0) || !isfinite(d->factor)))
         return SPLASH_ERR_INVALID_ARG;
-    if (d->scaling == SPLASH_ROPE_YARN) {
-        if (!(d->base > 1.0) || !(d->orig_ctx > 0) || !(d->beta_fast > 0) || !(d->beta_slow > 0) ||
-            !isfinite(d->orig_ctx) || !isfinite(d->beta_fast) || !isfinite(d->beta_slow))
-            return SPLASH_ERR_INVALID_ARG;
-        const double two_pi = 6.283185307179586476925;
-        lo = floor(d->dims * log(d->orig_ctx / (two_pi * d->beta_fast)) / (2 * log(d->base)));
-        hi = ceil(d->dims * log(d->orig_ctx / (two_pi * d->beta_slow)) / (2 * log(d->base)));
-        lo = lo > 0 ? lo : 0;
-        hi = hi < d->dims - 1 ? hi : d->dims - 1;
-    }
-    for (int i = 0; i < d->dims / 2; ++i) {
-        double f = pow(d->base, -2.0 * i / d->dims);
-        if (d->scaling == SPLASH_ROPE_LINEAR) f /= d->factor;
-        if (d->scaling == SPLASH_ROPE_YARN) {
-            const double w = hi - lo > 0.001 ? hi - lo : 0.001;
-            double g = (i - lo) / w;
-            g = g < 0 ? 0 : (g > 1 ? 1 : g);
-            f = f * (1 - g) + f * g / d->factor;
-        }
-        // f <= 1 radian, so the fraction of a turn is below 1 / 6
-        last_table.turns[i] = uint64_t(ldexp(f * 0.15915494309189533577, 64) + 0.5);
-    }
+    if (d->scaling == SPLASH_ROPE_YARN &&
+        (!(d->base > 1.0) || !(d->orig_ctx > 0) || !(d->beta_fast > 0) || !(d->beta_slow > 0) ||
+         !isfinite(d->orig_ctx) || !isfinite(d->beta_fast) || !isfinite(d->beta_slow)))
+        return SPLASH_ERR_INVALID_ARG;
+    rope_table(*d, last_table.turns);
     last_table.amplitude = float(d->amplitude);
     last = *d;
     valid = true;

@@ -393,10 +393,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             commit_pair(drain, on);
         }
-        // every MMA has completed before TMEM and shared memory go (bounded like every wait)
-        volatile int never = 0;
-        mbar_wait(drain, 0, &never, status);
-        __syncwarp();
     } else if (warp >= 4 && warp < 12) {
         // -------------------------------------------------------- softmax
         // Two warps per TMEM lane quadrant, each with 32 of a lane's 64 score columns: a lane
@@ -629,6 +625,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (worked) ob = o_next(ob);
+        }
+        if (warp == 12) {
+            // Every MMA has completed before TMEM and shared memory go (bounded like every wait).  Here the wait begins
+            // when the work is done: begun by the second CTA's idle warp 1, it ran into its limit in calls of
+            // more than 2 s.
+            volatile int never = 0;
+            mbar_wait(drain, 0, &never, status);
+            __syncwarp();
         }
     }
 

@@ -77,6 +77,9 @@ constexpr int kTmemCols = 512;
 __device__ __forceinline__ uint32_t o_second(uint32_t o) { return o == 2 ? 0 : o + 1; }
 __device__ __forceinline__ uint32_t o_next(uint32_t o) { return o == 0 ? 2 : o - 1; }
 
+// What a key tile adds to the limit of a wait that lasts as long as an item: a tile takes 1.15 to 1.7 us.
+constexpr uint64_t kTileLimitNs = 20000;
+
 constexpr float kTau = 8.0f;                     // rescale O when a score beats the maximum by 2^8
 
 __device__ __forceinline__ float ex2(float x) {
@@ -542,7 +545,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool worked = it.t_hi > it.t_lo;   // no key tile: zeros
             float m = 0.f, l = 0.f;
             if (worked) {
-                if (!__all_sync(0xffffffffu, mbar_wait(fin_full, ph, abort_flag, status))) break;
+                // a wait for all of the item (a role that gives up sooner raises the abort flag, which ends it)
+                const uint64_t limit = kWaitLimitNs + uint64_t(it.t_hi - it.t_lo) * kTileLimitNs;
+                if (!__all_sync(0xffffffffu, mbar_wait(fin_full, ph, abort_flag, status, limit))) break;
                 const float2 f = sm_fin[row];
                 m = f.x;
                 l = f.y;

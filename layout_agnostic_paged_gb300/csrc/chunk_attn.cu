@@ -592,6 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 128; c += 64) {
                     float o[32];
                     if (worked) {
+                        __syncwarp();            // (a row that is not stored leaves its threads ahead of the others)
                         tmem_ld_rows16(t_o + (uint32_t(rr * 16) << 16) + buf * 128 + c, o);
                         tmem_wait_ld();
                         if (rr == 1 && c == 64) release(buf);

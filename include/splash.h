@@ -411,8 +411,9 @@ SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, co
 
 /*
  * Reads the device status of a decode or chunk workspace (SPLASH_DEVICE_* bits set
- * by the most recent splash_decode_attn or splash_chunk_attn that used it): synchronises
- * `stream`, then copies the bits to *flags (host pointer).  Returns SPLASH_OK or an error.
+ * by the most recent splash_decode_attn or splash_chunk_attn that used it; one without
+ * requests or new tokens clears them): synchronises `stream`, then copies the bits to *flags (host
+ * pointer).  Returns SPLASH_OK or an error.
  */
 SPLASH_API int splash_workspace_status(const void* workspace, uint32_t* flags, splash_stream_t stream);
 

@@ -53,6 +53,12 @@ int validate_desc(const splash_attn_desc* d) {
     return SPLASH_OK;
 }
 
+// A call without work leaves a workspace that reports no status bits (the first 16 bytes of either header).
+constexpr size_t kHeadBytes = 16;
+int clear_status(void* workspace, cudaStream_t stream) {
+    return cudaMemsetAsync(workspace, 0, kHeadBytes, stream) == cudaSuccess ? SPLASH_OK : SPLASH_ERR_CUDA;
+}
+
 // Launch geometry of the decode kernel for a head slice of Hs heads.
 struct Geometry {
     int head_groups;  // CTAs per CTA group (one per head group)
@@ -270,9 +276,9 @@ int splash_decode_attn_ex(const splash_attn_desc* desc, const splash_decode_ext*
     const int sts_cap = status_capacity(sms, ctas);
     const WorkspaceLayout lay(B, Hs, g.num_groups, sts_cap);
     if (ws_bytes < lay.total) return SPLASH_ERR_WORKSPACE;
-    if (B == 0) return SPLASH_OK;
-
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (B == 0) return clear_status(workspace, stream);
+
     DecodeArgs a;
     a.q = q;
     a.kv_pool = kv_pool;
@@ -518,7 +524,8 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     const size_t need = chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
     if (need == 0) return sms < 2 ? SPLASH_ERR_CUDA : SPLASH_ERR_UNSUPPORTED;
     if (ws_bytes < need) return SPLASH_ERR_WORKSPACE;
-    if (!work) return SPLASH_OK;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (!work) return clear_status(workspace, stream);
 
     const int64_t most = (int64_t(1) << 31) - 1;
     a.kv = static_cast<const uint8_t*>(kv_pool);
@@ -545,7 +552,6 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
               encode_pool(&maps.v, kv, rows, R, 4);
     for (int i = 0; ok && i < 3; ++i) ok = encode_pool(&maps.rows[i], kv, rows, 1u << (2 * i), 1);
     if (!ok) return SPLASH_ERR_CUDA;
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (launch_chunk_attn(a, maps, stream) != cudaSuccess || launch_chunk_combine(a, sms, stream) != cudaSuccess)
         return SPLASH_ERR_CUDA;
     return SPLASH_OK;
@@ -555,7 +561,7 @@ int splash_workspace_status(const void* workspace, uint32_t* flags, splash_strea
     if (!workspace || !flags) return SPLASH_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return SPLASH_ERR_CUDA;
-    uint32_t head[4];
+    uint32_t head[kHeadBytes / 4];
     if (cudaMemcpy(head, workspace, sizeof(head), cudaMemcpyDeviceToHost) != cudaSuccess) return SPLASH_ERR_CUDA;
     uint32_t bits = head[0];
     if (head[1] == kChunkMagic) {   // a chunk call: its CTAs' words hold the rest

@@ -219,7 +219,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane < loads) {
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
-                    else if (key < it.ctx && !second) atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
+                    else if (key + R > a.tok_lo && key < min(it.ctx, a.tok_hi) && !second)   // a page of the share
+                        atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
                 for (int g = 0; g < kKGroups; ++g) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[g], ph ^ 1, abort_flag, status))) {

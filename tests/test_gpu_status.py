@@ -53,3 +53,38 @@ def test_a_decode_without_requests_leaves_a_clean_status():
     assert S.splash_noalloc_status() == S.SPLASH_DEVICE_BAD_INPUT
     S.splash_decode_attn_noalloc(*none, b.scale)
     assert S.splash_noalloc_status() == 0
+
+
+SHARES = [(0, 100), (100, 300), (37, 61), (300, -1), (130, 250), (64, 192), (399, 400)]
+
+
+def share_table(b, page, lo, hi):
+    """b's block table with -1 for the pages that no token of [lo, hi) lies on."""
+    t = b.table.clone()
+    for r, c in enumerate(b.ctx):
+        end = c if hi < 0 else min(hi, c)
+        for p in range(t.shape[1]):
+            if p * page >= end or (p + 1) * page <= lo:
+                t[r, p] = -1
+    return t
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("lo,hi", SHARES)
+def test_pages_outside_a_share_need_not_exist(page, lo, hi):
+    b = Batch([2, 30], [333, 400], 16, page, 50, DEV)
+    ref = chunk_reference(b, 0, 16, lo, hi)
+    b.table = share_table(b, page, lo, hi)
+    out, lse, ws = chunk(b, lo, hi)
+    assert_chunk(b, out, lse, ref, 0, 16, f"share [{lo}, {hi})")
+    assert S.splash_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_a_missing_page_at_the_edge_of_a_share_is_flagged(page):
+    for lo, hi in ((100, 300), (37, 161)):
+        for tok in (lo, hi - 1):
+            b = Batch([1, 1], [333, 400], 16, page, 52, DEV)
+            b.table[1, tok // page] = -1
+            out, lse, ws = chunk(b, lo, hi)
+            assert S.splash_workspace_status(ws) == S.SPLASH_DEVICE_BAD_INPUT, (lo, hi, tok)

@@ -308,8 +308,15 @@ __global__ void __launch_bounds__(TcConfig<NPAD>::kThreads, 1)
                         }
                     }
                     const uint32_t present = __ballot_sync(0xffffffffu, my_pid >= 0);
-                    if (pw == 0 && __any_sync(0xffffffffu, bad) && lane == 0)
-                        atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
+                    if (pw == 0 && __any_sync(0xffffffffu, bad)) {
+                        // input that is wrong only where the page has a token of the range, which is looked up
+                        // again here (kept at hand for every tile, it cost the decode 1.6%)
+                        bool unused = false;
+                        const ReqPlan range = span_of(a, it.r - 1, unused);
+                        const int ptok = tok0 + lane * P;
+                        if (bad && ptok + P > range.lo && ptok < range.hi)
+                            atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
+                    }
                     const uint32_t blk_bytes = uint32_t(__popc(present)) * P * 128;
                     if (pw == 0 && lane == 0 && unsigned(ttr) < 3u) TRACE(4 + ttr * 3);
                     // box b of the tile (pair jj, page k, column block c2: b = jj * bpp + 2k + c2;

@@ -81,10 +81,26 @@ def test_pages_outside_a_share_need_not_exist(page, lo, hi):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("lo,hi", SHARES)
+def test_pages_outside_a_decode_share_need_not_exist(page, lo, hi):
+    b = Batch([1, 1], [333, 400], 16, page, 51, DEV)
+    ref = chunk_reference(b, 0, 16, lo, hi)
+    b.table = share_table(b, page, lo, hi)
+    out, lse = torch.empty(2, 16, 512, device=DEV), torch.empty(2, 16, device=DEV)
+    ws = S.decode_workspace(b.q, b.pool, b.table, b.scale)
+    S.splash_decode_attn(b.q, b.pool, b.table, b.ctx_t, 0, 16, lo, hi, out, lse, ws, b.scale)
+    assert_chunk(b, out, lse, ref, 0, 16, f"share [{lo}, {hi})")
+    assert S.splash_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
 def test_a_missing_page_at_the_edge_of_a_share_is_flagged(page):
     for lo, hi in ((100, 300), (37, 161)):
         for tok in (lo, hi - 1):
             b = Batch([1, 1], [333, 400], 16, page, 52, DEV)
             b.table[1, tok // page] = -1
             out, lse, ws = chunk(b, lo, hi)
+            assert S.splash_workspace_status(ws) == S.SPLASH_DEVICE_BAD_INPUT, (lo, hi, tok)
+            ws = S.decode_workspace(b.q, b.pool, b.table, b.scale)
+            S.splash_decode_attn(b.q, b.pool, b.table, b.ctx_t, 0, 16, lo, hi, out, lse, ws, b.scale)
             assert S.splash_workspace_status(ws) == S.SPLASH_DEVICE_BAD_INPUT, (lo, hi, tok)

@@ -332,8 +332,9 @@ SPLASH_API int splash_rope(const splash_rope_desc* rope, int dtype, const void* 
  *                    the least with max |x| <= 448 * 2^(b - 127) over its finite x (0 for a group
  *                    of zeros), and its codes are x / 2^(b - 127) rounded to nearest even.  NaN stays
  *                    NaN, an infinity becomes the group's largest code.  Every held value
- *                    is exact in bf16 (scale bytes below 3 aside, where values reach below
- *                    bf16's least).
+ *                    is exact in bf16, with two exceptions: with scale bytes below 3 values
+ *                    reach below bf16's least, and a finite |x| of 248 * 2^120 or more (bf16's last
+ *                    eight) rounds to 2^128, which splash_kv_unpack reads back as an infinity.
  * Pages are P consecutive rows either way, so splash_kv_migrate moves both.
  */
 enum { SPLASH_KV_BF16 = 0, SPLASH_KV_MXFP8 = 1 };

@@ -401,8 +401,9 @@ SPLASH_API size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int 
  * A cu_q that descends or leaves [0, total_q] (no row is written then), a context length
  * outside [0, max_pages_per_req * P] (clamped) and a needed page id outside [0, num_pages) (its
  * tokens are left out) set SPLASH_DEVICE_BAD_INPUT, read with splash_workspace_status.
- * max_pages_per_req * P may be 2^31 - 1024 at most.  The same call on the same device gives the
- * same bits.
+ * max_pages_per_req * P may be 2^31 - 1024 at most.  out is summed over the keys in fp32 with truncation:
+ * over a context of millions of keys it comes out small, by up to 0.5% per million.  The same call on
+ * the same device gives the same bits.
  */
 SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool,
                                  const int32_t* cu_q, int total_q, const int32_t* block_table,

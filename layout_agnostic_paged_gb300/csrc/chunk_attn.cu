@@ -35,8 +35,12 @@
 // (89%).  Four whole prompts of 257-1,024 tokens: 0.26 ms (51%), an item being three tiles long on average
 // and the causal edge half of one; what is left is the chain from an item's last scores over
 // their softmax and O to the next item's first (6,400 clocks for an item of one tile).  64 requests of 4
-// drafted tokens, 16 heads, over 512-4,096 (173 MB): 53 us, 3.2 TB/s: 15 tiles a pair, each held
+// drafted tokens, 16 heads, over 512-4,096 (173 MB): 54 us, 3.2 TB/s: 15 tiles a pair, each held
 // by the latency of its keys, between the start (5 us) and the merge (6 us).
+//
+// The tensor cores' fp32 additions truncate, so O comes out small where one item sums very many keys: by
+// 0.05% over 131,072 keys and 0.44% over a million, measured with values of one sign, which is the worst case
+// (0.07% over a million normal ones); l, summed in registers with rounding, does not share it.
 #include <math.h>
 
 #include "chunk.h"

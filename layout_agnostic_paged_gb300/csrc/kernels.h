@@ -81,6 +81,35 @@ cudaError_t launch_kv_unpack(const void* src, void* dst, int P, const int32_t* s
                              const int32_t* dst_ids, int n, int src_np, int dst_np, int sms,
                              cudaStream_t stream);
 
+// A batch's index arrays (see splash_batch_tables), and pages back to the free list.
+struct BatchTablesArgs {
+    const int32_t* past;
+    const int32_t* fresh;         // new tokens
+    int32_t* table;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* cu;
+    int32_t* ctx;
+    int32_t* positions;
+    int32_t* slots;
+    int32_t* left;
+    int B, total_q, P_log, num_pages, max_pages;
+    int wide;                     // positions and slots are 16-byte aligned
+};
+struct BatchReleaseArgs {
+    int32_t* ctx;
+    const int32_t* keep;          // null: every token is kept
+    int32_t* table;
+    int32_t* free_pages;
+    int32_t* free_count;
+    int B, P_log, num_pages, max_pages;
+    int window, sinks;            // window 0: none
+};
+constexpr int kReleaseCtas = 8;
+constexpr int kSmallBatchRows = 2048;   // up to so many rows one CTA writes them all
+cudaError_t launch_batch_tables(const BatchTablesArgs& a, cudaStream_t stream);
+cudaError_t launch_batch_release(const BatchReleaseArgs& a, cudaStream_t stream);
+
 // Tensor-core decode kernel: head groups of at most 64 heads, one CTA per (CTA group,
 // head group), persistent over the plan.  map_q covers q as [B*H rows][576] bf16 with
 // a {64, pad(group_heads)} box; map_kv covers the pool as [num_pages*P rows][576] with

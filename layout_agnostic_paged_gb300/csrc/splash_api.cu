@@ -6,6 +6,7 @@
 
 #include <math.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <unordered_map>
 
@@ -460,6 +461,78 @@ int splash_kv_unpack(const void* src_pool, void* dst_pool, int page_size, const 
 
 namespace {
 
+int page_log(int P) { return P == 16 ? 4 : (P == 32 ? 5 : (P == 64 ? 6 : 7)); }
+
+}  // namespace
+
+int splash_batch_tables(const splash_attn_desc* desc, const int32_t* past_lens, const int32_t* new_lens,
+                        int32_t* block_table, const int32_t* free_pages, const int32_t* free_count, int total_q,
+                        int32_t* cu_q, int32_t* ctx_lens, int32_t* positions, int32_t* slots, int32_t* left,
+                        splash_stream_t stream) {
+    const int st = validate_desc(desc);
+    if (st != SPLASH_OK) return st;
+    if (total_q < 0) return SPLASH_ERR_INVALID_ARG;
+    if (total_q > 1 << 30) return SPLASH_ERR_UNSUPPORTED;
+    if (!cu_q || !left || !free_count) return SPLASH_ERR_INVALID_ARG;
+    if (desc->num_reqs > 0 && (!past_lens || !new_lens || !ctx_lens)) return SPLASH_ERR_INVALID_ARG;
+    if (desc->num_reqs > 0 && desc->max_pages_per_req > 0 && !block_table) return SPLASH_ERR_INVALID_ARG;
+    if ((desc->num_pages > 0 && !free_pages) || (total_q > 0 && (!positions || !slots))) return SPLASH_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(past_lens), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_count), static_cast<const void*>(cu_q),
+                          static_cast<const void*>(ctx_lens), static_cast<const void*>(positions),
+                          static_cast<const void*>(slots), static_cast<const void*>(left)})
+        if (!aligned(p, 4)) return SPLASH_ERR_INVALID_ARG;
+    BatchTablesArgs a = {};
+    a.past = past_lens;
+    a.fresh = new_lens;
+    a.table = block_table;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.cu = cu_q;
+    a.ctx = ctx_lens;
+    a.positions = positions;
+    a.slots = slots;
+    a.left = left;
+    a.B = desc->num_reqs;
+    a.total_q = total_q;
+    a.P_log = page_log(desc->page_size);
+    a.num_pages = desc->num_pages;
+    a.max_pages = desc->max_pages_per_req;
+    a.wide = aligned(positions, 16) && aligned(slots, 16);
+    if (launch_batch_tables(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+int splash_batch_release(const splash_attn_desc* desc, int32_t* ctx_lens, const int32_t* keep_lens,
+                         int32_t* block_table, int32_t* free_pages, int32_t* free_count, int window, int sinks,
+                         splash_stream_t stream) {
+    const int st = validate_desc(desc);
+    if (st != SPLASH_OK) return st;
+    if (window < 0 || sinks < 0) return SPLASH_ERR_INVALID_ARG;
+    if (desc->num_reqs == 0 || desc->max_pages_per_req == 0) return SPLASH_OK;
+    if (!ctx_lens || !block_table || !free_count || (desc->num_pages > 0 && !free_pages)) return SPLASH_ERR_INVALID_ARG;
+    if (!aligned(ctx_lens, 4) || !aligned(keep_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_count, 4))
+        return SPLASH_ERR_INVALID_ARG;
+    BatchReleaseArgs a = {};
+    a.ctx = ctx_lens;
+    a.keep = keep_lens;
+    a.table = block_table;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.B = desc->num_reqs;
+    a.P_log = page_log(desc->page_size);
+    a.num_pages = desc->num_pages;
+    a.max_pages = desc->max_pages_per_req;
+    a.window = window;
+    a.sinks = sinks;
+    if (launch_batch_release(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
+namespace {
+
 // Positions rounded up to whole tiles, and a tile ahead, stay below 2^31.
 bool chunk_too_long(const splash_attn_desc* d) {
     return int64_t(d->max_pages_per_req) * d->page_size > (int64_t(1) << 31) - 1024;
@@ -479,7 +552,7 @@ size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int h
     a->head_lo = head_lo;
     a->Hs = head_hi - head_lo;
     a->P = desc->page_size;
-    a->P_log = a->P == 16 ? 4 : (a->P == 32 ? 5 : (a->P == 64 ? 6 : 7));
+    a->P_log = page_log(a->P);
     a->num_pages = desc->num_pages;
     a->max_pages = desc->max_pages_per_req;
     a->max_ctx = desc->max_pages_per_req * desc->page_size;

@@ -29,6 +29,7 @@ EXPORTED = ("splash_decode_workspace_size", "splash_decode_attn", "splash_decode
             "splash_decode_attn_noalloc", "splash_noalloc_status",
             "splash_lse_merge", "splash_kv_migrate", "splash_rope", "splash_kv_append",
             "splash_kv_unpack", "splash_chunk_workspace_size", "splash_chunk_attn",
+            "splash_batch_tables", "splash_batch_release",
             "splash_workspace_status", "splash_status_string")
 
 SPLASH_BF16, SPLASH_F16, SPLASH_F32 = 0, 1, 2
@@ -109,6 +110,10 @@ def load_library(path: str | None = None):
         lib.splash_chunk_attn.argtypes = [dp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i64, i32, vp, vp,
                                           vp, sz, vp]
         lib.splash_chunk_attn.restype = i32
+        lib.splash_batch_tables.argtypes = [dp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+        lib.splash_batch_tables.restype = i32
+        lib.splash_batch_release.argtypes = [dp, vp, vp, vp, vp, vp, i32, i32, vp]
+        lib.splash_batch_release.restype = i32
         lib.splash_workspace_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         lib.splash_workspace_status.restype = i32
         lib.splash_status_string.argtypes = [i32]
@@ -345,6 +350,58 @@ def _index_arrays(where: str, cu_q, block_table, ctx_lens) -> tuple[int, int]:
 def _shape_desc(B: int, H: int, P: int, num_pages: int, max_pages: int, scale: float) -> SplashAttnDesc:
     """The description of a shape (read-only; the library reads it during the call)."""
     return SplashAttnDesc(B, H, 576, 512, P, num_pages, max_pages, scale)
+
+
+def _int32_arrays(where: str, **arrays) -> None:
+    """Contiguous int32 tensors, each of the shape given beside it."""
+    for name, (t, shape) in arrays.items():
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous int32 {list(shape)}")
+
+
+def splash_batch_tables(past_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                        free_pages: torch.Tensor, free_count: torch.Tensor, cu_q: torch.Tensor,
+                        ctx_lens: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, left: torch.Tensor,
+                        stream=None) -> None:
+    """A step's arrays from its requests' lengths (all int32): takes pages for the new tokens from the top of
+    the stack free_pages [num_pages] (free_count [1] entries) into block_table [B][max_pages], and writes cu_q
+    [B + 1], ctx_lens [B], positions and slots [N rows] and left [2] = (free pages left, requests served).
+    ctx_lens may be past_lens, and free_count left[:1]; see splash.h for batches that do not fit."""
+    where = "splash_batch_tables"
+    dev = _device_of(where, past_lens, new_lens, block_table, free_pages, free_count, cu_q, ctx_lens, positions, slots,
+                     left)
+    shape = block_table.shape
+    if len(shape) != 2 or free_pages.dim() != 1 or positions.dim() != 1:
+        raise ValueError(f"{where}: block_table [B][max_pages], free_pages [num_pages] and positions [N]")
+    B, N = shape[0], positions.shape[0]
+    _int32_arrays(where, past_lens=(past_lens, (B,)), new_lens=(new_lens, (B,)), block_table=(block_table, shape),
+                  free_pages=(free_pages, free_pages.shape), free_count=(free_count, (1,)), cu_q=(cu_q, (B + 1,)),
+                  ctx_lens=(ctx_lens, (B,)), positions=(positions, (N,)), slots=(slots, (N,)), left=(left, (2,)))
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_tables,
+          _shape_desc(B, 1, int(page_size), free_pages.shape[0], shape[1], 1.0), past_lens.data_ptr(), new_lens.data_ptr(),
+          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), N, cu_q.data_ptr(), ctx_lens.data_ptr(),
+          positions.data_ptr(), slots.data_ptr(), left.data_ptr())
+
+
+def splash_batch_release(ctx_lens: torch.Tensor, keep_lens: torch.Tensor | None, block_table: torch.Tensor,
+                         page_size: int, free_pages: torch.Tensor, free_count: torch.Tensor, window: int = 0,
+                         sinks: int = 0, stream=None) -> None:
+    """Drops all but the first keep_lens [B] tokens of each request (None: drops none), and with a window also
+    the tokens that no later one sees: their pages go back on the stack free_pages (free_count [1] entries, or left
+    of splash_batch_tables, whose first entry is the count), their entries of block_table become -1, and ctx_lens [B]
+    the tokens that are left."""
+    where = "splash_batch_release"
+    dev = _device_of(where, ctx_lens, block_table, free_pages, free_count, *(() if keep_lens is None else (keep_lens,)))
+    shape = block_table.shape
+    if len(shape) != 2 or free_pages.dim() != 1 or free_count.dim() != 1 or free_count.shape[0] not in (1, 2):
+        raise ValueError(f"{where}: block_table [B][max_pages], free_pages [num_pages] and free_count [1]")
+    B = shape[0]
+    _int32_arrays(where, ctx_lens=(ctx_lens, (B,)), block_table=(block_table, shape), free_pages=(free_pages, free_pages.shape),
+                  free_count=(free_count, free_count.shape), keep_lens=(ctx_lens if keep_lens is None else keep_lens, (B,)))
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_release,
+          _shape_desc(B, 1, int(page_size), free_pages.shape[0], shape[1], 1.0), ctx_lens.data_ptr(),
+          None if keep_lens is None else keep_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+          free_count.data_ptr(), int(window), int(sinks))
 
 
 def make_rope_desc(dims: int, base: float = 10000.0, interleaved: bool = True, scaling: str = "none",

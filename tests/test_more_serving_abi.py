@@ -1,0 +1,81 @@
+"""Host-side refusals of the batch tables, the norm with rope and the attention's windows and groups.  CPU only:
+no call here reaches a kernel."""
+import pytest
+import torch
+
+from layout_agnostic_paged_gb300 import build as B
+from layout_agnostic_paged_gb300 import splash as S
+
+FAKE = 0x10000  # never dereferenced: every call below fails host validation first
+INVALID, UNSUPPORTED = S.SPLASH_ERR_INVALID_ARG, S.SPLASH_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return S.load_library()
+
+
+def desc(**kw):
+    d = dict(num_reqs=2, num_heads=8, d_qk=576, d_v=512, page_size=16, num_pages=11, max_pages_per_req=7,
+             scale=0.0721)
+    d.update(kw)
+    return S.SplashAttnDesc(**d)
+
+
+# ------------------------------------------------------------------ batch tables
+
+def tables(lib, d, past=FAKE, new=FAKE, table=FAKE, pages=FAKE, count=FAKE, n=6, cu=FAKE, ctx=FAKE, pos=FAKE, slots=FAKE,
+           left=FAKE):
+    return lib.splash_batch_tables(d, past, new, table, pages, count, n, cu, ctx, pos, slots, left, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(past=0), INVALID), (dict(new=0), INVALID), (dict(table=0), INVALID), (dict(pages=0), INVALID),
+    (dict(count=0), INVALID), (dict(cu=0), INVALID), (dict(ctx=0), INVALID), (dict(pos=0), INVALID),
+    (dict(slots=0), INVALID), (dict(left=0), INVALID), (dict(n=-1), INVALID), (dict(n=(1 << 30) + 1), UNSUPPORTED),
+    (dict(past=FAKE + 2), INVALID), (dict(slots=FAKE + 1), INVALID), (dict(left=FAKE + 2), INVALID),
+])
+def test_tables_rejects_bad_arguments(lib, kw, code):
+    assert tables(lib, desc(), **kw) == code
+
+
+def test_tables_rejects_bad_shapes(lib):
+    assert tables(lib, None) == INVALID
+    for kw, code in ((dict(page_size=48), UNSUPPORTED), (dict(num_reqs=-1), INVALID), (dict(d_v=576), UNSUPPORTED),
+                     (dict(num_pages=1 << 28), UNSUPPORTED), (dict(max_pages_per_req=-1), INVALID)):
+        assert tables(lib, desc(**kw)) == code
+
+
+def release(lib, d, ctx=FAKE, keep=FAKE, table=FAKE, pages=FAKE, count=FAKE, window=0, sinks=0):
+    return lib.splash_batch_release(d, ctx, keep, table, pages, count, window, sinks, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(ctx=0), INVALID), (dict(table=0), INVALID), (dict(pages=0), INVALID), (dict(count=0), INVALID),
+    (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(keep=FAKE + 2), INVALID), (dict(table=FAKE + 1), INVALID),
+])
+def test_release_rejects_bad_arguments(lib, kw, code):
+    assert release(lib, desc(), **kw) == code
+
+
+def test_release_of_nothing_is_fine(lib):
+    assert release(lib, None) == INVALID
+    assert release(lib, desc(page_size=8)) == UNSUPPORTED
+    assert release(lib, desc(num_reqs=0), ctx=0, table=0) == S.SPLASH_OK
+    assert release(lib, desc(max_pages_per_req=0), ctx=0, table=0) == S.SPLASH_OK
+
+
+def test_binding_refuses_cpu_tensors_and_bad_shapes():
+    i = torch.zeros(2, dtype=torch.int32)
+    t = torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        S.splash_batch_tables(i, i, t, 16, i, i, i, i, i, i, i)
+    with pytest.raises(ValueError, match="CUDA"):
+        S.splash_batch_release(i, None, t, 16, i, i)
+    with pytest.raises(ValueError, match="past_lens"):
+        S._int32_arrays("x", past_lens=(i.long(), (2,)))
+    with pytest.raises(ValueError, match="cu_q"):
+        S._int32_arrays("x", cu_q=(i, (3,)))
+    with pytest.raises(ValueError, match="slots"):
+        S._int32_arrays("x", slots=(t[:, 0], (2,)))

@@ -370,6 +370,57 @@ SPLASH_API int splash_rope(const splash_rope_desc* rope, int dtype, const void* 
                            int T, int H, splash_stream_t stream);
 
 /*
+ * RMS norm of head rows with the rotary positions of a part of each row in the same pass (host structs,
+ * read during the call only).
+ *   width         D, dims of a row, 1..1024
+ *   norm_dims     n, 1..D: dims [0, n) are normalised, the others are copied (a key row whose position dims
+ *                 follow its latent, for instance)
+ *   rope_lo       the first rotated dim: [rope_lo, rope_lo + rope->dims) lies within the row
+ *   weight_dtype  SPLASH_BF16, SPLASH_F16 or SPLASH_F32, of the weights
+ *   eps           >= 0, finite
+ *   weight_offset added to every weight (1 for weights that are held as differences from one)
+ */
+typedef struct {
+    int32_t width;
+    int32_t norm_dims;
+    int32_t rope_lo;
+    int32_t weight_dtype;
+    float eps;
+    float weight_offset;
+} splash_norm_desc;
+
+/*
+ * One side's rows: x and y [T][heads][D] of the call's dtype with strides in elements (rows dense), and
+ * weight [n] (NULL: ones, without the offset).  reserved is 0.
+ */
+typedef struct {
+    const void* x;
+    int64_t x_token_stride;
+    int64_t x_head_stride;
+    void* y;
+    int64_t y_token_stride;
+    int64_t y_head_stride;
+    const void* weight;
+    int32_t heads;
+    int32_t reserved;
+} splash_norm_rows;
+
+/*
+ * For every row of q, and of k with weights of its own (k may be NULL):
+ *   z_j = x_j * (mean(x_0^2, ..., x_{n-1}^2) + eps)^(-1/2) * (weight_j + weight_offset), j < n;  z_j = x_j, j >= n
+ *   y = z with the dims [rope_lo, rope_lo + d) rotated as by splash_rope (rope NULL: y = z, positions unused)
+ * Computed in fp32 and rounded once; the sum of squares neither over- nor underflows.  Among the first n dims a NaN
+ * makes NaN of them all, an infinity NaN of itself and zeros of the others, and a row of zeros with eps = 0 is NaN.
+ *   positions   int32 [T], of both sides' rows
+ * A side's y may be its x with the same strides; otherwise no two of the arrays may overlap.  Any alignment of
+ * the elements' own size is taken; fastest are 16-byte aligned pointers and strides with n, rope_lo, D and d / 2
+ * multiples of 16 bytes.
+ */
+SPLASH_API int splash_norm_rope(const splash_norm_desc* norm, const splash_rope_desc* rope, int dtype,
+                                const splash_norm_rows* q, const splash_norm_rows* k, const int32_t* positions,
+                                int T, splash_stream_t stream);
+
+/*
  * Cache formats of splash_kv_append:
  *   SPLASH_KV_BF16   rows of 576 bf16 (1,152 bytes), what the attention reads
  *   SPLASH_KV_MXFP8  rows of 656 bytes: 512 e4m3 latents, 16 scale bytes (one per 32 latents),

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "rope.cuh"
+
 namespace splash {
 
 // Launches `kernel` on `stream` with programmatic stream serialization (the kernel
@@ -64,7 +66,6 @@ cudaError_t launch_kv_migrate(const void* src, void* dst, size_t page_bytes, con
                               cudaStream_t stream);
 
 constexpr int kMxRowBytes = 656;   // MXFP8 cache row: 512 e4m3, 16 scale bytes, 64 bf16
-struct RopeTable;
 struct RopeTable32;
 // Rotary positions of T x H head rows (dtype: SPLASH_BF16 / F16 / F32); vec_bytes: the vectors that
 // pointers, strides and dims allow (32, 16, or 0 for single elements).
@@ -109,6 +110,31 @@ constexpr int kReleaseCtas = 8;
 constexpr int kSmallBatchRows = 2048;   // up to so many rows one CTA writes them all
 cudaError_t launch_batch_tables(const BatchTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_batch_release(const BatchReleaseArgs& a, cudaStream_t stream);
+
+// RMS norm and rotation of head rows (see splash_norm_rope).
+constexpr int kMaxNormWidth = 1024;
+struct NormRows {
+    const void* x;
+    void* y;
+    const void* weight;           // null: ones
+    int64_t xt, xh, yt, yh;       // strides in elements
+    int H;
+};
+struct NormArgs {
+    NormRows q, k;                // k.H == 0: no keys
+    const int32_t* positions;
+    int T, width, norm_dims, rope_lo, dims, weight_dtype;   // dims 0: nothing is rotated
+    float eps, weight_offset;
+    RopeTable table;
+    // set by the launcher
+    float inv_n;
+    int weight_len;               // floats of a weight array in shared memory
+    int units, rot_units, plain_units;   // of a row: two vectors each, the rotated ones first
+    int G, G_log;                 // lanes of a row
+    int chunks, rows_per_block, tokens_per_block;
+};
+// vectors: pointers, strides and the parts of a row allow 16-byte vectors, whose pairs lie in one unit.
+cudaError_t launch_norm_rope(NormArgs& a, int dtype, bool interleaved, bool vectors, int sms, cudaStream_t stream);
 
 // Tensor-core decode kernel: head groups of at most 64 heads, one CTA per (CTA group,
 // head group), persistent over the plan.  map_q covers q as [B*H rows][576] bf16 with

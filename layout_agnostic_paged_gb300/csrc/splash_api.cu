@@ -406,6 +406,79 @@ int splash_rope(const splash_rope_desc* rope, int dtype, const void* x, int64_t 
     return SPLASH_OK;
 }
 
+namespace {
+
+// Checks one side's rows of splash_norm_rope and copies them; `vectors` stays true if 16-byte vectors fit them.
+int norm_rows(const splash_norm_rows* r, const splash_norm_desc* norm, int size, int T, NormRows* out, bool* vectors) {
+    if (r->heads < 0 || r->reserved != 0 || r->x_token_stride < 0 || r->x_head_stride < 0 || r->y_token_stride < 0 ||
+        r->y_head_stride < 0)
+        return SPLASH_ERR_INVALID_ARG;
+    out->H = r->heads;
+    if (r->heads == 0 || T == 0) return SPLASH_OK;
+    // rows of y may not share elements: the head rows of a token, then the tokens, or the other way round
+    const int64_t D = norm->width, yt = r->y_token_stride, yh = r->y_head_stride, H = r->heads;
+    if ((H > 1 && yh < D) || (T > 1 && yt < D)) return SPLASH_ERR_INVALID_ARG;
+    if (T > 1 && H > 1 && yt < (H - 1) * yh + D && yh < (T - 1) * yt + D) return SPLASH_ERR_INVALID_ARG;
+    if (!r->x || !r->y || !aligned(r->x, size) || !aligned(r->y, size)) return SPLASH_ERR_INVALID_ARG;
+    if (!aligned(r->weight, norm->weight_dtype == SPLASH_F32 ? 4 : 2)) return SPLASH_ERR_INVALID_ARG;
+    out->x = r->x;
+    out->y = r->y;
+    out->weight = r->weight;
+    out->xt = r->x_token_stride;
+    out->xh = r->x_head_stride;
+    out->yt = yt;
+    out->yh = yh;
+    const int ve = 16 / size;
+    *vectors = *vectors && aligned(r->x, 16) && aligned(r->y, 16) && out->xt % ve == 0 && out->xh % ve == 0 &&
+               yt % ve == 0 && yh % ve == 0;
+    return SPLASH_OK;
+}
+
+}  // namespace
+
+int splash_norm_rope(const splash_norm_desc* norm, const splash_rope_desc* rope, int dtype, const splash_norm_rows* q,
+                     const splash_norm_rows* k, const int32_t* positions, int T, splash_stream_t stream) {
+    if (!norm || !q) return SPLASH_ERR_INVALID_ARG;
+    if (dtype != SPLASH_BF16 && dtype != SPLASH_F16 && dtype != SPLASH_F32) return SPLASH_ERR_UNSUPPORTED;
+    if (norm->weight_dtype != SPLASH_BF16 && norm->weight_dtype != SPLASH_F16 && norm->weight_dtype != SPLASH_F32)
+        return SPLASH_ERR_UNSUPPORTED;
+    if (norm->width < 1 || norm->norm_dims < 1 || norm->norm_dims > norm->width || T < 0) return SPLASH_ERR_INVALID_ARG;
+    if (norm->width > kMaxNormWidth) return SPLASH_ERR_UNSUPPORTED;
+    if (!(norm->eps >= 0.f) || !isfinite(norm->eps) || !isfinite(norm->weight_offset)) return SPLASH_ERR_INVALID_ARG;
+    NormArgs a = {};
+    if (rope) {
+        const int st = rope_turns(rope, &a.table);
+        if (st != SPLASH_OK) return st;
+        if (norm->rope_lo < 0 || norm->rope_lo > norm->width - rope->dims) return SPLASH_ERR_INVALID_ARG;
+        a.rope_lo = norm->rope_lo;
+        a.dims = rope->dims;
+    }
+    const int size = dtype == SPLASH_F32 ? 4 : 2, ve = 16 / size;
+    // every part of a row, and each half of the rotated dims, is whole vectors
+    bool vectors = norm->width % ve == 0 && norm->norm_dims % ve == 0 && a.rope_lo % ve == 0 && a.dims / 2 % ve == 0;
+    int st = norm_rows(q, norm, size, T, &a.q, &vectors);
+    if (st == SPLASH_OK && k) st = norm_rows(k, norm, size, T, &a.k, &vectors);
+    if (st != SPLASH_OK) return st;
+    if (int64_t(T) * (int64_t(a.q.H) + a.k.H) >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
+    if (T == 0 || a.q.H + a.k.H == 0) return SPLASH_OK;
+    if (rope && (!positions || !aligned(positions, 4))) return SPLASH_ERR_INVALID_ARG;
+    a.positions = positions;
+    a.T = T;
+    a.width = norm->width;
+    a.norm_dims = norm->norm_dims;
+    a.weight_dtype = norm->weight_dtype;
+    a.eps = norm->eps;
+    a.weight_offset = norm->weight_offset;
+    int dev = 0;
+    if (current_device(&dev) != 0) return SPLASH_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SPLASH_ERR_CUDA;
+    if (launch_norm_rope(a, dtype, rope && rope->interleaved, vectors, sms, reinterpret_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+        return SPLASH_ERR_CUDA;
+    return SPLASH_OK;
+}
+
 int splash_kv_append(const splash_attn_desc* desc, const splash_rope_desc* rope, int format, const void* latent,
                      int64_t latent_stride, const void* k_rope, int64_t k_rope_stride, const int32_t* cu_q,
                      int total_q, const int32_t* block_table, const int32_t* ctx_lens, void* kv_pool,

@@ -29,7 +29,7 @@ EXPORTED = ("splash_decode_workspace_size", "splash_decode_attn", "splash_decode
             "splash_decode_attn_noalloc", "splash_noalloc_status",
             "splash_lse_merge", "splash_kv_migrate", "splash_rope", "splash_kv_append",
             "splash_kv_unpack", "splash_chunk_workspace_size", "splash_chunk_attn",
-            "splash_batch_tables", "splash_batch_release",
+            "splash_batch_tables", "splash_batch_release", "splash_norm_rope",
             "splash_workspace_status", "splash_status_string")
 
 SPLASH_BF16, SPLASH_F16, SPLASH_F32 = 0, 1, 2
@@ -67,6 +67,17 @@ class SplashRopeDesc(ctypes.Structure):
                 ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double)]
 
 
+class SplashNormDesc(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("norm_dims", ctypes.c_int32), ("rope_lo", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class SplashNormRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -101,6 +112,9 @@ def load_library(path: str | None = None):
         rp = ctypes.POINTER(SplashRopeDesc)
         lib.splash_rope.argtypes = [rp, i32, vp, i64, i64, vp, i64, i64, vp, i32, i32, vp]
         lib.splash_rope.restype = i32
+        np = ctypes.POINTER(SplashNormRows)
+        lib.splash_norm_rope.argtypes = [ctypes.POINTER(SplashNormDesc), rp, i32, np, np, vp, i32, vp]
+        lib.splash_norm_rope.restype = i32
         lib.splash_kv_append.argtypes = [dp, rp, i32, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp]
         lib.splash_kv_append.restype = i32
         lib.splash_kv_unpack.argtypes = [vp, vp, i32, vp, vp, i32, ctypes.c_int32, ctypes.c_int32, vp]
@@ -433,6 +447,63 @@ def splash_rope(x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor, rop
         raise ValueError("splash_rope: head rows and positions must be dense")
     _call(dev, stream, "splash_rope", (_lib or load_library()).splash_rope, rope, dtype, x.data_ptr(), xt, xh,
           out.data_ptr(), yt, yh, positions.data_ptr(), T, H)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_desc(width: int, norm_dims: int, rope_lo: int, weight_dtype: int, eps: float, offset: float) -> SplashNormDesc:
+    """The description of a norm (read-only; the library reads it during the call)."""
+    return SplashNormDesc(width, norm_dims, rope_lo, weight_dtype, eps, offset)
+
+
+def _norm_rows(where: str, x, weight, out, T: int, D: int, n: int, dtype, weight_dtype) -> SplashNormRows:
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or out.shape != shape:
+        raise ValueError(f"{where}: rows and their results must be [T][heads][D], q's and k's with the same T and D")
+    if x.dtype != dtype or out.dtype != dtype:
+        raise ValueError(f"{where}: rows and results must share one dtype")
+    xt, xh, x1 = x.stride()
+    yt, yh, y1 = out.stride()
+    H = shape[1]
+    if (x1 != 1 or y1 != 1) and D > 1 and T and H:
+        raise ValueError(f"{where}: rows must be dense")
+    w = None
+    if weight is not None:
+        if weight.dtype != weight_dtype or weight.shape != (n,) or not weight.is_contiguous():
+            raise ValueError(f"{where}: weights must be dense [norm_dims] of one floating dtype")
+        w = weight.data_ptr()
+    return SplashNormRows(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, w, H, 0)
+
+
+def splash_norm_rope(q: torch.Tensor, q_weight: torch.Tensor | None, q_out: torch.Tensor, k: torch.Tensor | None,
+                     k_weight: torch.Tensor | None, k_out: torch.Tensor | None, positions: torch.Tensor | None,
+                     rope: SplashRopeDesc | None, eps: float, norm_dims: int | None = None, rope_lo: int = 0,
+                     weight_offset: float = 0.0, stream=None) -> None:
+    """RMS norm (weights [norm_dims], None: ones) of the first norm_dims dims (None: all) of every row of q
+    [T][Hq][D] and k [T][Hk][D] (None: q alone), and the rotation of dims [rope_lo, rope_lo + rope.dims) by positions
+    int32 [T] (rope None: no rotation).  All are views with dense rows and any token and head strides; an output
+    may be its input."""
+    where = "splash_norm_rope"
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{where}: k and k_out belong together")
+    weight = q_weight if q_weight is not None else k_weight
+    dev = _device_of(where, q, q_out, *(t for t in (q_weight, k, k_weight, k_out, positions) if t is not None))
+    if q.dim() != 3:
+        raise ValueError(f"{where}: q must be [T][heads][D]")
+    T, _, D = q.shape
+    n = D if norm_dims is None else int(norm_dims)
+    dtype = _DTYPES.get(q.dtype)
+    weight_dtype = SPLASH_F32 if weight is None else _DTYPES.get(weight.dtype)
+    if dtype is None or weight_dtype is None:
+        raise ValueError(f"{where}: rows and weights must be bfloat16, float16 or float32")
+    if rope is not None and (positions is None or positions.dtype != torch.int32 or positions.shape != (T,)
+                             or not positions.is_contiguous()):
+        raise ValueError(f"{where}: positions must be contiguous int32 [T]")
+    wd = None if weight is None else weight.dtype
+    a = _norm_rows(where, q, q_weight, q_out, T, D, n, q.dtype, wd)
+    b = None if k is None else _norm_rows(where, k, k_weight, k_out, T, D, n, q.dtype, wd)
+    _call(dev, stream, where, (_lib or load_library()).splash_norm_rope,
+          _norm_desc(D, n, int(rope_lo), weight_dtype, float(eps), float(weight_offset)), rope, dtype, a, b,
+          None if positions is None else positions.data_ptr(), T)
 
 
 def splash_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, cu_q: torch.Tensor,

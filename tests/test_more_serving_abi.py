@@ -79,3 +79,53 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
         S._int32_arrays("x", cu_q=(i, (3,)))
     with pytest.raises(ValueError, match="slots"):
         S._int32_arrays("x", slots=(t[:, 0], (2,)))
+
+
+# ------------------------------------------------------------------ norm with rope
+
+def rows(**kw):
+    d = dict(x=FAKE, x_token_stride=1024, x_head_stride=128, y=FAKE << 8, y_token_stride=1024, y_head_stride=128,
+             weight=FAKE, heads=4, reserved=0)
+    d.update(kw)
+    return S.SplashNormRows(**d)
+
+
+def norm(lib, n=None, r="rope", dtype=0, q="rows", k=None, pos=FAKE, T=3, **kw):
+    d = dict(width=128, norm_dims=128, rope_lo=0, weight_dtype=0, eps=1e-6, weight_offset=0.0)
+    d.update(n or {})
+    return lib.splash_norm_rope(S.SplashNormDesc(**d), S.make_rope_desc(64) if r == "rope" else r, dtype,
+                                rows() if q == "rows" else q, k, pos, T, None)
+
+
+@pytest.mark.parametrize("n,code", [
+    (dict(width=0), INVALID), (dict(width=1025), UNSUPPORTED), (dict(norm_dims=0), INVALID), (dict(norm_dims=129), INVALID),
+    (dict(rope_lo=-1), INVALID), (dict(rope_lo=65), INVALID), (dict(weight_dtype=3), UNSUPPORTED), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(weight_offset=float("inf")), INVALID),
+    (dict(width=32, norm_dims=32), INVALID),
+])
+def test_norm_rejects_bad_descriptions(lib, n, code):
+    assert norm(lib, n) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=3), UNSUPPORTED), (dict(T=-1), INVALID), (dict(pos=0), INVALID), (dict(pos=FAKE + 2), INVALID),
+    (dict(q=None), INVALID), (dict(r=S.make_rope_desc(7)), INVALID),
+])
+def test_norm_rejects_bad_arguments(lib, kw, code):
+    assert norm(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=0), INVALID), (dict(y=0), INVALID), (dict(x=FAKE + 1), INVALID), (dict(weight=FAKE + 1), INVALID),
+    (dict(heads=-1), INVALID), (dict(reserved=1), INVALID), (dict(x_token_stride=-8), INVALID), (dict(y_head_stride=64), INVALID),
+    (dict(y_token_stride=64), INVALID), (dict(y_token_stride=256, y_head_stride=128), INVALID),
+    (dict(heads=1 << 30, y_token_stride=1 << 40), UNSUPPORTED),
+])
+def test_norm_rejects_bad_rows(lib, kw, code):
+    assert norm(lib, q=rows(**kw)) == code
+    assert norm(lib, k=rows(**kw)) == code
+
+
+def test_norm_of_nothing_is_fine(lib):
+    assert norm(lib, T=0, q=rows(x=0, y=0), pos=0) == S.SPLASH_OK
+    assert norm(lib, q=rows(heads=0, x=0), pos=0) == S.SPLASH_OK

@@ -508,6 +508,32 @@ SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, co
                                  void* workspace, size_t ws_bytes, splash_stream_t stream);
 
 /*
+ * Which keys the new tokens of splash_chunk_attn_ex see.
+ *   window, sinks   window > 0: the token at position p sees the last `window` positions up to its own,
+ *                   p + 1 - window .. p, and the first `sinks` ones.  window 0: every position up to its own (sinks is
+ *                   then unused)
+ */
+typedef struct {
+    int32_t window;
+    int32_t sinks;
+} splash_chunk_ext;
+
+/*
+ * splash_chunk_attn where T is restricted by `ext` (NULL: not):
+ *   T = {t in [tok_lo, min(tok_hi < 0 ? e : tok_hi, e)) : window == 0 or t >= e - window or t < sinks}
+ * A page that holds no token which a new token of its request sees is not needed: its table entry may be
+ * anything (splash_batch_release gives such pages back).
+ * Otherwise the same arguments, results, errors and workspace as splash_chunk_attn.
+ */
+SPLASH_API size_t splash_chunk_workspace_size_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, int total_q,
+                                                 int head_lo, int head_hi);
+SPLASH_API int splash_chunk_attn_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, const void* q,
+                                    const void* kv_pool, const int32_t* cu_q, int total_q, const int32_t* block_table,
+                                    const int32_t* ctx_lens, int head_lo, int head_hi, int64_t tok_lo, int64_t tok_hi,
+                                    int out_dtype, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                    splash_stream_t stream);
+
+/*
  * Reads the device status of a decode or chunk workspace (SPLASH_DEVICE_* bits set
  * by the most recent splash_decode_attn or splash_chunk_attn that used it; one without
  * requests or new tokens clears them): synchronises `stream`, then copies the bits to *flags (host

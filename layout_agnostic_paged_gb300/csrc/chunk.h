@@ -13,6 +13,12 @@ constexpr int kChunkKeys = 128;        // keys of one tile
 constexpr int kChunkKBlocks = 3;       // 64-dim blocks of the keys loaded and released together
 constexpr int kChunkSlotsPerPair = 8;  // partial results the workspace holds, per CTA pair
 
+// What a call's kernels are compiled for.  Each form has its own code, so that the plain one pays for nothing else.
+enum ChunkMode {
+    kChunkPlain,     // every key before a token, in one range
+    kChunkWindow     // the keys of a sliding window and some first ones
+};
+
 // How query rows are laid over the rows of CTA pairs.
 // flat: the call has all heads, so a request's (token, head) rows are consecutive rows of q and a pair
 //   takes 128 of them, wherever tokens begin (head counts that do not divide 64 waste nothing).
@@ -80,7 +86,8 @@ struct ChunkHeader {
 };
 
 // One pair's work: the rows of one token block and head group pair against key tiles
-// [t_lo, t_hi).
+// [t_lo, t_hi).  A tile is two blocks of 64 keys.  In the windowed form the first tokens' blocks and the window's
+// are counted as one sequence, with `base` between a block's number in it and its place in the context.
 struct alignas(16) ChunkItem {
     int32_t r;            // request
     int32_t tok;          // first new token (flat: of the request)
@@ -92,7 +99,7 @@ struct alignas(16) ChunkItem {
     int32_t slot;         // partial slot, or -1: the result goes to out
     int32_t ctx;          // context length (keys at or past it do not exist)
     int32_t alone;        // few row tiles share these keys: they are prefetched into L2
-    int32_t pad;
+    int32_t base;         // windowed: see above
 };
 static_assert(sizeof(ChunkItem) == 48, "ChunkItem layout");
 
@@ -116,6 +123,9 @@ struct ChunkArgs {
     int P, P_log, num_pages, max_pages, max_ctx;   // P = 2^P_log
     int past_row;         // a row of the pool's maps that does not exist: copies from there fill zeros
     int tok_lo, tok_hi;   // tok_hi: INT32_MAX for "to the end"
+    int mode;             // ChunkMode
+    int window, sinks;    // windowed: a token sees the last `window` keys up to its own, and the first `sinks`
+    int sink_blocks;      // blocks of first tokens from tok_lo's block on
     int pairs;            // CTA pairs of the grid
     ChunkTiling tile;
     int out_f32;

@@ -109,6 +109,28 @@ __device__ __forceinline__ int page_of(const ChunkArgs& a, const int32_t* table,
     return id >= 0 && id < a.num_pages ? id : -1;
 }
 
+// First key of a half of tile t.
+template <int MODE>
+__device__ __forceinline__ int tile_key(const ChunkArgs& a, const ChunkItem& it, int t, int half) {
+    if constexpr (MODE == kChunkWindow) {
+        const int b = 2 * t + half;
+        return (b + (b < a.sink_blocks ? a.tok_lo / kChunkRows : it.base)) * kChunkRows;
+    }
+    return t * kChunkKeys + half * kChunkRows;
+}
+
+// Windowed: the first key of the item's first window.  Keys [key, key + n) that lie before it and behind the
+// first tokens are seen by none of its rows: their page may be gone, and nothing of it is read.
+template <int MODE>
+__device__ __forceinline__ int window_start(const ChunkArgs& a, const ChunkItem& it) {
+    return MODE == kChunkWindow ? it.seen + it.row0 / a.Hs - a.window : 0;
+}
+template <int MODE>
+__device__ __forceinline__ bool left_behind(const ChunkArgs& a, int start, int key, int n) {
+    return MODE == kChunkWindow && key >= a.sinks && key + n <= start;
+}
+
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -168,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     static_assert(sizeof(PlanScratch) <= 9 * kBlk, "the plan's scratch fits in K's buffer");
     int2* planned = reinterpret_cast<int2*>(smem + kMiscOff + 24);
     {
-        const int2 r = plan_items(a, pair, blockIdx.x == 0, *reinterpret_cast<PlanScratch*>(smem + kKOff));
+        const int2 r = plan_items<MODE>(a, pair, blockIdx.x == 0, *reinterpret_cast<PlanScratch*>(smem + kKOff));
         if (threadIdx.x == 0) *planned = r;
     }
     fence_proxy_async_smem();
@@ -221,11 +243,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_4d(&maps.q, 0, to.x, to.y, lane);
             }
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
+            const int start = window_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 // lane k < loads looks up the page behind keys [64 c + k R, + R) of the tile
-                const int key = t * kChunkKeys + int(rank) * kChunkRows + lane * R;
+                const int key = tile_key<MODE>(a, it, t, int(rank)) + lane * R;
                 int row = a.past_row;            // past the pool: the copy fills zeros
-                if (lane < loads) {
+                if (lane < loads && !left_behind<MODE>(a, start, key, R)) {
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
                     else if (key + R > a.tok_lo && key < min(it.ctx, a.tok_hi) && !second)   // a page of the share
@@ -255,8 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // next tile's into L2, each page's rows as one run (35 requests of 3-9 tokens and 16 heads
                 // over some 10,000 keys: 117 -> 106 us; further ahead is slower, and where pairs share
                 // the keys it costs 2%).
-                const int ahead = key + kChunkKeys;
-                if (it.alone && t + 1 < it.t_hi && lane < loads && !second) {
+                const int ahead = MODE == kChunkWindow ? tile_key<MODE>(a, it, t + 1, int(rank)) + lane * R : key + kChunkKeys;
+                if (it.alone && t + 1 < it.t_hi && lane < loads && !second && !left_behind<MODE>(a, start, ahead, R)) {
                     const int id = page_of(a, table, ahead, it.ctx);
                     if (id >= 0)
                         prefetch_l2(a.kv + ((int64_t(id) << a.P_log) + (ahead & (a.P - 1))) * (kDqk * 2),
@@ -278,10 +301,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
+            const int start = window_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
-                const int key = t * kChunkKeys + lane * R;      // lane k < 2 * loads: load k of the tile
+                int key = t * kChunkKeys + lane * R;            // lane k < 2 * loads: load k of the tile
+                if (MODE == kChunkWindow) key = lane < loads ? tile_key<MODE>(a, it, t, 0) + lane * R : tile_key<MODE>(a, it, t, 1) + (lane - loads) * R;
                 int row = past;
-                if (lane < 2 * loads) {
+                if (lane < 2 * loads && !left_behind<MODE>(a, start, key, R)) {
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
                 }
@@ -302,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (cuts) {                                  // one page at most
                         const int src = __ffs(cuts) - 1;
                         const int y = __shfl_sync(0xffffffffu, row, src);
-                        const int n = it.ctx - (t * kChunkKeys + src * R);   // valid rows, 0 < n < R
+                        const int n = it.ctx - __shfl_sync(0xffffffffu, key, src);   // valid rows, 0 < n < R
                         if (lane < 4) {
                             const uint32_t d0 = sv + src * R * 512 + lane * R * 128;
                             for (int o = 0, b = 2; o < R;) {        // runs of 16, 4 and 1 rows
@@ -429,10 +454,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const ChunkItem it = items[i];
             const ChunkRow at = chunk_row(a.tile, a.Hs, it.row0, it.ntok, it.pair_group, int(rank), row);
             const int lim = at.live ? min(it.seen + at.token, a.tok_hi) : 0;      // keys [tok_lo, lim)
+            const int from = it.seen + at.token - a.window;                       // windowed: the row's first key behind the sinks
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             float m = -INFINITY, l = 0.f;        // maximum and sum (this thread's keys) of c * x
             for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
-                const int key0 = t * kChunkKeys + share * 32;
+                const int key0 = MODE == kChunkWindow ? tile_key<MODE>(a, it, t, half) + part * 32 : t * kChunkKeys + share * 32;
                 uint32_t gone = 0;               // bit k: this thread's keys k R .. have no page
                 for (int k = 0; k * R < 32; ++k)
                     if (key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
@@ -446,10 +472,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] *= sign;
                 }
-                if (gone || key0 < a.tok_lo || key0 + 32 > lim) {
+                if (gone || key0 < a.tok_lo || key0 + 32 > lim || (MODE == kChunkWindow && key0 < from && key0 + 32 > a.sinks)) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (key0 + e < a.tok_lo || key0 + e >= lim || (gone >> (e >> rlog) & 1)) x[e] = -INFINITY;
+                        if (key0 + e < a.tok_lo || key0 + e >= lim || (gone >> (e >> rlog) & 1) ||
+                            (MODE == kChunkWindow && key0 + e < from && key0 + e >= a.sinks))
+                            x[e] = -INFINITY;
                 }
                 float mx[4];
 #pragma unroll
@@ -670,10 +698,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
-    const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(chunk_attn_kernel), kSmem);
+namespace {
+
+template <int MODE>
+cudaError_t launch_mode(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
+    const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(chunk_attn_kernel<MODE>), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_attn_kernel, dim3(2 * a.pairs), dim3(kThreads), size_t(kSmem), stream, maps, a);
+    return launch_pdl(chunk_attn_kernel<MODE>, dim3(2 * a.pairs), dim3(kThreads), size_t(kSmem), stream, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
+    return a.mode == kChunkWindow ? launch_mode<kChunkWindow>(a, maps, stream) : launch_mode<kChunkPlain>(a, maps, stream);
 }
 
 }  // namespace splash

@@ -43,11 +43,22 @@ struct Span {
     bool bad_order;   // the offsets
 };
 
-__device__ __forceinline__ int key_tiles(const ChunkArgs& a, int seen) {
-    const int e = min(seen, a.tok_hi);
-    return e > a.tok_lo ? (e + kChunkKeys - 1) / kChunkKeys - a.tok_lo / kChunkKeys : 0;
+// Key tiles of a row tile whose tokens see the keys before `first` .. `last` (positions + 1).  Windowed: the blocks
+// of the first tokens, then those from the first token's window on; *base is the item's.
+template <int MODE>
+__device__ __forceinline__ int key_tiles(const ChunkArgs& a, int first, int last, int* base = nullptr) {
+    const int e = min(last, a.tok_hi);
+    if (e <= a.tok_lo) return 0;
+    if constexpr (MODE == kChunkWindow) {
+        const int b0 = a.tok_lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
+        const int w = max(b0 + a.sink_blocks, max(first - a.window, 0) / kChunkRows);
+        if (base) *base = w - a.sink_blocks;
+        return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
+    }
+    return (e + kChunkKeys - 1) / kChunkKeys - a.tok_lo / kChunkKeys;
 }
 
+template <int MODE>
 __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     Span s;
     const int c0 = a.cu_q[r], c1 = a.cu_q[r + 1], ctx = a.ctx_lens[r];
@@ -57,8 +68,23 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     s.bad_order = s.c0 != c0 || c1 != s.c0 + s.n;
     s.bad = s.bad_order || s.ctx != ctx;
     s.u = int(a.tile.row_tiles(s.n));
-    s.m = key_tiles(a, s.ctx);
+    s.m = key_tiles<kChunkPlain>(a, s.ctx, s.ctx);
+    // windowed: a row tile's windows span window + tokens - 1 keys, wherever they begin
+    if constexpr (MODE == kChunkWindow)
+        s.m = min(s.m, (a.sink_blocks + (a.window + a.tile.pair_tokens() - 1 + 126) / kChunkRows + 1) / 2);
     return s;
+}
+
+// The key tiles of all row tiles of a request, about: in a row as long as windows grow, then all the same.
+template <int MODE>
+__device__ __forceinline__ float tiles_about(const ChunkArgs& a, const Span& s) {
+    const int past = s.ctx - s.n, seen = past + min(s.n, a.tile.pair_tokens());
+    const float mean = 0.5f * float(s.m + key_tiles<MODE>(a, past + 1, seen));
+    if constexpr (MODE == kChunkWindow) {
+        const float grow = float(min(max(a.window - past, 0), s.n)) / float(s.n);
+        return float(s.u) * (grow * mean + (1.f - grow) * float(s.m));
+    }
+    return float(s.u) * mean;
 }
 
 // Over the whole block: sums of N ints and a float, and a maximum.
@@ -118,6 +144,7 @@ __device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*
 }
 
 // The row tile `tile` of request r.
+template <int MODE>
 __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s, int r, int tile, int* tiles) {
     ChunkItem it = {};
     it.r = r;
@@ -137,7 +164,7 @@ __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s,
     }
     it.ntok = s.c0 + s.n - it.tok;
     it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
-    *tiles = key_tiles(a, it.seen + last);
+    *tiles = key_tiles<MODE>(a, it.seen + it.row0 / a.Hs, it.seen + last, &it.base);
     return it;
 }
 
@@ -165,6 +192,7 @@ struct PlanScratch {
 
 // The items [x, y) of `pair`, written to the workspace's item array (by both of its CTAs, the same
 // values).  `writer`: also write the header and the split row tiles.  Called by the whole block.
+template <int MODE>
 __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool writer, PlanScratch& sh) {
     const int tid = threadIdx.x;
     constexpr int NT = kPlanThreads;
@@ -176,12 +204,13 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     Span mine = {};
     Totals<4> sum = {};
     for (int r = tid; r < a.B; r += NT) {
-        const Span s = span_of(a, r);
+        const Span s = span_of<MODE>(a, r);
         if (r == tid) mine = s;
         sum.v[0] += s.u;
-        if (s.n > 0) sum.f += 0.5f * float(s.u) * float(s.m + key_tiles(a, s.ctx - s.n + min(s.n, a.tile.pair_tokens())));
+        if (s.n > 0) sum.f += tiles_about<MODE>(a, s);
         sum.v[1] |= s.bad;
-        sum.v[2] |= s.u > 1 && int64_t(s.ctx) * (kDqk * 2) > kSharedBytes;
+        const int64_t swept = MODE == kChunkWindow ? min(int64_t(s.ctx), int64_t(a.window) + s.n) : int64_t(s.ctx);
+        sum.v[2] |= s.u > 1 && swept * (kDqk * 2) > kSharedBytes;
         sum.v[3] |= s.bad_order;
         if (s.u > 0) sum.most = max(sum.most, s.m);
     }
@@ -213,7 +242,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     if (!is_even && may_cut) {
         Totals<2 * kCuts> n = {};
         for (int r = tid; r < a.B; r += NT) {
-            const Span s = r == tid ? mine : span_of(a, r);
+            const Span s = r == tid ? mine : span_of<MODE>(a, r);
 #pragma unroll
             for (int w = 0; w < kCuts; ++w) {
                 const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
@@ -236,7 +265,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         }
     }
 
-    const int t0 = a.tok_lo / kChunkKeys;
+    const int t0 = MODE == kChunkWindow ? 0 : a.tok_lo / kChunkKeys;
     int num_splits = 0;
     int2 range;
     if (is_even) {
@@ -244,7 +273,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         ChunkItem it[kEvenTiles] = {};
         int tiles[kEvenTiles] = {}, base = 0;
         for (int r0 = 0; r0 < a.B; r0 += NT) {
-            const Span s = r0 + tid >= a.B ? Span{} : (r0 == 0 ? mine : span_of(a, r0 + tid));
+            const Span s = r0 + tid >= a.B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid));
             int v[1] = {s.u}, tot[1];
             block_scan<1>(v, tot, sh.scan1);
             sh.from[tid] = base + v[0];
@@ -255,7 +284,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 const int x = tid * kEvenTiles + e;
                 if (x >= base && x < base + tot[0]) {
                     const int k = last_at_most(sh.from, min(NT, a.B - r0), x);
-                    it[e] = row_tile(a, sh.spans[k], r0 + k, x - sh.from[k], &tiles[e]);
+                    it[e] = row_tile<MODE>(a, sh.spans[k], r0 + k, x - sh.from[k], &tiles[e]);
                 }
             }
             base += tot[0];
@@ -353,7 +382,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             Span s = {};
             int np = 1;
             if (r < a.B) {
-                s = r0 == 0 ? mine : span_of(a, r);
+                s = r0 == 0 ? mine : span_of<MODE>(a, r);
                 np = best_len == INT_MAX ? 1 : max(1, (s.m + best_len - 1) / best_len);
             }
             sh.spans[tid] = s;
@@ -375,7 +404,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 const int pc = sh.pieces[q], local = int(i) - sh.from[q];
                 const int tile = pc == 1 ? local : local / pc, piece = pc == 1 ? 0 : local % pc;
                 int tiles;
-                ChunkItem it = row_tile(a, sh.spans[q], r0 + q, tile, &tiles);
+                ChunkItem it = row_tile<MODE>(a, sh.spans[q], r0 + q, tile, &tiles);
                 it.t_lo = t0 + min(tiles, piece * sh.piece_tiles[q]);
                 it.t_hi = t0 + min(tiles, (piece + 1) * sh.piece_tiles[q]);
                 if (pc > 1) it.slot = sh.slot0[q] + local;
@@ -385,7 +414,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 for (int i = tid; i < tot[2]; i += NT) {
                     const int q = last_at_most(sh.split0, NT, i);   // (others share a start with the next split request)
                     int tiles;
-                    const ChunkItem it = row_tile(a, sh.spans[q], r0 + q, i - sh.split0[q], &tiles);
+                    const ChunkItem it = row_tile<MODE>(a, sh.spans[q], r0 + q, i - sh.split0[q], &tiles);
                     ChunkSplit sp = {};
                     sp.tok = it.tok;
                     sp.ntok = it.ntok;

@@ -611,6 +611,11 @@ bool chunk_too_long(const splash_attn_desc* d) {
     return int64_t(d->max_pages_per_req) * d->page_size > (int64_t(1) << 31) - 1024;
 }
 
+int chunk_ext_error(const splash_chunk_ext* ext) {
+    if (!ext) return SPLASH_OK;
+    return ext->window < 0 || ext->sinks < 0 ? SPLASH_ERR_INVALID_ARG : SPLASH_OK;
+}
+
 // Shape, tiling and workspace layout of a chunk call; returns its workspace bytes, 0 for a bad shape.
 size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi, ChunkArgs* a, int* sms) {
     if (validate_desc(desc) != SPLASH_OK || chunk_too_long(desc) || total_q < 0) return 0;
@@ -641,6 +646,12 @@ size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int h
 }  // namespace
 
 size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi) {
+    return splash_chunk_workspace_size_ex(desc, nullptr, total_q, head_lo, head_hi);
+}
+
+size_t splash_chunk_workspace_size_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, int total_q, int head_lo,
+                                      int head_hi) {
+    if (chunk_ext_error(ext) != SPLASH_OK) return 0;
     ChunkArgs a = {};
     int sms = 0;
     return chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
@@ -649,8 +660,17 @@ size_t splash_chunk_workspace_size(const splash_attn_desc* desc, int total_q, in
 int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool, const int32_t* cu_q,
                       int total_q, const int32_t* block_table, const int32_t* ctx_lens, int head_lo, int head_hi,
                       int64_t tok_lo, int64_t tok_hi, int out_dtype, void* out, float* lse, void* workspace,
-                      size_t ws_bytes, splash_stream_t stream_) {
-    const int st = validate_desc(desc);
+                      size_t ws_bytes, splash_stream_t stream) {
+    return splash_chunk_attn_ex(desc, nullptr, q, kv_pool, cu_q, total_q, block_table, ctx_lens, head_lo, head_hi, tok_lo,
+                                tok_hi, out_dtype, out, lse, workspace, ws_bytes, stream);
+}
+
+int splash_chunk_attn_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, const void* q, const void* kv_pool,
+                         const int32_t* cu_q, int total_q, const int32_t* block_table, const int32_t* ctx_lens, int head_lo,
+                         int head_hi, int64_t tok_lo, int64_t tok_hi, int out_dtype, void* out, float* lse, void* workspace,
+                         size_t ws_bytes, splash_stream_t stream_) {
+    int st = validate_desc(desc);
+    if (st == SPLASH_OK) st = chunk_ext_error(ext);
     if (st != SPLASH_OK) return st;
     if (total_q < 0 || head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return SPLASH_ERR_INVALID_ARG;
     if (tok_lo < 0 || (tok_hi >= 0 && tok_hi < tok_lo)) return SPLASH_ERR_INVALID_ARG;
@@ -683,6 +703,13 @@ int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* k
     a.ws = static_cast<uint8_t*>(workspace);
     a.tok_lo = int(tok_lo < most ? tok_lo : most);
     a.tok_hi = int(tok_hi >= 0 && tok_hi < most ? tok_hi : most);
+    // a window that reaches back from the last position to the first hides nothing
+    if (ext && ext->window > 0 && ext->window < a.max_ctx) {
+        a.mode = kChunkWindow;
+        a.window = ext->window;
+        a.sinks = min(ext->sinks, a.max_ctx);
+        a.sink_blocks = max(0, (a.sinks + kChunkRows - 1) / kChunkRows - a.tok_lo / kChunkRows);
+    }
     a.out_f32 = out_dtype == SPLASH_F32;
     ChunkMaps maps;
     const uint64_t row = uint64_t(kDqk) * 2;

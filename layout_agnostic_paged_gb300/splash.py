@@ -30,6 +30,7 @@ EXPORTED = ("splash_decode_workspace_size", "splash_decode_attn", "splash_decode
             "splash_lse_merge", "splash_kv_migrate", "splash_rope", "splash_kv_append",
             "splash_kv_unpack", "splash_chunk_workspace_size", "splash_chunk_attn",
             "splash_batch_tables", "splash_batch_release", "splash_norm_rope",
+            "splash_chunk_workspace_size_ex", "splash_chunk_attn_ex",
             "splash_workspace_status", "splash_status_string")
 
 SPLASH_BF16, SPLASH_F16, SPLASH_F32 = 0, 1, 2
@@ -78,6 +79,10 @@ class SplashNormRows(ctypes.Structure):
                 ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class SplashChunkExt(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -124,6 +129,11 @@ def load_library(path: str | None = None):
         lib.splash_chunk_attn.argtypes = [dp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i64, i32, vp, vp,
                                           vp, sz, vp]
         lib.splash_chunk_attn.restype = i32
+        ep = ctypes.POINTER(SplashChunkExt)
+        lib.splash_chunk_workspace_size_ex.argtypes = [dp, ep, i32, i32, i32]
+        lib.splash_chunk_workspace_size_ex.restype = sz
+        lib.splash_chunk_attn_ex.argtypes = [dp, ep, vp, vp, vp, i32, vp, vp, i32, i32, i64, i64, i32, vp, vp, vp, sz, vp]
+        lib.splash_chunk_attn_ex.restype = i32
         lib.splash_batch_tables.argtypes = [dp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
         lib.splash_batch_tables.restype = i32
         lib.splash_batch_release.argtypes = [dp, vp, vp, vp, vp, vp, i32, i32, vp]
@@ -590,23 +600,42 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
                       stream=None) -> None:
     """Causal attention of new tokens q [N][H][576] over the paged cache that holds them (see
     splash.h); writes heads [head_lo, head_hi) of out [N][H][512] (bf16 or fp32) and lse [N][H]."""
-    where = "splash_chunk_attn"
+    args, dev = _chunk_args("splash_chunk_attn", q, kv_pool, cu_q, block_table, ctx_lens, head_lo, head_hi, tok_lo,
+                            tok_hi, out, lse, workspace, scale)
+    _call(dev, stream, "splash_chunk_attn", (_lib or load_library()).splash_chunk_attn, *args)
+
+
+def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
+                         ctx_lens: torch.Tensor, head_lo: int, head_hi: int, tok_lo: int, tok_hi: int,
+                         out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, scale: float, window: int = 0,
+                         sinks: int = 0, stream=None) -> None:
+    """splash_chunk_attn whose new tokens see, with window > 0, the last `window` positions up to their own and the
+    first `sinks` ones."""
+    where = "splash_chunk_attn_ex"
+    args, dev = _chunk_args(where, q, kv_pool, cu_q, block_table, ctx_lens, head_lo, head_hi, tok_lo, tok_hi, out, lse,
+                            workspace, scale)
+    _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn_ex, args[0],
+          SplashChunkExt(int(window), int(sinks)), *args[1:])
+
+
+def _chunk_args(where: str, q, kv_pool, cu_q, block_table, ctx_lens, head_lo, head_hi, tok_lo, tok_hi, out, lse, workspace,
+                scale):
+    """The C arguments of a chunk call (ext and stream aside) and the device."""
     dev = _device_of(where, q, kv_pool, cu_q, block_table, ctx_lens, out, lse, workspace)
     B, pages = _index_arrays(where, cu_q, block_table, ctx_lens)
     desc = _chunk_desc(where, q, kv_pool, B, pages, scale)
     N, H, _ = q.shape
     out_dtype = _DTYPES.get(out.dtype)
     if out_dtype not in (SPLASH_BF16, SPLASH_F32) or lse.dtype != torch.float32:
-        raise ValueError("splash_chunk_attn: out must be bfloat16 or float32, lse float32")
+        raise ValueError(f"{where}: out must be bfloat16 or float32, lse float32")
     if out.shape != (N, H, 512) or lse.shape != (N, H):
-        raise ValueError("splash_chunk_attn: out must be [N][H][512], lse [N][H]")
+        raise ValueError(f"{where}: out must be [N][H][512], lse [N][H]")
     if not (q.is_contiguous() and kv_pool.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
             and workspace.is_contiguous()):
-        raise ValueError("splash_chunk_attn: tensors must be contiguous")
-    _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn, desc, q.data_ptr(), kv_pool.data_ptr(),
-          cu_q.data_ptr(), N, block_table.data_ptr(), ctx_lens.data_ptr(), int(head_lo), int(head_hi), int(tok_lo),
-          int(tok_hi), out_dtype, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+        raise ValueError(f"{where}: tensors must be contiguous")
+    return (desc, q.data_ptr(), kv_pool.data_ptr(), cu_q.data_ptr(), N, block_table.data_ptr(), ctx_lens.data_ptr(),
+            int(head_lo), int(head_hi), int(tok_lo), int(tok_hi), out_dtype, out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size()), dev
 
 
 def splash_workspace_status(workspace: torch.Tensor, stream=None) -> int:

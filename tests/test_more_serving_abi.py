@@ -129,3 +129,21 @@ def test_norm_rejects_bad_rows(lib, kw, code):
 def test_norm_of_nothing_is_fine(lib):
     assert norm(lib, T=0, q=rows(x=0, y=0), pos=0) == S.SPLASH_OK
     assert norm(lib, q=rows(heads=0, x=0), pos=0) == S.SPLASH_OK
+
+
+# ------------------------------------------------------------------ windowed attention
+
+def chunk_ex(lib, d, ext, n=6, lo=0, hi=8, ws_bytes=1 << 40, q=FAKE):
+    return lib.splash_chunk_attn_ex(d, ext, q, FAKE, FAKE, n, FAKE, FAKE, lo, hi, 0, -1, 0, FAKE, FAKE, FAKE, ws_bytes, None)
+
+
+def test_windowed_attention_rejects_bad_arguments(lib):
+    for w, s in ((-1, 0), (5, -1), (0, -1), (-2 ** 31, 0)):
+        assert chunk_ex(lib, desc(), S.SplashChunkExt(window=w, sinks=s)) == INVALID
+        assert lib.splash_chunk_workspace_size_ex(desc(), S.SplashChunkExt(window=w, sinks=s), 6, 0, 8) == 0
+    ok = S.SplashChunkExt(window=5, sinks=1)
+    assert chunk_ex(lib, None, ok) == INVALID
+    assert chunk_ex(lib, desc(d_qk=512), ok) == UNSUPPORTED
+    assert chunk_ex(lib, desc(), ok, q=0) == INVALID
+    assert chunk_ex(lib, desc(), ok, lo=4, hi=4) == INVALID
+    assert chunk_ex(lib, desc(), ok, n=-1) == INVALID

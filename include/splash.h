@@ -508,22 +508,40 @@ SPLASH_API int splash_chunk_attn(const splash_attn_desc* desc, const void* q, co
                                  void* workspace, size_t ws_bytes, splash_stream_t stream);
 
 /*
- * Which keys the new tokens of splash_chunk_attn_ex see.
+ * What splash_chunk_attn_ex knows about the keys that new tokens see.  All zero: nothing.
  *   window, sinks   window > 0: the token at position p sees the last `window` positions up to its own,
  *                   p + 1 - window .. p, and the first `sinks` ones.  window 0: every position up to its own (sinks is
  *                   then unused)
+ *   num_groups      G groups of requests with a common prefix, 1,024 at most; not together with a window
+ *   cu_groups       int32 [G + 1] device, ascending, 0 <= cu_groups[g] <= B: group g is the requests [cu_groups[g],
+ *                   cu_groups[g + 1]); requests outside every group share nothing
+ *   prefix_lens     int32 [G] device: the first prefix_lens[g] tokens of the group's requests are the same, and in the cache
+ *                   before their new ones.  They are read through the table of the group's first request
  */
 typedef struct {
     int32_t window;
     int32_t sinks;
+    const int32_t* cu_groups;
+    const int32_t* prefix_lens;
+    int32_t num_groups;
+    int32_t reserved; /* 0 */
 } splash_chunk_ext;
 
 /*
- * splash_chunk_attn where T is restricted by `ext` (NULL: not):
- *   T = {t in [tok_lo, min(tok_hi < 0 ? e : tok_hi, e)) : window == 0 or t >= e - window or t < sinks}
- * A page that holds no token which a new token of its request sees is not needed: its table entry may be
- * anything (splash_batch_release gives such pages back).
- * Otherwise the same arguments, results, errors and workspace as splash_chunk_attn.
+ * splash_chunk_attn with `ext` (NULL: without).
+ * Window:  T = {t in [tok_lo, min(tok_hi < 0 ? e : tok_hi, e)) : t >= e - window or t < sinks}.  A page that holds no token
+ * which a new token of its request sees is not needed: its table entry may be anything (splash_batch_release gives
+ * such pages back).
+ * Groups:  the results are those of splash_chunk_attn; where it pays, the rows of a group's requests are worked on
+ * together over the prefix, whose keys are then read and multiplied once for up to 128 of them (16 heads of 8
+ * single tokens, for instance) instead of once a request.  With 128 heads and more a token's own rows are that many,
+ * and there is nothing to gain.  Whether it pays goes by the numbers of rows and keys, so equal calls give equal bits.
+ * The prefix's entries in the tables of the group's other requests may or may not be read.  A prefix that is negative or longer than
+ * max_pages_per_req * P (clamped), or longer than the tokens that one of its requests has before its new ones (whose rows
+ * may then see all of it), and cu_groups that descend or leave [0, B] (no row is written then) set SPLASH_DEVICE_BAD_INPUT.
+ * The workspace is that of splash_chunk_workspace_size_ex, which takes num_groups from ext and reads neither of its
+ * arrays; a partial result of every 128 rows (262 KB) is kept for each request and group.
+ * Otherwise the same arguments, results and errors as splash_chunk_attn, and without groups the same workspace.
  */
 SPLASH_API size_t splash_chunk_workspace_size_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, int total_q,
                                                  int head_lo, int head_hi);

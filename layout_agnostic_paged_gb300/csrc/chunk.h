@@ -11,12 +11,14 @@ namespace splash {
 constexpr int kChunkRows = 64;         // query rows of one CTA; a pair works on 128
 constexpr int kChunkKeys = 128;        // keys of one tile
 constexpr int kChunkKBlocks = 3;       // 64-dim blocks of the keys loaded and released together
+constexpr int kChunkMaxGroups = 1024;
 constexpr int kChunkSlotsPerPair = 8;  // partial results the workspace holds, per CTA pair
 
 // What a call's kernels are compiled for.  Each form has its own code, so that the plain one pays for nothing else.
 enum ChunkMode {
     kChunkPlain,     // every key before a token, in one range
-    kChunkWindow     // the keys of a sliding window and some first ones
+    kChunkWindow,    // the keys of a sliding window and some first ones
+    kChunkGroups     // groups of requests share a prefix, which is worked on for all rows of a group at once
 };
 
 // How query rows are laid over the rows of CTA pairs.
@@ -88,6 +90,9 @@ struct ChunkHeader {
 // One pair's work: the rows of one token block and head group pair against key tiles
 // [t_lo, t_hi).  A tile is two blocks of 64 keys.  In the windowed form the first tokens' blocks and the window's
 // are counted as one sequence, with `base` between a block's number in it and its place in the context.
+// In the grouped form an item's keys begin at `base`, and a group's own item is one of all its requests' rows.
+constexpr int kItemAlone = 1;    // few row tiles share these keys: they are prefetched into L2
+constexpr int kItemPrefix = 2;   // every row sees every key up to ctx: a group's rows over its prefix
 struct alignas(16) ChunkItem {
     int32_t r;            // request
     int32_t tok;          // first new token (flat: of the request)
@@ -98,13 +103,16 @@ struct alignas(16) ChunkItem {
     int32_t t_lo, t_hi;   // key tiles
     int32_t slot;         // partial slot, or -1: the result goes to out
     int32_t ctx;          // context length (keys at or past it do not exist)
-    int32_t alone;        // few row tiles share these keys: they are prefetched into L2
-    int32_t base;         // windowed: see above
+    int32_t flags;
+    int32_t base;         // windowed, grouped: see above
 };
 static_assert(sizeof(ChunkItem) == 48, "ChunkItem layout");
 
+// A row tile whose results lie in partial slots.  pre: 0; -1 for a group's row tile, which is merged into its
+// requests' ones; n + 1 for the row tile of a request whose group's row tiles begin at split n, with rows counted
+// from row c0 of q.
 struct alignas(16) ChunkSplit {
-    int32_t tok, ntok, row0, pair_group, slot, pieces, pad[2];
+    int32_t tok, ntok, row0, pair_group, slot, pieces, pre, c0;
 };
 static_assert(sizeof(ChunkSplit) == 32, "ChunkSplit layout");
 
@@ -126,6 +134,9 @@ struct ChunkArgs {
     int mode;             // ChunkMode
     int window, sinks;    // windowed: a token sees the last `window` keys up to its own, and the first `sinks`
     int sink_blocks;      // blocks of first tokens from tok_lo's block on
+    const int32_t* cu_groups;     // grouped: [groups + 1], requests of group g from cu_groups[g] on
+    const int32_t* prefix_lens;   // [groups]
+    int groups;
     int pairs;            // CTA pairs of the grid
     ChunkTiling tile;
     int out_f32;

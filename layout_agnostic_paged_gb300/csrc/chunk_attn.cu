@@ -119,15 +119,21 @@ __device__ __forceinline__ int tile_key(const ChunkArgs& a, const ChunkItem& it,
     return t * kChunkKeys + half * kChunkRows;
 }
 
-// Windowed: the first key of the item's first window.  Keys [key, key + n) that lie before it and behind the
-// first tokens are seen by none of its rows: their page may be gone, and nothing of it is read.
+// No row of the item sees keys before it.
 template <int MODE>
-__device__ __forceinline__ int window_start(const ChunkArgs& a, const ChunkItem& it) {
-    return MODE == kChunkWindow ? it.seen + it.row0 / a.Hs - a.window : 0;
+__device__ __forceinline__ int first_key(const ChunkArgs& a, const ChunkItem& it) {
+    return MODE == kChunkGroups ? it.base : a.tok_lo;
+}
+
+// Where the keys of an item begin, the first tokens aside.  Keys [key, key + n) that lie before it are seen by none of
+// its rows: their page may be gone, and nothing of it is read.
+template <int MODE>
+__device__ __forceinline__ int item_start(const ChunkArgs& a, const ChunkItem& it) {
+    return MODE == kChunkWindow ? it.seen + it.row0 / a.Hs - a.window : (MODE == kChunkGroups ? it.base : 0);
 }
 template <int MODE>
 __device__ __forceinline__ bool left_behind(const ChunkArgs& a, int start, int key, int n) {
-    return MODE == kChunkWindow && key >= a.sinks && key + n <= start;
+    return MODE != kChunkPlain && key + n <= start && (MODE != kChunkWindow || key >= a.sinks);
 }
 
 template <int MODE>
@@ -243,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_prefetch_4d(&maps.q, 0, to.x, to.y, lane);
             }
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
-            const int start = window_start<MODE>(a, it);
+            const int start = item_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 // lane k < loads looks up the page behind keys [64 c + k R, + R) of the tile
                 const int key = tile_key<MODE>(a, it, t, int(rank)) + lane * R;
@@ -251,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane < loads && !left_behind<MODE>(a, start, key, R)) {
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
-                    else if (key + R > a.tok_lo && key < min(it.ctx, a.tok_hi) && !second)   // a page of the share
+                    else if (key + R > first_key<MODE>(a, it) && key < min(it.ctx, a.tok_hi) && !second)   // a page of the share
                         atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
                 for (int g = 0; g < kKGroups; ++g) {
@@ -279,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // over some 10,000 keys: 117 -> 106 us; further ahead is slower, and where pairs share
                 // the keys it costs 2%).
                 const int ahead = MODE == kChunkWindow ? tile_key<MODE>(a, it, t + 1, int(rank)) + lane * R : key + kChunkKeys;
-                if (it.alone && t + 1 < it.t_hi && lane < loads && !second && !left_behind<MODE>(a, start, ahead, R)) {
+                if ((it.flags & kItemAlone) && t + 1 < it.t_hi && lane < loads && !second && !left_behind<MODE>(a, start, ahead, R)) {
                     const int id = page_of(a, table, ahead, it.ctx);
                     if (id >= 0)
                         prefetch_l2(a.kv + ((int64_t(id) << a.P_log) + (ahead & (a.P - 1))) * (kDqk * 2),
@@ -301,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
-            const int start = window_start<MODE>(a, it);
+            const int start = item_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 int key = t * kChunkKeys + lane * R;            // lane k < 2 * loads: load k of the tile
                 if (MODE == kChunkWindow) key = lane < loads ? tile_key<MODE>(a, it, t, 0) + lane * R : tile_key<MODE>(a, it, t, 1) + (lane - loads) * R;
@@ -453,7 +459,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = range.x; ok && i < range.y; ++i) {
             const ChunkItem it = items[i];
             const ChunkRow at = chunk_row(a.tile, a.Hs, it.row0, it.ntok, it.pair_group, int(rank), row);
-            const int lim = at.live ? min(it.seen + at.token, a.tok_hi) : 0;      // keys [tok_lo, lim)
+            // keys [lo, lim)
+            const int lo = first_key<MODE>(a, it);
+            const bool whole = MODE == kChunkGroups && (it.flags & kItemPrefix);
+            const int lim = at.live ? min(whole ? it.ctx : it.seen + at.token, a.tok_hi) : 0;
             const int from = it.seen + at.token - a.window;                       // windowed: the row's first key behind the sinks
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             float m = -INFINITY, l = 0.f;        // maximum and sum (this thread's keys) of c * x
@@ -472,10 +481,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] *= sign;
                 }
-                if (gone || key0 < a.tok_lo || key0 + 32 > lim || (MODE == kChunkWindow && key0 < from && key0 + 32 > a.sinks)) {
+                if (gone || key0 < lo || key0 + 32 > lim || (MODE == kChunkWindow && key0 < from && key0 + 32 > a.sinks)) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (key0 + e < a.tok_lo || key0 + e >= lim || (gone >> (e >> rlog) & 1) ||
+                        if (key0 + e < lo || key0 + e >= lim || (gone >> (e >> rlog) & 1) ||
                             (MODE == kChunkWindow && key0 + e < from && key0 + e >= a.sinks))
                             x[e] = -INFINITY;
                 }
@@ -710,7 +719,11 @@ cudaError_t launch_mode(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_chunk_attn(const ChunkArgs& a, const ChunkMaps& maps, cudaStream_t stream) {
-    return a.mode == kChunkWindow ? launch_mode<kChunkWindow>(a, maps, stream) : launch_mode<kChunkPlain>(a, maps, stream);
+    switch (a.mode) {
+        case kChunkWindow: return launch_mode<kChunkWindow>(a, maps, stream);
+        case kChunkGroups: return launch_mode<kChunkGroups>(a, maps, stream);
+        default: return launch_mode<kChunkPlain>(a, maps, stream);
+    }
 }
 
 }  // namespace splash

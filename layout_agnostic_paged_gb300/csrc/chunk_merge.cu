@@ -12,18 +12,24 @@ namespace splash {
 namespace {
 
 // One row of a split row tile and Q quarters of its value dims from `quarter` on, by a warp:
-// out = sum_s w_s part_s / sum_s w_s over the pieces, as in the split combine of the decode.
-template <bool F32, int Q>
+// out = sum_s w_s part_s / sum_s w_s over the pieces, as in the split combine of the decode.  Grouped: piece s
+// is the s-th of the row's own pieces, then of those over the group's prefix, `pre` rows of slots further on.
+template <bool F32, int Q, bool GROUPS>
 __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& sp, const ChunkRow& at, int row,
-                                          int quarter, int lane) {
+                                          int quarter, int lane, int pre_pieces, int64_t pre) {
     const float* lse = reinterpret_cast<const float*>(a.ws + a.plse_off) + int64_t(sp.slot) * (2 * kChunkRows) + row;
     const float4* part = reinterpret_cast<const float4*>(a.ws + a.pout_off) +
                          (int64_t(sp.slot) * (2 * kChunkRows) + row) * (kDv / 4) + quarter * 32 + lane;
+    const int pieces = GROUPS ? sp.pieces + pre_pieces : sp.pieces;
+    // rows of slots from the first piece's row on
+    auto piece = [&](int s) -> int64_t {
+        return int64_t(s) * (2 * kChunkRows) + (GROUPS && s >= sp.pieces ? pre : int64_t(0));
+    };
     // lane s reads piece s; a NaN stays
     float m = -INFINITY;
     bool nan = false;
-    for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
-        const float x = s0 + lane < sp.pieces ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+    for (int s0 = 0; s0 < pieces; s0 += 32) {
+        const float x = s0 + lane < pieces ? lse[piece(s0 + lane)] : -INFINITY;
         nan |= __any_sync(0xffffffffu, x != x);
         m = fmaxf(m, x);
     }
@@ -33,9 +39,9 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& 
     float acc[Q][4] = {};
     float l = 0.f;
     if (m != -INFINITY)
-        for (int s0 = 0; s0 < sp.pieces; s0 += 32) {
-            const int n = min(32, sp.pieces - s0);
-            const float x = lane < n ? lse[int64_t(s0 + lane) * (2 * kChunkRows)] : -INFINITY;
+        for (int s0 = 0; s0 < pieces; s0 += 32) {
+            const int n = min(32, pieces - s0);
+            const float x = lane < n ? lse[piece(s0 + lane)] : -INFINITY;
             const float mine = x == -INFINITY ? 0.f : expf(x - m);
             float t = mine;
 #pragma unroll
@@ -46,7 +52,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& 
                 const float wt = __shfl_sync(0xffffffffu, mine, s);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const float4 v = __ldcs(part + int64_t(s0 + s) * (2 * kChunkRows * kDv / 4) + q * 32);
+                    const float4 v = __ldcs(part + piece(s0 + s) * (kDv / 4) + q * 32);
                     acc[q][0] += wt * v.x;        // (an empty piece holds zeros)
                     acc[q][1] += wt * v.y;
                     acc[q][2] += wt * v.z;
@@ -75,7 +81,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& 
 // warps idle (one token over a long context: one row tile of up to a piece per pair).  Its time is
 // a chain of loads (count and split, weights, partials), so one pass of the resident warps over the rows
 // is what counts: with quarters always, the 64 splits of drafted tokens take 10.6 us instead of 6.
-template <bool F32>
+template <bool F32, bool GROUPS>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a) {
     pdl_wait();
     const ChunkHeader* head = reinterpret_cast<const ChunkHeader*>(a.ws);
@@ -90,8 +96,28 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
         const int row = int(r % (2 * kChunkRows));
         const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, row / kChunkRows, row % kChunkRows);
         if (!at.live) continue;
-        if (parts == 4) merge_row<F32, 1>(a, sp, at, row, int(w) & 3, lane);
-        else merge_row<F32, 4>(a, sp, at, row, 0, lane);
+        int pre_pieces = 0;
+        int64_t pre = 0;
+        if (GROUPS && sp.pre != 0) {
+            if (sp.pre < 0) continue;
+            // the row among the group's, and the group's row tile that holds it
+            const int64_t rel = sp.tok + at.token - sp.c0;
+            int tile, in;
+            if (a.tile.flat) {
+                const int64_t x = rel * a.Hs + at.head;
+                tile = int(x / (2 * kChunkRows));
+                in = int(x % (2 * kChunkRows));
+            } else {                                  // one head group: more would leave one token to a pair
+                const int per = a.tile.pair_tokens(), tok = int(rel % per);
+                tile = int(rel / per);
+                in = tok / a.tile.tokens * kChunkRows + tok % a.tile.tokens * a.tile.heads + at.head;
+            }
+            const ChunkSplit& g = splits[sp.pre - 1 + tile];
+            pre_pieces = g.pieces;
+            pre = int64_t(g.slot - sp.slot - sp.pieces) * (2 * kChunkRows) + in - row;
+        }
+        if (parts == 4) merge_row<F32, 1, GROUPS>(a, sp, at, row, int(w) & 3, lane, pre_pieces, pre);
+        else merge_row<F32, 4, GROUPS>(a, sp, at, row, 0, lane, pre_pieces, pre);
     }
 }
 
@@ -101,9 +127,13 @@ size_t chunk_layout(ChunkArgs& a) {
     const int64_t tiles = (int64_t(a.max_ctx) + kChunkKeys - 1) / kChunkKeys;
     const int64_t u = a.tile.row_tiles(a.total_q) + int64_t(a.B) * a.tile.pair_groups();   // each request rounds up
     const int64_t most = int64_t(kChunkSlotsPerPair) * a.pairs;
-    const int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles);
+    int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles), more = 0;
+    if (a.mode == kChunkGroups) {        // the groups' row tiles, and a partial of every row tile
+        more = a.tile.row_tiles(a.total_q) + a.groups;
+        slots += u + more;
+    }
     a.cap_slots = int(slots);
-    a.cap_items = u + slots + a.pairs;   // a dealt plan pads the pairs to equal counts
+    a.cap_items = u + more + slots + a.pairs;   // a dealt plan pads the pairs to equal counts
     a.words_off = kChunkWordsOff;
     a.items_off = align256(a.words_off + sizeof(uint32_t) * 2 * size_t(a.pairs));
     a.splits_off = align256(a.items_off + sizeof(ChunkItem) * size_t(a.cap_items));
@@ -117,8 +147,12 @@ cudaError_t launch_chunk_combine(const ChunkArgs& a, int sms, cudaStream_t strea
     // enough blocks for every split of a small call (two slots each at least), eight a SM at most
     const int64_t want = int64_t(a.cap_slots + 1) / 2 * (2 * kChunkRows * 4 / 8);
     const int blocks = int(want < int64_t(sms) * 8 ? want : int64_t(sms) * 8);
-    if (a.out_f32) return launch_pdl(chunk_combine_kernel<true>, dim3(blocks), dim3(256), 0, stream, a);
-    return launch_pdl(chunk_combine_kernel<false>, dim3(blocks), dim3(256), 0, stream, a);
+    const dim3 g(blocks), b(256);
+    if (a.mode == kChunkGroups)
+        return a.out_f32 ? launch_pdl(chunk_combine_kernel<true, true>, g, b, 0, stream, a)
+                         : launch_pdl(chunk_combine_kernel<false, true>, g, b, 0, stream, a);
+    return a.out_f32 ? launch_pdl(chunk_combine_kernel<true, false>, g, b, 0, stream, a)
+                     : launch_pdl(chunk_combine_kernel<false, false>, g, b, 0, stream, a);
 }
 
 }  // namespace splash

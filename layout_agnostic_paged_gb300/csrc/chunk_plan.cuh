@@ -41,25 +41,49 @@ struct Span {
     int m;            // key tiles of the last token, the request's most
     bool bad;         // the length or the offsets
     bool bad_order;   // the offsets
+    // grouped: the request whose pages these are, the first key, and what becomes of the results
+    int r, lo;
+    int group;        // kOwn: a request's own keys are all it sees; kPrefix: a group's prefix; else the group
+};
+constexpr int kOwn = -1, kPrefix = -2;
+
+// The groups of a call, in shared memory.
+struct GroupScratch {
+    int cu[kChunkMaxGroups + 1];
+    int prefix[kChunkMaxGroups];   // shared keys; ~keys for a group that is not worth it
+    int split0[kChunkMaxGroups];   // first split row tile
 };
 
-// Key tiles of a row tile whose tokens see the keys before `first` .. `last` (positions + 1).  Windowed: the blocks
-// of the first tokens, then those from the first token's window on; *base is the item's.
+// The last index in [0, n) with from[i] <= x (from[0] <= x, ascending).
+__device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (from[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Key tiles of a row tile whose tokens see the keys from `lo` on before `first` .. `last` (positions + 1).  Windowed: the
+// blocks of the first tokens, then those from the first token's window on; *base is the item's.
 template <int MODE>
-__device__ __forceinline__ int key_tiles(const ChunkArgs& a, int first, int last, int* base = nullptr) {
+__device__ __forceinline__ int key_tiles(const ChunkArgs& a, int lo, int first, int last, int* base = nullptr) {
     const int e = min(last, a.tok_hi);
-    if (e <= a.tok_lo) return 0;
+    if (MODE == kChunkGroups && base) *base = lo;
+    if (e <= lo) return 0;
     if constexpr (MODE == kChunkWindow) {
-        const int b0 = a.tok_lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
+        const int b0 = lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
         const int w = max(b0 + a.sink_blocks, max(first - a.window, 0) / kChunkRows);
         if (base) *base = w - a.sink_blocks;
         return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
     }
-    return (e + kChunkKeys - 1) / kChunkKeys - a.tok_lo / kChunkKeys;
+    return (e + kChunkKeys - 1) / kChunkKeys - lo / kChunkKeys;
 }
 
+// The rows of request r.
 template <int MODE>
-__device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
+__device__ __forceinline__ Span request_span(const ChunkArgs& a, int r) {
     Span s;
     const int c0 = a.cu_q[r], c1 = a.cu_q[r + 1], ctx = a.ctx_lens[r];
     s.c0 = min(max(c0, 0), a.total_q);
@@ -68,18 +92,57 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int r) {
     s.bad_order = s.c0 != c0 || c1 != s.c0 + s.n;
     s.bad = s.bad_order || s.ctx != ctx;
     s.u = int(a.tile.row_tiles(s.n));
-    s.m = key_tiles<kChunkPlain>(a, s.ctx, s.ctx);
+    s.r = r;
+    s.lo = a.tok_lo;
+    s.group = kOwn;
+    s.m = key_tiles<kChunkPlain>(a, s.lo, s.ctx, s.ctx);
     // windowed: a row tile's windows span window + tokens - 1 keys, wherever they begin
     if constexpr (MODE == kChunkWindow)
         s.m = min(s.m, (a.sink_blocks + (a.window + a.tile.pair_tokens() - 1 + 126) / kChunkRows + 1) / 2);
     return s;
 }
 
+// The i-th of the call's runs of rows.  Grouped: the groups' prefixes come first, then the requests, whose
+// keys begin behind the prefix that they share.
+template <int MODE>
+__device__ __forceinline__ Span span_of(const ChunkArgs& a, int i, const GroupScratch& gs) {
+    if constexpr (MODE == kChunkGroups) {
+        if (i < a.groups) {
+            Span s = {};
+            s.r = gs.cu[i];
+            s.lo = a.tok_lo;
+            s.group = kPrefix;
+            if (gs.prefix[i] > 0) {
+                s.c0 = min(max(a.cu_q[s.r], 0), a.total_q);
+                s.n = min(max(a.cu_q[gs.cu[i + 1]], s.c0), a.total_q) - s.c0;
+                s.ctx = gs.prefix[i];
+                s.u = int(a.tile.row_tiles(s.n));
+                s.m = key_tiles<MODE>(a, s.lo, s.ctx, s.ctx);
+            }
+            return s;
+        }
+        const int r = i - a.groups;
+        Span s = request_span<MODE>(a, r);
+        if (s.n > 0 && r >= gs.cu[0] && r < gs.cu[a.groups]) {
+            const int g = last_at_most(gs.cu, a.groups, r), p = gs.prefix[g];
+            s.bad |= s.ctx - s.n < (p < 0 ? ~p : p);
+            if (p > 0) {
+                s.group = g;
+                s.lo = max(a.tok_lo, p);
+                s.m = key_tiles<MODE>(a, s.lo, s.ctx, s.ctx);
+            }
+        }
+        return s;
+    }
+    return request_span<MODE>(a, i);
+}
+
 // The key tiles of all row tiles of a request, about: in a row as long as windows grow, then all the same.
 template <int MODE>
 __device__ __forceinline__ float tiles_about(const ChunkArgs& a, const Span& s) {
+    if (MODE == kChunkGroups && s.group == kPrefix) return float(s.u) * float(s.m);
     const int past = s.ctx - s.n, seen = past + min(s.n, a.tile.pair_tokens());
-    const float mean = 0.5f * float(s.m + key_tiles<MODE>(a, past + 1, seen));
+    const float mean = 0.5f * float(s.m + key_tiles<MODE>(a, s.lo, past + 1, seen));
     if constexpr (MODE == kChunkWindow) {
         const float grow = float(min(max(a.window - past, 0), s.n)) / float(s.n);
         return float(s.u) * (grow * mean + (1.f - grow) * float(s.m));
@@ -143,13 +206,13 @@ __device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*
     __syncthreads();
 }
 
-// The row tile `tile` of request r.
+// The row tile `tile` of a run of rows.
 template <int MODE>
-__device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s, int r, int tile, int* tiles) {
+__device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s, int tile, int* tiles) {
     ChunkItem it = {};
-    it.r = r;
+    it.r = s.r;
     it.ctx = s.ctx;
-    it.alone = s.u <= kAlone;
+    it.flags = s.u <= kAlone ? kItemAlone : 0;
     it.slot = -1;
     int last;                                     // the tile's last token, from `tok` on
     if (a.tile.flat) {
@@ -163,20 +226,15 @@ __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s,
         last = min(s.c0 + s.n - it.tok, per_block) - 1;
     }
     it.ntok = s.c0 + s.n - it.tok;
-    it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
-    *tiles = key_tiles<MODE>(a, it.seen + it.row0 / a.Hs, it.seen + last, &it.base);
-    return it;
-}
-
-// The last index in [0, n) with from[i] <= x (from[0] <= x, ascending).
-__device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (from[mid] <= x) lo = mid;
-        else hi = mid;
+    if (MODE == kChunkGroups && s.group == kPrefix) {
+        it.seen = s.ctx;
+        it.flags |= kItemPrefix;
+        *tiles = key_tiles<MODE>(a, s.lo, s.ctx, s.ctx, &it.base);
+        return it;
     }
-    return lo;
+    it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
+    *tiles = key_tiles<MODE>(a, s.lo, it.seen + it.row0 / a.Hs, it.seen + last, &it.base);
+    return it;
 }
 
 // Shared memory of the plan (its buffers are not in use yet).
@@ -188,7 +246,69 @@ struct PlanScratch {
     int pieces[kPlanThreads], piece_tiles[kPlanThreads];
     Span spans[kPlanThreads];
     int first, last;
+    GroupScratch groups;
 };
+
+// What it gains, in key tiles, to work on the m requests of a group, n rows together, at once over their `keys` shared
+// keys: the tiles that their own row tiles would take beyond the group's, less the group's items and two partial
+// results a row.  (The merge's latency comes once a call.)
+__device__ __forceinline__ float gain_of_sharing(const ChunkArgs& a, int m, int n, int keys) {
+    if (m < 2 || n < 2) return 0.f;
+    const float own = float(m) * float(a.tile.row_tiles((n + m - 1) / m)), together = float(a.tile.row_tiles(n));
+    const float tiles = float(key_tiles<kChunkGroups>(a, a.tok_lo, keys, keys));
+    return (own - together) * tiles - kItemCost * together - kSlotCost * (own + together);
+}
+
+// Reads the groups into shared memory; returns {a length is bad, the groups are out of order} for the thread's.
+__device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh) {
+    GroupScratch& gs = sh.groups;
+    int2 bad = {0, 0};
+    for (int g = threadIdx.x; g <= a.groups; g += kPlanThreads) {
+        const int r = a.cu_groups[g];
+        gs.cu[g] = min(max(r, 0), a.B);
+        bad.y |= r != gs.cu[g];
+    }
+    __syncthreads();
+    Totals<4> gain = {};
+    for (int g = threadIdx.x; g < a.groups; g += kPlanThreads) {
+        const int r0 = gs.cu[g], r1 = gs.cu[g + 1], given = a.prefix_lens[g];
+        const int p = min(max(given, 0), a.max_ctx);
+        bad.x |= p != given;
+        bad.y |= r1 < r0;
+        const int c0 = min(max(a.cu_q[r0], 0), a.total_q), n = min(max(a.cu_q[max(r0, r1)], c0), a.total_q) - c0;
+        const float x = gain_of_sharing(a, r1 - r0, n, p);
+        gs.prefix[g] = x > 0.f ? p : ~p;
+        gain.f += fmaxf(x, 0.f);
+    }
+    block_totals(gain, sh.totals);
+    if (gain.f <= kMergeCost * float(a.pairs)) {
+        for (int g = threadIdx.x; g < a.groups; g += kPlanThreads)
+            if (gs.prefix[g] >= 0) gs.prefix[g] = ~gs.prefix[g];
+        __syncthreads();
+    }
+    return bad;
+}
+
+// The split row tile of an item whose first slot and number of pieces are given.
+template <int MODE>
+__device__ __forceinline__ ChunkSplit split_of(const ChunkArgs& a, const ChunkItem& it, int slot, int pieces, int group,
+                                               const GroupScratch& gs) {
+    ChunkSplit sp = {};
+    sp.tok = it.tok;
+    sp.ntok = it.ntok;
+    sp.row0 = it.row0;
+    sp.pair_group = it.pair_group;
+    sp.slot = slot;
+    sp.pieces = pieces;
+    if constexpr (MODE == kChunkGroups) {
+        if (group == kPrefix) sp.pre = -1;
+        if (group >= 0) {
+            sp.pre = gs.split0[group] + 1;
+            sp.c0 = a.cu_q[gs.cu[group]];
+        }
+    }
+    return sp;
+}
 
 // The items [x, y) of `pair`, written to the workspace's item array (by both of its CTAs, the same
 // values).  `writer`: also write the header and the split row tiles.  Called by the whole block.
@@ -203,13 +323,20 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     // last), the longest, whether an even cut is allowed; requests with bad values, and with bad offsets
     Span mine = {};
     Totals<4> sum = {};
-    for (int r = tid; r < a.B; r += NT) {
-        const Span s = span_of<MODE>(a, r);
+    const int B = MODE == kChunkGroups ? a.groups + a.B : a.B;     // runs of rows
+    if constexpr (MODE == kChunkGroups) {
+        const int2 bad = read_groups(a, sh);
+        sum.v[1] = bad.x;
+        sum.v[3] = bad.y;
+    }
+    for (int r = tid; r < B; r += NT) {
+        const Span s = span_of<MODE>(a, r, sh.groups);
         if (r == tid) mine = s;
         sum.v[0] += s.u;
         if (s.n > 0) sum.f += tiles_about<MODE>(a, s);
         sum.v[1] |= s.bad;
-        const int64_t swept = MODE == kChunkWindow ? min(int64_t(s.ctx), int64_t(a.window) + s.n) : int64_t(s.ctx);
+        const int64_t swept = MODE == kChunkWindow ? min(int64_t(s.ctx), int64_t(a.window) + s.n)
+                                                   : (MODE == kChunkGroups ? int64_t(s.ctx) - s.lo : int64_t(s.ctx));
         sum.v[2] |= s.u > 1 && swept * (kDqk * 2) > kSharedBytes;
         sum.v[3] |= s.bad_order;
         if (s.u > 0) sum.most = max(sum.most, s.m);
@@ -236,19 +363,19 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     // positions times pairs stay below 2^31)
     const int64_t tiles_most = int64_t(U) * longest;
     const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
-                      (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs) <= a.cap_slots &&
+                      (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
                       tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
     const bool is_even = may_cut && room && U <= kEvenTiles * NT && a.pairs <= 256 && sum.v[2] == 0 && even < best;
     if (!is_even && may_cut) {
         Totals<2 * kCuts> n = {};
-        for (int r = tid; r < a.B; r += NT) {
-            const Span s = r == tid ? mine : span_of<MODE>(a, r);
+        for (int r = tid; r < B; r += NT) {
+            const Span s = r == tid ? mine : span_of<MODE>(a, r, sh.groups);
 #pragma unroll
             for (int w = 0; w < kCuts; ++w) {
                 const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
                 const int np = max(1, (s.m + len - 1) / len);
                 n.v[w] += s.u * np;
-                if (np > 1) n.v[kCuts + w] += s.u * np;
+                if (np > 1 || (MODE == kChunkGroups && s.group != kOwn)) n.v[kCuts + w] += s.u * np;
             }
         }
         block_totals(n, sh.cuts);
@@ -271,20 +398,22 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     if (is_even) {
         // kEvenTiles consecutive row tiles per thread; from[] holds the requests' first row tiles
         ChunkItem it[kEvenTiles] = {};
-        int tiles[kEvenTiles] = {}, base = 0;
-        for (int r0 = 0; r0 < a.B; r0 += NT) {
-            const Span s = r0 + tid >= a.B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid));
+        int tiles[kEvenTiles] = {}, group[kEvenTiles], base = 0;
+        for (int r0 = 0; r0 < B; r0 += NT) {
+            const Span s = r0 + tid >= B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid, sh.groups));
             int v[1] = {s.u}, tot[1];
             block_scan<1>(v, tot, sh.scan1);
             sh.from[tid] = base + v[0];
             sh.spans[tid] = s;
+            if (MODE == kChunkGroups && r0 + tid < a.groups) sh.groups.split0[r0 + tid] = base + v[0];   // (each is split)
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < kEvenTiles; ++e) {
                 const int x = tid * kEvenTiles + e;
                 if (x >= base && x < base + tot[0]) {
-                    const int k = last_at_most(sh.from, min(NT, a.B - r0), x);
-                    it[e] = row_tile<MODE>(a, sh.spans[k], r0 + k, x - sh.from[k], &tiles[e]);
+                    const int k = last_at_most(sh.from, min(NT, B - r0), x);
+                    it[e] = row_tile<MODE>(a, sh.spans[k], x - sh.from[k], &tiles[e]);
+                    group[e] = sh.spans[k].group;
                 }
             }
             base += tot[0];
@@ -310,7 +439,9 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             const int x = int(uint32_t(j) * T / P) - A[e] - own;
             return x < kLeastPiece ? 0 : (tiles[e] - x < kLeastPiece ? tiles[e] : x);
         };
-        int packed[1] = {0}, packed_tot[1];
+        // items, partials and split row tiles
+        int sums[3] = {}, totals[3];
+        bool split_up[kEvenTiles] = {};
         int at = v[0];
 #pragma unroll
         for (int e = 0; e < kEvenTiles; ++e) {
@@ -325,18 +456,30 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             } else {
                 np[e] = 1;                        // (no key in sight: its rows become zeros)
             }
-            // items, partials and split row tiles: at most 1,024 + pairs, 2 pairs, pairs
-            packed[0] += np[e] | (np[e] > 1 ? np[e] : 0) << 12 | (np[e] > 1 ? 1 : 0) << 22;
+            split_up[e] = np[e] > 1 || (MODE == kChunkGroups && group[e] != kOwn);
+            sums[0] += np[e];
+            sums[1] += split_up[e] ? np[e] : 0;
+            sums[2] += split_up[e];
             at += tiles[e] + own;
         }
-        block_scan<1>(packed, packed_tot, sh.scan1);
+        if constexpr (MODE == kChunkGroups) {
+            block_scan<3>(sums, totals, sh.scan3);
+        } else {
+            // in one word: at most 1,024 + pairs, 2 pairs, pairs
+            int packed[1] = {sums[0] | sums[1] << 12 | sums[2] << 22}, tot[1];
+            block_scan<1>(packed, tot, sh.scan1);
+            sums[0] = packed[0] & 0xfff;
+            sums[1] = packed[0] >> 12 & 0x3ff;
+            sums[2] = packed[0] >> 22;
+            totals[2] = tot[0] >> 22;
+        }
         if (tid == 0) {
             sh.first = INT_MAX;
             sh.last = 0;
         }
         __syncthreads();
         // the items are in the order of their pairs, so a pair's are a range
-        int item = packed[0] & 0xfff, slot = packed[0] >> 12 & 0x3ff, split = packed[0] >> 22;
+        int item = sums[0], slot = sums[1], split = sums[2];
 #pragma unroll
         for (int e = 0; e < kEvenTiles; ++e) {
             if (np[e] > 0 && pair >= j0[e] && pair <= j1[e]) {
@@ -345,25 +488,17 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 if (empty ? pair == j0[e] : hi > lo) {
                     const int k = empty ? 0 : pair - j0[e] - no_first[e];
                     ChunkItem o = it[e];
-                    o.t_lo = t0 + (empty ? 0 : lo);
-                    o.t_hi = t0 + (empty ? 0 : hi);
-                    o.slot = np[e] > 1 ? slot + k : -1;
+                    const int from = MODE == kChunkGroups ? o.base / kChunkKeys : t0;
+                    o.t_lo = from + (empty ? 0 : lo);
+                    o.t_hi = from + (empty ? 0 : hi);
+                    o.slot = split_up[e] ? slot + k : -1;
                     items[item + k] = o;
                     atomicMin(&sh.first, item + k);
                     atomicMax(&sh.last, item + k + 1);
                 }
             }
-            if (np[e] > 1) {
-                if (writer) {
-                    ChunkSplit sp = {};
-                    sp.tok = it[e].tok;
-                    sp.ntok = it[e].ntok;
-                    sp.row0 = it[e].row0;
-                    sp.pair_group = it[e].pair_group;
-                    sp.slot = slot;
-                    sp.pieces = np[e];
-                    splits[split] = sp;
-                }
+            if (split_up[e]) {
+                if (writer) splits[split] = split_of<MODE>(a, it[e], slot, np[e], group[e], sh.groups);
                 slot += np[e];
                 ++split;
             }
@@ -371,29 +506,31 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         }
         __syncthreads();
         range = make_int2(sh.first < sh.last ? sh.first : 0, sh.first < sh.last ? sh.last : 0);
-        num_splits = packed_tot[0] >> 22;
+        num_splits = totals[2];
     } else {
         // item i is the (i / pairs)-th of pair i mod pairs, whose items lie next to each other
         const int per_pair = (dealt + a.pairs - 1) / a.pairs;
         const int64_t x0 = int64_t(pair) * per_pair;
         int slot_base = 0, base = 0;
-        for (int r0 = 0; r0 < a.B; r0 += NT) {
+        for (int r0 = 0; r0 < B; r0 += NT) {
             const int r = r0 + tid;
             Span s = {};
             int np = 1;
-            if (r < a.B) {
-                s = r0 == 0 ? mine : span_of<MODE>(a, r);
+            if (r < B) {
+                s = r0 == 0 ? mine : span_of<MODE>(a, r, sh.groups);
                 np = best_len == INT_MAX ? 1 : max(1, (s.m + best_len - 1) / best_len);
             }
             sh.spans[tid] = s;
             const int n = s.u * np;
-            int c[3] = {n, np > 1 ? n : 0, np > 1 ? s.u : 0}, tot[3];
+            const bool split_up = np > 1 || (MODE == kChunkGroups && r < B && s.group != kOwn);
+            int c[3] = {n, split_up ? n : 0, split_up ? s.u : 0}, tot[3];
             block_scan<3>(c, tot, sh.scan3);
             sh.from[tid] = c[0];
             sh.slot0[tid] = slot_base + c[1];
             sh.split0[tid] = c[2];
             sh.pieces[tid] = np;
             sh.piece_tiles[tid] = (s.m + np - 1) / np;
+            if (MODE == kChunkGroups && r < a.groups) sh.groups.split0[r] = num_splits + c[2];
             __syncthreads();
             // this pair's items among the batch's [base, base + tot[0])
             const int k0 = (base - pair + a.pairs - 1) / a.pairs;
@@ -404,25 +541,20 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 const int pc = sh.pieces[q], local = int(i) - sh.from[q];
                 const int tile = pc == 1 ? local : local / pc, piece = pc == 1 ? 0 : local % pc;
                 int tiles;
-                ChunkItem it = row_tile<MODE>(a, sh.spans[q], r0 + q, tile, &tiles);
-                it.t_lo = t0 + min(tiles, piece * sh.piece_tiles[q]);
-                it.t_hi = t0 + min(tiles, (piece + 1) * sh.piece_tiles[q]);
-                if (pc > 1) it.slot = sh.slot0[q] + local;
+                ChunkItem it = row_tile<MODE>(a, sh.spans[q], tile, &tiles);
+                const int from = MODE == kChunkGroups ? it.base / kChunkKeys : t0;
+                it.t_lo = from + min(tiles, piece * sh.piece_tiles[q]);
+                it.t_hi = from + min(tiles, (piece + 1) * sh.piece_tiles[q]);
+                if (pc > 1 || (MODE == kChunkGroups && sh.spans[q].group != kOwn)) it.slot = sh.slot0[q] + local;
                 items[x0 + k] = it;
             }
             if (writer)
                 for (int i = tid; i < tot[2]; i += NT) {
                     const int q = last_at_most(sh.split0, NT, i);   // (others share a start with the next split request)
                     int tiles;
-                    const ChunkItem it = row_tile<MODE>(a, sh.spans[q], r0 + q, i - sh.split0[q], &tiles);
-                    ChunkSplit sp = {};
-                    sp.tok = it.tok;
-                    sp.ntok = it.ntok;
-                    sp.row0 = it.row0;
-                    sp.pair_group = it.pair_group;
-                    sp.slot = sh.slot0[q] + (i - sh.split0[q]) * sh.pieces[q];
-                    sp.pieces = sh.pieces[q];
-                    splits[num_splits + i] = sp;
+                    const ChunkItem it = row_tile<MODE>(a, sh.spans[q], i - sh.split0[q], &tiles);
+                    splits[num_splits + i] = split_of<MODE>(a, it, sh.slot0[q] + (i - sh.split0[q]) * sh.pieces[q],
+                                                            sh.pieces[q], sh.spans[q].group, sh.groups);
                 }
             base += tot[0];
             slot_base += tot[1];

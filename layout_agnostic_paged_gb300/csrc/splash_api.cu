@@ -613,11 +613,13 @@ bool chunk_too_long(const splash_attn_desc* d) {
 
 int chunk_ext_error(const splash_chunk_ext* ext) {
     if (!ext) return SPLASH_OK;
-    return ext->window < 0 || ext->sinks < 0 ? SPLASH_ERR_INVALID_ARG : SPLASH_OK;
+    if (ext->window < 0 || ext->sinks < 0 || ext->num_groups < 0 || ext->reserved != 0) return SPLASH_ERR_INVALID_ARG;
+    return ext->num_groups > kChunkMaxGroups || (ext->num_groups > 0 && ext->window > 0) ? SPLASH_ERR_UNSUPPORTED : SPLASH_OK;
 }
 
 // Shape, tiling and workspace layout of a chunk call; returns its workspace bytes, 0 for a bad shape.
-size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int head_hi, ChunkArgs* a, int* sms) {
+size_t chunk_shape(const splash_attn_desc* desc, const splash_chunk_ext* ext, int total_q, int head_lo, int head_hi,
+                   ChunkArgs* a, int* sms) {
     if (validate_desc(desc) != SPLASH_OK || chunk_too_long(desc) || total_q < 0) return 0;
     if (head_lo < 0 || head_hi > desc->num_heads || head_lo >= head_hi) return 0;
     int dev = 0;
@@ -638,6 +640,20 @@ size_t chunk_shape(const splash_attn_desc* desc, int total_q, int head_lo, int h
     a->pairs = *sms / 2;
     a->tile = chunk_tiling(a->H, a->Hs);
     a->scale = desc->scale;
+    if (ext) {
+        // a window that reaches back from the last position to the first hides nothing, and requests whose every
+        // token fills a pair's rows have nothing to share
+        if (ext->window > 0 && ext->window < a->max_ctx) {
+            a->mode = kChunkWindow;
+            a->window = ext->window;
+            a->sinks = min(ext->sinks, a->max_ctx);
+        } else if (ext->num_groups > 0 && a->tile.pair_tokens() > 1) {
+            a->mode = kChunkGroups;
+            a->groups = ext->num_groups;
+            a->cu_groups = ext->cu_groups;
+            a->prefix_lens = ext->prefix_lens;
+        }
+    }
     const size_t bytes = chunk_layout(*a);
     if (a->cap_items >= (int64_t(1) << 31)) return 0;
     return bytes;
@@ -654,7 +670,7 @@ size_t splash_chunk_workspace_size_ex(const splash_attn_desc* desc, const splash
     if (chunk_ext_error(ext) != SPLASH_OK) return 0;
     ChunkArgs a = {};
     int sms = 0;
-    return chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
+    return chunk_shape(desc, ext, total_q, head_lo, head_hi, &a, &sms);
 }
 
 int splash_chunk_attn(const splash_attn_desc* desc, const void* q, const void* kv_pool, const int32_t* cu_q,
@@ -684,10 +700,13 @@ int splash_chunk_attn_ex(const splash_attn_desc* desc, const splash_chunk_ext* e
             !aligned(block_table, 4) || !aligned(ctx_lens, 4))
             return SPLASH_ERR_INVALID_ARG;
         if (desc->num_pages > 0 && (!kv_pool || !aligned(kv_pool, 16))) return SPLASH_ERR_INVALID_ARG;
+        if (ext && ext->num_groups > 0 && (!ext->cu_groups || !ext->prefix_lens || !aligned(ext->cu_groups, 4) ||
+                                           !aligned(ext->prefix_lens, 4)))
+            return SPLASH_ERR_INVALID_ARG;
     }
     ChunkArgs a = {};
     int sms = 0;
-    const size_t need = chunk_shape(desc, total_q, head_lo, head_hi, &a, &sms);
+    const size_t need = chunk_shape(desc, ext, total_q, head_lo, head_hi, &a, &sms);
     if (need == 0) return sms < 2 ? SPLASH_ERR_CUDA : SPLASH_ERR_UNSUPPORTED;
     if (ws_bytes < need) return SPLASH_ERR_WORKSPACE;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
@@ -703,13 +722,8 @@ int splash_chunk_attn_ex(const splash_attn_desc* desc, const splash_chunk_ext* e
     a.ws = static_cast<uint8_t*>(workspace);
     a.tok_lo = int(tok_lo < most ? tok_lo : most);
     a.tok_hi = int(tok_hi >= 0 && tok_hi < most ? tok_hi : most);
-    // a window that reaches back from the last position to the first hides nothing
-    if (ext && ext->window > 0 && ext->window < a.max_ctx) {
-        a.mode = kChunkWindow;
-        a.window = ext->window;
-        a.sinks = min(ext->sinks, a.max_ctx);
+    if (a.mode == kChunkWindow)
         a.sink_blocks = max(0, (a.sinks + kChunkRows - 1) / kChunkRows - a.tok_lo / kChunkRows);
-    }
     a.out_f32 = out_dtype == SPLASH_F32;
     ChunkMaps maps;
     const uint64_t row = uint64_t(kDqk) * 2;

@@ -80,7 +80,8 @@ class SplashNormRows(ctypes.Structure):
 
 
 class SplashChunkExt(ctypes.Structure):
-    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("cu_groups", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("num_groups", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -578,9 +579,9 @@ def _chunk_desc(where: str, q, kv_pool, B: int, pages: int, scale) -> SplashAttn
 
 
 def chunk_workspace(q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor, scale: float,
-                    head_lo: int = 0, head_hi: int | None = None) -> torch.Tensor:
-    """Allocates (with torch, on q's device) a workspace for splash_chunk_attn on q's rows; it serves
-    every later call with no more new tokens, requests and pages per request."""
+                    head_lo: int = 0, head_hi: int | None = None, num_groups: int = 0) -> torch.Tensor:
+    """Allocates (with torch, on q's device) a workspace for splash_chunk_attn and splash_chunk_attn_ex on q's
+    rows; it serves every later call with no more new tokens, requests, pages per request and groups."""
     where = "splash_chunk_workspace_size"
     dev = _device_of(where, q, kv_pool, block_table)
     if block_table.dim() != 2:
@@ -588,7 +589,8 @@ def chunk_workspace(q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.T
     desc = _chunk_desc(where, q, kv_pool, *block_table.shape, scale)
     head_hi = q.shape[1] if head_hi is None else head_hi
     with torch.cuda.device(dev):
-        n = int(load_library().splash_chunk_workspace_size(desc, q.shape[0], int(head_lo), int(head_hi)))
+        n = int(load_library().splash_chunk_workspace_size_ex(desc, SplashChunkExt(num_groups=int(num_groups)), q.shape[0],
+                                                              int(head_lo), int(head_hi)))
     if n == 0:
         raise SplashError(SPLASH_ERR_UNSUPPORTED, where)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -608,14 +610,24 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
 def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
                          ctx_lens: torch.Tensor, head_lo: int, head_hi: int, tok_lo: int, tok_hi: int,
                          out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, scale: float, window: int = 0,
-                         sinks: int = 0, stream=None) -> None:
+                         sinks: int = 0, cu_groups: torch.Tensor | None = None,
+                         prefix_lens: torch.Tensor | None = None, stream=None) -> None:
     """splash_chunk_attn whose new tokens see, with window > 0, the last `window` positions up to their own and the
-    first `sinks` ones."""
+    first `sinks` ones; or where the requests [cu_groups[g], cu_groups[g + 1]) (int32 [G + 1]) share the pages of their
+    first prefix_lens[g] (int32 [G]) tokens, which gives the same results with fewer reads and products."""
     where = "splash_chunk_attn_ex"
     args, dev = _chunk_args(where, q, kv_pool, cu_q, block_table, ctx_lens, head_lo, head_hi, tok_lo, tok_hi, out, lse,
                             workspace, scale)
-    _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn_ex, args[0],
-          SplashChunkExt(int(window), int(sinks)), *args[1:])
+    if (cu_groups is None) != (prefix_lens is None):
+        raise ValueError(f"{where}: cu_groups and prefix_lens belong together")
+    if cu_groups is None:
+        ext = SplashChunkExt(int(window), int(sinks))
+    else:
+        _device_of(where, q, cu_groups, prefix_lens)
+        G = prefix_lens.numel()
+        _int32_arrays(where, cu_groups=(cu_groups, (G + 1,)), prefix_lens=(prefix_lens, (G,)))
+        ext = SplashChunkExt(int(window), int(sinks), cu_groups.data_ptr(), prefix_lens.data_ptr(), G)
+    _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn_ex, args[0], ext, *args[1:])
 
 
 def _chunk_args(where: str, q, kv_pool, cu_q, block_table, ctx_lens, head_lo, head_hi, tok_lo, tok_hi, out, lse, workspace,

@@ -147,3 +147,13 @@ def test_windowed_attention_rejects_bad_arguments(lib):
     assert chunk_ex(lib, desc(), ok, q=0) == INVALID
     assert chunk_ex(lib, desc(), ok, lo=4, hi=4) == INVALID
     assert chunk_ex(lib, desc(), ok, n=-1) == INVALID
+
+
+def test_groups_are_checked(lib):
+    good = dict(cu_groups=FAKE, prefix_lens=FAKE, num_groups=2)
+    for kw, code in ((dict(num_groups=-1), INVALID), (dict(num_groups=1025), UNSUPPORTED), (dict(window=9), UNSUPPORTED),
+                     (dict(cu_groups=0), INVALID), (dict(prefix_lens=0), INVALID), (dict(cu_groups=FAKE + 2), INVALID),
+                     (dict(prefix_lens=FAKE + 1), INVALID), (dict(reserved=1), INVALID)):
+        assert chunk_ex(lib, desc(), S.SplashChunkExt(**{**good, **kw})) == code, kw
+    for kw in (dict(num_groups=-1), dict(num_groups=1025), dict(window=9), dict(reserved=7)):
+        assert lib.splash_chunk_workspace_size_ex(desc(), S.SplashChunkExt(**{**good, **kw}), 6, 0, 8) == 0

@@ -102,6 +102,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The low n bits, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32)); }
+
 // The page id behind a key, or -1 where there is none (past the context, or a bad id).
 __device__ __forceinline__ int page_of(const ChunkArgs& a, const int32_t* table, int key, int ctx) {
     if (key >= ctx) return -1;
@@ -481,12 +484,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] *= sign;
                 }
-                if (gone || key0 < lo || key0 + 32 > lim || (MODE == kChunkWindow && key0 < from && key0 + 32 > a.sinks)) {
+                // the keys that this row does not see, a bit each: in code this short, because a tile that needs it may be
+                // the only one of a launch, and its instructions come from memory then
+                uint32_t hidden = low_bits(lo - key0) | ~low_bits(lim - key0);
+                if (MODE == kChunkWindow) hidden |= low_bits(from - key0) & ~low_bits(a.sinks - key0);
+                if (gone) hidden |= rlog == 4 ? (gone & 1 ? 0xffffu : 0u) | (gone & 2 ? 0xffff0000u : 0u) : 0xffffffffu;
+                if (hidden) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (key0 + e < lo || key0 + e >= lim || (gone >> (e >> rlog) & 1) ||
-                            (MODE == kChunkWindow && key0 + e < from && key0 + e >= a.sinks))
-                            x[e] = -INFINITY;
+                        if (hidden >> e & 1) x[e] = -INFINITY;
                 }
                 float mx[4];
 #pragma unroll

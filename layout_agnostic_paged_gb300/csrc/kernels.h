@@ -119,6 +119,10 @@ struct NormRows {
     const void* weight;           // null: ones
     int64_t xt, xh, yt, yh;       // strides in elements
     int H;
+    // set by the launcher
+    int blocks, rows_per_block;
+    int step_tokens, step_heads;  // from a lane's row to its next, in elements too; wrap: on to the next token's heads
+    int64_t x_step, y_step, x_wrap, y_wrap;
 };
 struct NormArgs {
     NormRows q, k;                // k.H == 0: no keys
@@ -131,7 +135,6 @@ struct NormArgs {
     int weight_len;               // floats of a weight array in shared memory
     int units, rot_units, plain_units;   // of a row: two vectors each, the rotated ones first
     int G, G_log;                 // lanes of a row
-    int chunks, rows_per_block, tokens_per_block;
 };
 // vectors: pointers, strides and the parts of a row allow 16-byte vectors, whose pairs lie in one unit.
 cudaError_t launch_norm_rope(NormArgs& a, int dtype, bool interleaved, bool vectors, int sms, cudaStream_t stream);

@@ -7,8 +7,9 @@
 // HBM-bound: every element is read and written once, where a norm and a rotation one after the other move
 // it twice.  G lanes hold a row in registers: each has "units" of two vectors, and the two vectors of a
 // rotated unit are the halves of its pairs (d / 2 apart), so that no element crosses lanes and only the sum
-// of squares does.  A block owns a run of one token's rows, queries and keys alike, or all rows of a few
-// tokens where one's are few; its tokens' cos / sin and the weights lie in shared memory.
+// of squares does.  A block owns a run of one side's rows, several to a lane: a lane's place in the row, its weights and
+// its tokens' cos / sin are worked out once for all of them.  (With a block per token the kernel executed 25
+// instructions an element and was bound by their issue.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -20,9 +21,8 @@ namespace splash {
 namespace {
 
 constexpr int kNormThreads = 256;    // a block's, at most
-constexpr int kNormPairs = 256;      // cos / sin a block holds, at most (one token has 128 at most)
-template <int K>
-constexpr int norm_rows_per_lane = K == 1 ? 2 : 1;   // 32 to 64 bytes of loads in flight
+constexpr int kNormPasses = 8;       // rows of a lane one after the other, at most
+constexpr int kNormPairs = 1024;     // cos / sin a block holds, at most (one token has 128 at most)
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -30,6 +30,33 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float& d, float v) { d = v; }
+// Two at a time, where there are two.
+__device__ __forceinline__ void from_f32x2(__nv_bfloat16* d, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(d) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void from_f32x2(__half* d, float a, float b) { *reinterpret_cast<__half2*>(d) = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void from_f32x2(float* d, float a, float b) {
+    d[0] = a;
+    d[1] = b;
+}
+
+// Two fp32 products, multiply-adds or differences in one instruction.
+__device__ __forceinline__ void mul2(float* d, const float* a, float b0, float b1) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %7};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void sub2(float* d, const float* a, const float* b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tsub.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
 
 // 16 bytes, or one element.
 template <typename T, int VE>
@@ -57,29 +84,29 @@ __device__ __forceinline__ float range_scale(float ss, float eps) {
     return ss < __uint_as_float((127u - 110u) << 23) && eps < __uint_as_float((127u - 80u) << 23) ? up : 1.f;
 }
 
-// VE elements a vector, K units a lane, U rows of a lane in flight (a block has no more rows than that).
+// VE elements a vector, K units a lane.
 template <typename T, bool INTER, int VE, int K>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int U = norm_rows_per_lane<K>;
     // Weights and cos / sin in runs with gaps, so that lanes at different runs read different banks.
     constexpr int kWRun = VE >= 8 ? VE + 4 : VE;
     constexpr int RN = INTER && VE > 1 ? VE / 2 : VE;  // pairs whose cos / sin a lane reads together
-    constexpr int kCRun = RN >= 4 ? RN + 2 : RN;
-    extern __shared__ __align__(16) float sm[];        // weights of q and of k; then cos / sin
+    constexpr int kCRun = 2 * RN + (RN >= 4 ? 4 : 0);  // their cosines, then their sines
+    extern __shared__ __align__(16) float sm[];        // weights; then cos / sin
     pdl_wait();
     float* wts = sm;
-    float2* cs = reinterpret_cast<float2*>(sm + 2 * a.weight_len);
+    float* cs = sm + a.weight_len;
     const int tid = threadIdx.x, NT = blockDim.x;
-    const int t0 = blockIdx.x / a.chunks * a.tokens_per_block;
-    const int ntok = min(a.tokens_per_block, a.T - t0);
-    const int j0 = (blockIdx.x % a.chunks) * a.rows_per_block;
-    const int nrow = min(a.rows_per_block, a.q.H + a.k.H - j0);
-    const int rows = ntok * nrow;                      // of the block
+    const bool key = int(blockIdx.x) >= a.q.blocks;
+    const NormRows& side = key ? a.k : a.q;
+    const int H = side.H;
+    // rows of the side, token by token
+    const int row0 = (int(blockIdx.x) - (key ? a.q.blocks : 0)) * side.rows_per_block;
+    const int rows = min(side.rows_per_block, a.T * H - row0);      // (a side has fewer than 2^31)
+    const int t0 = row0 / H, h0 = row0 - t0 * H;
     const int lane = tid & (a.G - 1), groups = NT >> a.G_log;
     const int half = a.dims >> 1;
-    const uint64_t* turns = generic_table(a.table.turns);
 
-    // first elements of a unit's vectors; -1: none
+    // first elements of a unit's vectors (-1: none)
     int ea[K], eb[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -89,60 +116,77 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
             ea[k] = a.rope_lo + (INTER && VE == 1 ? 2 * u : u * VE);
             eb[k] = ea[k] + (INTER && VE == 1 ? 1 : half);
         } else if (u < a.units) {
+            // (the later half first: with half of a row rotated, lanes then meet in no bank of the weights)
             const int p = u - a.rot_units, other = p + a.plain_units;
-            ea[k] = p * VE < a.rope_lo ? p * VE : p * VE + a.dims;
-            if (other * VE < a.width - a.dims) eb[k] = other * VE < a.rope_lo ? other * VE : other * VE + a.dims;
+            eb[k] = p * VE < a.rope_lo ? p * VE : p * VE + a.dims;
+            if (other * VE < a.width - a.dims) ea[k] = other * VE < a.rope_lo ? other * VE : other * VE + a.dims;
         }
     }
-    alignas(16) T in[U][K][2][VE];
-    T* out[U];
-    int token[U];
-    bool key[U];
+    // the lane's next row: token and head counted from t0 and 0, and where it lies
+    int i = tid >> a.G_log, token = (h0 + i) / H, h = h0 + i - token * H;
+    const T* px = static_cast<const T*>(side.x) + int64_t(t0 + token) * side.xt + int64_t(h) * side.xh;
+    T* py = static_cast<T*>(side.y) + int64_t(t0 + token) * side.yt + int64_t(h) * side.yh;
+    struct Row {
+        alignas(16) T v[K][2][VE];
+        T* out;
+        int token;
+    };
+    auto load = [&](Row& r) {
+        r.out = nullptr;
+        if (i >= rows) return;
+        r.out = py;
+        r.token = token;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = (tid >> a.G_log) + u * groups;
-        out[u] = nullptr;
-        token[u] = 0;
-        key[u] = false;
-        if (i < rows) {
-            token[u] = ntok == 1 ? 0 : i / nrow;
-            const int j = j0 + i - token[u] * nrow;
-            key[u] = j >= a.q.H;
-            const NormRows& s = key[u] ? a.k : a.q;
-            const int h = key[u] ? j - a.q.H : j;
-            const T* x = static_cast<const T*>(s.x) + int64_t(t0 + token[u]) * s.xt + int64_t(h) * s.xh;
-            out[u] = static_cast<T*>(s.y) + int64_t(t0 + token[u]) * s.yt + int64_t(h) * s.yh;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (ea[k] >= 0) load_vec<T, VE>(in[u][k][0], x + ea[k]);
-                if (eb[k] >= 0) load_vec<T, VE>(in[u][k][1], x + eb[k]);
-            }
+        for (int k = 0; k < K; ++k) {
+            if (ea[k] >= 0) load_vec<T, VE>(r.v[k][0], px + ea[k]);
+            if (eb[k] >= 0) load_vec<T, VE>(r.v[k][1], px + eb[k]);
         }
-    }
-    // behind the loads
-    for (int i = tid; i < a.norm_dims; i += NT) {
-        const int at = i / VE * kWRun + i % VE;
-        wts[at] = a.q.weight ? weight_at(a.q.weight, a.weight_dtype, i) + a.weight_offset : 1.f;
-        wts[a.weight_len + at] = a.k.weight ? weight_at(a.k.weight, a.weight_dtype, i) + a.weight_offset : 1.f;
-    }
-    for (int i = tid; i < ntok * half; i += NT) {
-        const int tok = ntok == 1 ? 0 : i / half;
-        cs[i / RN * kCRun + i % RN] = rope_cos_sin(turns[i - tok * half], a.positions[t0 + tok], a.table.amplitude);
+        i += groups;
+        h += side.step_heads;
+        token += side.step_tokens;
+        px += side.x_step;
+        py += side.y_step;
+        if (h >= H) {
+            h -= H;
+            ++token;
+            px += side.x_wrap;
+            py += side.y_wrap;
+        }
+    };
+    Row one = {}, two = {};                            // (a lane without a vector keeps zeros)
+    load(one);
+    // behind the first loads
+    for (int j = tid; j < a.norm_dims; j += NT)
+        wts[j / VE * kWRun + j % VE] = side.weight ? weight_at(side.weight, a.weight_dtype, j) + a.weight_offset : 1.f;
+    if (half > 0) {
+        const uint64_t* turns = generic_table(a.table.turns);
+        const int pairs = ((h0 + rows - 1) / H + 1) * half;
+        for (int j = tid; j < pairs; j += NT) {
+            const int t = j / half;
+            const float2 v = rope_cos_sin(turns[j - t * half], a.positions[t0 + t], a.table.amplitude);
+            cs[j / RN * kCRun + j % RN] = v.x;
+            cs[j / RN * kCRun + j % RN + RN] = v.y;
+        }
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+
+    auto work = [&](Row& row) {
         float x[K][2][VE];
         float ss = 0.f;
         auto squares = [&]() {
-            ss = 0.f;
+            float sum[2] = {};
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if ((s ? eb[k] : ea[k]) < a.norm_dims)
+                    if ((s ? eb[k] : ea[k]) < a.norm_dims) {
+                        if constexpr (VE == 1) sum[0] = fmaf(x[k][s][0], x[k][s][0], sum[0]);
+                        else {
 #pragma unroll
-                        for (int e = 0; e < VE; ++e) ss = fmaf(x[k][s][e], x[k][s][e], ss);
+                            for (int e = 0; e < VE; e += 2) fma2(sum, &x[k][s][e], &x[k][s][e], sum);
+                        }
+                    }
+            ss = sum[0] + sum[1];
             for (int o = a.G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         };
 #pragma unroll
@@ -150,8 +194,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    x[k][s][e] = out[u] != nullptr && (s ? eb[k] : ea[k]) >= 0 ? to_f32(in[u][k][s][e]) : 0.f;
+                for (int e = 0; e < VE; ++e) x[k][s][e] = to_f32(row.v[k][s][e]);
         squares();
         const float scale = range_scale(ss, a.eps);
         if (__any_sync(0xffffffffu, scale != 1.f)) {
@@ -165,36 +208,60 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
             squares();
         }
         const float r = rsqrtf(ss * a.inv_n + a.eps * scale * scale);
-        if (out[u] == nullptr) continue;
-        const float* w = wts + (key[u] ? a.weight_len : 0);
-        const float2* turn = cs + token[u] * (half / RN * kCRun);
+        if (row.out == nullptr) return;
+        const float* turn = cs + row.token * (half / RN * kCRun);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int e0 = s ? eb[k] : ea[k];
                 if (e0 >= 0 && e0 < a.norm_dims) {
+                    alignas(16) float w[VE];
+                    const float* from = wts + e0 / VE * kWRun;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) x[k][s][e] *= r * w[e0 / VE * kWRun + e];
+                    for (int e = 0; e < VE; ++e) w[e] = from[e];
+                    if constexpr (VE == 1) x[k][s][0] *= r * w[0];
+                    else {
+#pragma unroll
+                        for (int e = 0; e < VE; e += 2) {
+                            mul2(w + e, w + e, r, r);
+                            mul2(&x[k][s][e], &x[k][s][e], w[e], w[e + 1]);
+                        }
+                    }
                 }
             }
             const int unit = lane + k * a.G;
             if (unit < a.rot_units) {
                 if constexpr (INTER && VE > 1) {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int s = 0; s < 2; ++s) {
+                        const float* t = turn + (unit + s * a.rot_units) * kCRun;
 #pragma unroll
                         for (int e = 0; e < VE; e += 2) {
-                            const float2 v = rope_rotate(x[k][s][e], x[k][s][e + 1], turn[(unit + s * a.rot_units) * kCRun + (e >> 1)]);
+                            const float2 v = rope_rotate(x[k][s][e], x[k][s][e + 1], make_float2(t[e >> 1], t[RN + (e >> 1)]));
                             x[k][s][e] = v.x;
                             x[k][s][e + 1] = v.y;
                         }
+                    }
+                } else if constexpr (VE == 1) {
+                    const float2 v = rope_rotate(x[k][0][0], x[k][1][0], make_float2(turn[unit * kCRun], turn[unit * kCRun + 1]));
+                    x[k][0][0] = v.x;
+                    x[k][1][0] = v.y;
                 } else {
+                    alignas(16) float c[VE], sn[VE];
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
-                        const float2 v = rope_rotate(x[k][0][e], x[k][1][e], turn[unit * kCRun + e]);
-                        x[k][0][e] = v.x;
-                        x[k][1][e] = v.y;
+                        c[e] = turn[unit * kCRun + e];
+                        sn[e] = turn[unit * kCRun + RN + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < VE; e += 2) {
+                        float ac[2], as[2], bs[2];
+                        mul2(ac, &x[k][0][e], c[e], c[e + 1]);
+                        mul2(as, &x[k][0][e], sn[e], sn[e + 1]);
+                        mul2(bs, &x[k][1][e], sn[e], sn[e + 1]);
+                        sub2(&x[k][0][e], ac, bs);
+                        fma2(&x[k][1][e], &x[k][1][e], c + e, as);
                     }
                 }
             }
@@ -203,39 +270,62 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
                 const int e0 = s ? eb[k] : ea[k];
                 if (e0 >= 0) {
                     alignas(16) T o[VE];
+                    if constexpr (VE == 1) from_f32(o[0], x[k][s][0]);
+                    else {
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) from_f32(o[e], x[k][s][e]);
-                    store_vec<T, VE>(out[u] + e0, o);
+                        for (int e = 0; e < VE; e += 2) from_f32x2(o + e, x[k][s][e], x[k][s][e + 1]);
+                    }
+                    store_vec<T, VE>(row.out + e0, o);
                 }
             }
         }
+    };
+    // the next row's loads are under way while one is worked on (lanes of a warp run out of rows together or
+    // keep its exchanges company)
+    for (;;) {
+        load(two);
+        work(one);
+        if (!__any_sync(0xffffffffu, two.out != nullptr)) break;
+        load(one);
+        work(two);
+        if (!__any_sync(0xffffffffu, one.out != nullptr)) break;
     }
+}
+
+// The rows of a side's blocks: one row a lane where there are few, up to kNormPasses where the blocks still fill the GPU
+// several times over.
+void plan_side(const NormArgs& a, int sms, NormRows* s) {
+    s->blocks = 0;
+    if (s->H == 0) return;
+    const int64_t rows = int64_t(a.T) * s->H;
+    const int groups = kNormThreads / a.G;
+    int64_t passes = int64_t(a.T) * (a.q.H + a.k.H) / (int64_t(sms) * 8 * groups);
+    passes = passes < 1 ? 1 : (passes > kNormPasses ? kNormPasses : passes);
+    int64_t per = passes * groups;
+    // the tokens that so many rows can touch have to fit the table
+    if (a.dims > 0) {
+        const int64_t tokens = kNormPairs / (a.dims / 2);
+        if (per > (tokens - 1) * s->H) per = (tokens - 1) * s->H;
+    }
+    s->rows_per_block = int(per < rows ? per : rows);
+    s->blocks = int((rows + s->rows_per_block - 1) / s->rows_per_block);
+    s->step_tokens = groups / s->H;
+    s->step_heads = groups % s->H;
+    s->x_step = s->step_tokens * s->xt + s->step_heads * s->xh;
+    s->y_step = s->step_tokens * s->yt + s->step_heads * s->yh;
+    s->x_wrap = s->xt - s->H * s->xh;
+    s->y_wrap = s->yt - s->H * s->yh;
 }
 
 template <typename T, bool INTER, int VE, int K>
 cudaError_t launch_units(NormArgs& a, int sms, cudaStream_t stream) {
-    constexpr int U = norm_rows_per_lane<K>;
-    const int R = a.q.H + a.k.H;
-    // rows that a block's threads hold at once; a token's rows in equal runs of at most so many
-    const int fit = kNormThreads / a.G * U;
-    a.chunks = (R + fit - 1) / fit;
-    a.rows_per_block = (R + a.chunks - 1) / a.chunks;
-    // more tokens a block where one leaves threads without work, as long as the blocks fill the GPU
-    a.tokens_per_block = 1;
-    if (a.chunks == 1) {
-        const int64_t spread = a.T / (int64_t(sms) * 4);
-        int most = fit / R;
-        if (a.dims > 0 && most > kNormPairs / (a.dims / 2)) most = kNormPairs / (a.dims / 2);
-        a.tokens_per_block = spread < 1 || most < 1 ? 1 : (spread < most ? int(spread) : most);
-    }
-    const int groups = (a.tokens_per_block * a.rows_per_block + U - 1) / U;
-    const int threads = (groups * a.G + 31) / 32 * 32;
+    plan_side(a, sms, &a.q);
+    plan_side(a, sms, &a.k);
     // (with room for the gaps between runs)
     a.weight_len = (a.norm_dims + 7) / 8 * 12;
-    const size_t smem = 2 * size_t(a.weight_len) * sizeof(float) +
-                        size_t(a.tokens_per_block) * ((a.dims / 2 + 3) / 4 * 6) * sizeof(float2);
-    const int64_t grid = (int64_t(a.T) + a.tokens_per_block - 1) / a.tokens_per_block * a.chunks;
-    return launch_pdl(norm_rope_kernel<T, INTER, VE, K>, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, stream, a);
+    const size_t smem = size_t(a.weight_len) * sizeof(float) + (a.dims > 0 ? size_t(kNormPairs) * 3 * sizeof(float) : 0);
+    return launch_pdl(norm_rope_kernel<T, INTER, VE, K>, dim3(static_cast<unsigned>(a.q.blocks + a.k.blocks)), dim3(kNormThreads),
+                      smem, stream, a);
 }
 
 template <typename T, bool INTER>

@@ -10,6 +10,8 @@
 // of squares does.  A block owns a run of one side's rows, several to a lane: a lane's place in the row, its weights and
 // its tokens' cos / sin are worked out once for all of them.  (With a block per token the kernel executed 25
 // instructions an element and was bound by their issue.)
+#include <limits.h>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -20,8 +22,9 @@
 namespace splash {
 namespace {
 
-constexpr int kNormThreads = 256;    // a block's, at most
+constexpr int kNormThreads = 128;    // a block's, at most
 constexpr int kNormPasses = 8;       // rows of a lane one after the other, at most
+constexpr int kNormUnits = 4;        // units of a lane, at most
 constexpr int kNormPairs = 1024;     // cos / sin a block holds, at most (one token has 128 at most)
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -336,18 +339,32 @@ cudaError_t launch_typed(NormArgs& a, bool vectors, int sms, cudaStream_t stream
     const int plain = (a.width - a.dims) / ve;
     a.plain_units = (plain + 1) / 2;
     a.units = a.rot_units + a.plain_units;
-    a.G_log = 0;
-    while (a.G_log < 5 && (1 << a.G_log) < a.units) ++a.G_log;
+    // lanes and units a lane: as few idle places as can be, then as few units
+    int per_lane = 16;
+    if (vectors) {
+        int best = INT_MAX;
+        for (int k = 1; k <= kNormUnits; ++k) {
+            int g = 0;
+            while (g < 5 && (k << g) < a.units) ++g;
+            if ((k << g) >= a.units && (k << g) < best) {
+                best = k << g;
+                per_lane = k;
+                a.G_log = g;
+            }
+        }
+    } else {
+        a.G_log = 0;
+        while (a.G_log < 5 && (1 << a.G_log) < a.units) ++a.G_log;
+    }
     a.G = 1 << a.G_log;
-    const int per_lane = (a.units + a.G - 1) / a.G;
     if (!vectors) return launch_units<T, INTER, 1, 16>(a, sms, stream);
     if (per_lane == 1) return launch_units<T, INTER, V16, 1>(a, sms, stream);
-    if constexpr (sizeof(T) == 4)
-        if (per_lane > 2) return launch_units<T, INTER, V16, 4>(a, sms, stream);
-    return launch_units<T, INTER, V16, 2>(a, sms, stream);
+    if (per_lane == 2) return launch_units<T, INTER, V16, 2>(a, sms, stream);
+    if (per_lane == 3) return launch_units<T, INTER, V16, 3>(a, sms, stream);
+    return launch_units<T, INTER, V16, 4>(a, sms, stream);
 }
 static_assert(kMaxNormWidth <= 2 * 16 * 32, "a row of single elements: 16 units a lane");
-static_assert(kMaxNormWidth * 4 <= 2 * 4 * 32 * 16, "a row of vectors: 4 units a lane in fp32, 2 in 16 bits");
+static_assert(kMaxNormWidth * 4 <= 2 * kNormUnits * 32 * 16, "a row of vectors");
 
 }  // namespace
 

@@ -21,6 +21,20 @@ enum ChunkMode {
     kChunkGroups     // groups of requests share a prefix, which is worked on for all rows of a group at once
 };
 
+// n / d for 0 <= n < 2^31 and a d that the host knows: a product and a shift.  (The plan is a chain of such steps, and a
+// division takes some 100 clocks, one of 64 bits some 500.)  With s = 31 + ceil(log2 d) and m = ceil(2^s / d) the
+// product is off by less than n d / 2^s < 1 / d.
+struct FastDiv {
+    uint32_t m;
+    int32_t s;
+    __host__ __device__ int operator()(int n) const { return int(uint64_t(uint32_t(n)) * m >> s); }
+};
+inline FastDiv fast_div(int d) {
+    int k = 0;
+    while ((int64_t(1) << k) < d) ++k;
+    return FastDiv{uint32_t(((uint64_t(1) << (31 + k)) + uint64_t(d) - 1) / uint64_t(d)), 31 + k};
+}
+
 // How query rows are laid over the rows of CTA pairs.
 // flat: the call has all heads, so a request's (token, head) rows are consecutive rows of q and a pair
 //   takes 128 of them, wherever tokens begin (head counts that do not divide 64 waste nothing).
@@ -32,15 +46,14 @@ struct ChunkTiling {
     int groups;   // head groups of a token block: 1 or an even number (flat: 1)
     int heads;    // heads of a group (the last may have fewer); flat: all heads
     int tokens;   // tokens of a CTA's block (flat: unused)
+    int per;      // new tokens that a pair's rows span, at most
+    FastDiv by_heads, by_per;
     __host__ __device__ int pair_groups() const { return groups == 1 ? 1 : groups / 2; }
-    // new tokens that a pair's rows span, at most
-    __host__ __device__ int pair_tokens() const {
-        return flat ? (2 * kChunkRows + heads - 1) / heads : (groups == 1 ? 2 * tokens : tokens);
-    }
-    // row tiles of n new tokens
-    __host__ __device__ int64_t row_tiles(int64_t n) const {
-        if (flat) return (n * heads + 2 * kChunkRows - 1) / (2 * kChunkRows);
-        return (n + pair_tokens() - 1) / pair_tokens() * pair_groups();
+    __host__ __device__ int pair_tokens() const { return per; }
+    // row tiles of n new tokens (n times the call's heads is below 2^31)
+    __host__ __device__ int row_tiles(int n) const {
+        if (flat) return int((uint32_t(n) * uint32_t(heads) + (2 * kChunkRows - 1)) / (2 * kChunkRows));
+        return by_per(n + per - 1) * pair_groups();
     }
     __host__ __device__ int box_rows() const { return flat ? kChunkRows : heads * tokens; }
 };
@@ -51,6 +64,9 @@ inline ChunkTiling chunk_tiling(int H, int Hs) {
     t.groups = t.flat || Hs <= kChunkRows ? 1 : 2 * ((Hs + 2 * kChunkRows - 1) / (2 * kChunkRows));
     t.heads = (Hs + t.groups - 1) / t.groups;
     t.tokens = t.flat ? 0 : kChunkRows / t.heads;
+    t.per = t.flat ? (2 * kChunkRows + t.heads - 1) / t.heads : (t.groups == 1 ? 2 * t.tokens : t.tokens);
+    t.by_heads = fast_div(t.heads);
+    t.by_per = fast_div(t.per);
     return t;
 }
 
@@ -64,11 +80,11 @@ __host__ __device__ inline ChunkRow chunk_row(const ChunkTiling& t, int Hs, int 
     ChunkRow r;
     if (t.flat) {
         const int x = row0 + cta * kChunkRows + row;
-        r.token = x / Hs;
+        r.token = t.by_heads(x);
         r.head = x - r.token * Hs;
         r.live = r.token < ntok;
     } else {
-        const int in = row / t.heads;
+        const int in = t.by_heads(row);
         r.token = in + (t.groups == 1 ? cta * t.tokens : 0);
         r.head = row - in * t.heads + (t.groups == 1 ? 0 : (2 * pair_group + cta) * t.heads);
         r.live = in < t.tokens && r.token < ntok && r.head < Hs;
@@ -138,6 +154,7 @@ struct ChunkArgs {
     const int32_t* prefix_lens;   // [groups]
     int groups;
     int pairs;            // CTA pairs of the grid
+    FastDiv by_pairs;
     ChunkTiling tile;
     int out_f32;
     float scale;

@@ -132,7 +132,7 @@ __device__ __forceinline__ int first_key(const ChunkArgs& a, const ChunkItem& it
 // its rows: their page may be gone, and nothing of it is read.
 template <int MODE>
 __device__ __forceinline__ int item_start(const ChunkArgs& a, const ChunkItem& it) {
-    return MODE == kChunkWindow ? it.seen + it.row0 / a.Hs - a.window : (MODE == kChunkGroups ? it.base : 0);
+    return MODE == kChunkWindow ? it.seen + a.tile.by_heads(it.row0) - a.window : (MODE == kChunkGroups ? it.base : 0);
 }
 template <int MODE>
 __device__ __forceinline__ bool left_behind(const ChunkArgs& a, int start, int key, int n) {
@@ -212,14 +212,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int loads = kChunkRows / R;            // loads for 64 keys
     const int rlog = R == 64 ? 6 : (R == 32 ? 5 : 4);
 
-    if (warp == 0 || (warp == 3 && R < kChunkRows)) {
+    if (warp == 0 || warp == 3) {
         // -------------------------------------------------------- Q and K loads
         // One warp issues a copy in some 90 clocks.  Pages of 16 tokens take 36 of 2 KB for a tile's keys, more
-        // than the tile's time, so for pages below 64 a second warp issues every other one.
+        // than the tile's time, so for pages below 64 a second warp issues every other one.  That warp also loads the
+        // first item's Q: one warp's copies come from HBM one after the other (24 KB in 1,000 clocks), and the first scores
+        // wait for Q and K (tiny 11.2 to 10.5 us).  Later items' Q lies in L2, and asking for it before K is faster.
         const bool second = warp == 3;
         const uint32_t sq = smem_u32(smem + kQOff), sk = smem_u32(smem + kKOff);
         int ph = 0, qph = 0;
-        bool ok = true;
+        bool ok = true, fresh = true;
         // q's box of this CTA: head and token, or the flat row
         auto q_at = [&](const ChunkItem& x) -> int2 {
             if (a.tile.flat) return make_int2(x.tok * a.H + x.row0 + int(rank) * kChunkRows, 0);
@@ -234,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (i + 1 < range.y) next = items[i + 1];
             if (it.t_lo >= it.t_hi) continue;
             const int2 at = q_at(it);
-            for (int g = 0; g < kKGroups && ok && !second; ++g) {
+            for (int g = 0; g < kKGroups && ok && second == fresh; ++g) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[g], qph ^ 1, abort_flag, status))) { ok = false; break; }
                 const uint32_t bar = map_to_rank(smem_u32(&q_full[g]), 0);
                 if (rank == 0 && lane == 0)
@@ -244,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane < kKBlks) tma_pair_4d(sq + b * kBlk, &maps.q, bar, 0, at.x, at.y, b);
             }
             if (!ok) break;
+            fresh = false;
             qph ^= 1;
             // Q of the next item comes from HBM while this one is worked on: its buffer is free only
             // when the last scores are done, and the next item's first scores wait for it
@@ -251,6 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int2 to = q_at(next);
                 tma_prefetch_4d(&maps.q, 0, to.x, to.y, lane);
             }
+            if (second && R == kChunkRows) break;
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             const int start = item_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {

@@ -101,16 +101,16 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
         if (GROUPS && sp.pre != 0) {
             if (sp.pre < 0) continue;
             // the row among the group's, and the group's row tile that holds it
-            const int64_t rel = sp.tok + at.token - sp.c0;
+            const int rel = sp.tok + at.token - sp.c0;
             int tile, in;
             if (a.tile.flat) {
-                const int64_t x = rel * a.Hs + at.head;
-                tile = int(x / (2 * kChunkRows));
-                in = int(x % (2 * kChunkRows));
+                const int x = rel * a.Hs + at.head;   // (the call's rows are fewer than 2^31)
+                tile = x / (2 * kChunkRows);
+                in = x % (2 * kChunkRows);
             } else {                                  // one head group: more would leave one token to a pair
-                const int per = a.tile.pair_tokens(), tok = int(rel % per);
-                tile = int(rel / per);
-                in = tok / a.tile.tokens * kChunkRows + tok % a.tile.tokens * a.tile.heads + at.head;
+                tile = a.tile.by_per(rel);
+                const int tok = rel - tile * a.tile.per, second = tok >= a.tile.tokens;
+                in = second * kChunkRows + (tok - second * a.tile.tokens) * a.tile.heads + at.head;
             }
             const ChunkSplit& g = splits[sp.pre - 1 + tile];
             pre_pieces = g.pieces;

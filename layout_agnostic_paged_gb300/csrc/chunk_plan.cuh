@@ -11,6 +11,10 @@
 //     and share it in L2.  Requests with long contexts are cut into equal pieces if that helps.
 // As a kernel of its own the plan took 5 us for the smallest call and 11 us for 2,561 row tiles, and
 // each call one more launch.
+//
+// The prologue's 16 warps share four schedulers, so what all of them compute alike costs its instructions four
+// times over: warps without requests sit out, and one warp alone weighs the ways (a call of 64 requests: 7,200
+// to CLOCKS_NOW clocks).
 #pragma once
 
 #include <limits.h>
@@ -91,7 +95,7 @@ __device__ __forceinline__ Span request_span(const ChunkArgs& a, int r) {
     s.ctx = min(max(ctx, 0), a.max_ctx);
     s.bad_order = s.c0 != c0 || c1 != s.c0 + s.n;
     s.bad = s.bad_order || s.ctx != ctx;
-    s.u = int(a.tile.row_tiles(s.n));
+    s.u = a.tile.row_tiles(s.n);
     s.r = r;
     s.lo = a.tok_lo;
     s.group = kOwn;
@@ -116,7 +120,7 @@ __device__ __forceinline__ Span span_of(const ChunkArgs& a, int i, const GroupSc
                 s.c0 = min(max(a.cu_q[s.r], 0), a.total_q);
                 s.n = min(max(a.cu_q[gs.cu[i + 1]], s.c0), a.total_q) - s.c0;
                 s.ctx = gs.prefix[i];
-                s.u = int(a.tile.row_tiles(s.n));
+                s.u = a.tile.row_tiles(s.n);
                 s.m = key_tiles<MODE>(a, s.lo, s.ctx, s.ctx);
             }
             return s;
@@ -150,61 +154,62 @@ __device__ __forceinline__ float tiles_about(const ChunkArgs& a, const Span& s) 
     return float(s.u) * mean;
 }
 
-// Over the whole block: sums of N ints and a float, and a maximum.
-template <int N>
+// What the choice of a plan goes by: row tiles, key tiles (about), the most of a row tile, and flags.
+constexpr uint32_t kBadLength = 1, kBadOrder = 2;
+constexpr uint32_t kFarApart = 4;         // a request's row tiles sweep more than L2 holds
 struct Totals {
-    int v[N];
+    int u, most;
     float f;
-    int most;
+    uint32_t flags;
 };
+__device__ __forceinline__ void warp_totals(Totals& x) {
+    x.u = __reduce_add_sync(0xffffffffu, x.u);
+    x.most = __reduce_max_sync(0xffffffffu, x.most);
+    x.flags = __reduce_or_sync(0xffffffffu, x.flags);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x.f += __shfl_xor_sync(0xffffffffu, x.f, o);
+}
+
+// Exclusive prefix sums of N values over the block's first `active` warps, which alone have any and get theirs;
+// totals[] get the sums everywhere.
 template <int N>
-__device__ __forceinline__ void block_totals(Totals<N>& x, Totals<N>* scratch) {
-    const int lane = threadIdx.x & 31;
-    auto warp = [&]() {
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*scratch)[N], int active) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s[N];
+    if (warp < active) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) x.v[k] = __reduce_add_sync(0xffffffffu, x.v[k]);
-        x.most = __reduce_max_sync(0xffffffffu, x.most);
+        for (int k = 0; k < N; ++k) {
+            s[k] = v[k];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x.f += __shfl_xor_sync(0xffffffffu, x.f, o);
-    };
-    warp();
-    if (lane == 0) scratch[threadIdx.x >> 5] = x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, s[k], o);
+                if (lane >= o) s[k] += x;
+            }
+            if (lane == 31) scratch[warp][k] = s[k];
+        }
+    }
     __syncthreads();
-    x = lane < int(blockDim.x >> 5) ? scratch[lane] : Totals<N>{};
-    warp();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int w = lane < active ? scratch[lane][k] : 0;
+        if (warp < active) {
+            const int own = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w += x;
+            }
+            totals[k] = __shfl_sync(0xffffffffu, w, 31);
+            v[k] = __shfl_sync(0xffffffffu, w - own, warp) + s[k] - v[k];
+        } else {
+            totals[k] = __reduce_add_sync(0xffffffffu, w);
+        }
+    }
     __syncthreads();
 }
 
-// Exclusive prefix sums of N values over the block; totals[] get the sums.
-template <int N>
-__device__ __forceinline__ void block_scan(int (&v)[N], int (&totals)[N], int (*scratch)[N]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        s[k] = v[k];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, s[k], o);
-            if (lane >= o) s[k] += x;
-        }
-        if (lane == 31) scratch[warp][k] = s[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        int w = lane < int(blockDim.x >> 5) ? scratch[lane][k] : 0;
-        const int own = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += x;
-        }
-        totals[k] = __shfl_sync(0xffffffffu, w, 31);
-        v[k] = __shfl_sync(0xffffffffu, w - own, warp) + s[k] - v[k];
-    }
-    __syncthreads();
-}
+// Warps that hold n values, one a thread.
+__device__ __forceinline__ int warps_of(int n) { return min(kPlanThreads, n + 31) >> 5; }
 
 // The row tile `tile` of a run of rows.
 template <int MODE>
@@ -218,7 +223,7 @@ __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s,
     if (a.tile.flat) {
         it.row0 = tile * (2 * kChunkRows);
         it.tok = s.c0;
-        last = min(s.n - 1, (it.row0 + 2 * kChunkRows - 1) / a.Hs);
+        last = min(s.n - 1, a.tile.by_heads(it.row0 + 2 * kChunkRows - 1));
     } else {
         const int pg = a.tile.pair_groups(), per_block = a.tile.pair_tokens();
         it.tok = s.c0 + (pg == 1 ? tile : tile / pg) * per_block;
@@ -233,14 +238,20 @@ __device__ __forceinline__ ChunkItem row_tile(const ChunkArgs& a, const Span& s,
         return it;
     }
     it.seen = s.ctx - s.n + (it.tok - s.c0) + 1;
-    *tiles = key_tiles<MODE>(a, s.lo, it.seen + it.row0 / a.Hs, it.seen + last, &it.base);
+    *tiles = key_tiles<MODE>(a, s.lo, it.seen + a.tile.by_heads(it.row0), it.seen + last, &it.base);
     return it;
 }
 
 // Shared memory of the plan (its buffers are not in use yet).
 struct PlanScratch {
-    Totals<4> totals[32];
-    Totals<2 * kCuts> cuts[32];
+    Totals totals[32];
+    int cuts[32][2 * kCuts];
+    struct {
+        int U, longest, best_len, dealt;   // row tiles; key tiles of the longest; the plan
+        int len[kCuts];                    // piece lengths to try
+        float C, best;
+        bool bad, bad_order, is_even, cuts;
+    } choice;
     int scan1[32][1], scan3[32][3];
     int from[kPlanThreads], slot0[kPlanThreads], split0[kPlanThreads];
     int pieces[kPlanThreads], piece_tiles[kPlanThreads];
@@ -269,23 +280,31 @@ __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh)
         bad.y |= r != gs.cu[g];
     }
     __syncthreads();
-    Totals<4> gain = {};
-    for (int g = threadIdx.x; g < a.groups; g += kPlanThreads) {
-        const int r0 = gs.cu[g], r1 = gs.cu[g + 1], given = a.prefix_lens[g];
-        const int p = min(max(given, 0), a.max_ctx);
-        bad.x |= p != given;
-        bad.y |= r1 < r0;
-        const int c0 = min(max(a.cu_q[r0], 0), a.total_q), n = min(max(a.cu_q[max(r0, r1)], c0), a.total_q) - c0;
-        const float x = gain_of_sharing(a, r1 - r0, n, p);
-        gs.prefix[g] = x > 0.f ? p : ~p;
-        gain.f += fmaxf(x, 0.f);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, active = warps_of(a.groups);
+    if (warp < active) {
+        Totals gain = {};
+        for (int g = threadIdx.x; g < a.groups; g += kPlanThreads) {
+            const int r0 = gs.cu[g], r1 = gs.cu[g + 1], given = a.prefix_lens[g];
+            const int p = min(max(given, 0), a.max_ctx);
+            bad.x |= p != given;
+            bad.y |= r1 < r0;
+            const int c0 = min(max(a.cu_q[r0], 0), a.total_q), n = min(max(a.cu_q[max(r0, r1)], c0), a.total_q) - c0;
+            const float x = gain_of_sharing(a, r1 - r0, n, p);
+            gs.prefix[g] = x > 0.f ? p : ~p;
+            gain.f += fmaxf(x, 0.f);
+        }
+        warp_totals(gain);
+        if (lane == 0) sh.totals[warp].f = gain.f;
     }
-    block_totals(gain, sh.totals);
-    if (gain.f <= kMergeCost * float(a.pairs)) {
-        for (int g = threadIdx.x; g < a.groups; g += kPlanThreads)
-            if (gs.prefix[g] >= 0) gs.prefix[g] = ~gs.prefix[g];
-        __syncthreads();
+    __syncthreads();
+    if (warp < active) {
+        float gain = 0.f;
+        for (int w = 0; w < active; ++w) gain += sh.totals[w].f;
+        if (gain <= kMergeCost * float(a.pairs))
+            for (int g = threadIdx.x; g < a.groups; g += kPlanThreads)
+                if (gs.prefix[g] >= 0) gs.prefix[g] = ~gs.prefix[g];
     }
+    __syncthreads();
     return bad;
 }
 
@@ -322,75 +341,119 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     // all the row tiles, all their key tiles (a row tile's are about the mean of its request's first and
     // last), the longest, whether an even cut is allowed; requests with bad values, and with bad offsets
     Span mine = {};
-    Totals<4> sum = {};
     const int B = MODE == kChunkGroups ? a.groups + a.B : a.B;     // runs of rows
-    if constexpr (MODE == kChunkGroups) {
-        const int2 bad = read_groups(a, sh);
-        sum.v[1] = bad.x;
-        sum.v[3] = bad.y;
+    const int lane = tid & 31, warp = tid >> 5, active = warps_of(B);
+    int2 bad = {0, 0};
+    if constexpr (MODE == kChunkGroups) bad = read_groups(a, sh);
+    if (warp < active) {
+        Totals sum = {};
+        sum.flags = (bad.x ? kBadLength : 0) | (bad.y ? kBadOrder : 0);
+        for (int r = tid; r < B; r += NT) {
+            const Span s = span_of<MODE>(a, r, sh.groups);
+            if (r == tid) mine = s;
+            sum.u += s.u;
+            if (s.n > 0) sum.f += tiles_about<MODE>(a, s);
+            sum.flags |= (s.bad ? kBadLength : 0) | (s.bad_order ? kBadOrder : 0);
+            const int64_t swept = MODE == kChunkWindow ? min(int64_t(s.ctx), int64_t(a.window) + s.n)
+                                                       : (MODE == kChunkGroups ? int64_t(s.ctx) - s.lo : int64_t(s.ctx));
+            if (s.u > 1 && swept * (kDqk * 2) > kSharedBytes) sum.flags |= kFarApart;
+            if (s.u > 0) sum.most = max(sum.most, s.m);
+        }
+        warp_totals(sum);
+        if (lane == 0) sh.totals[warp] = sum;
     }
-    for (int r = tid; r < B; r += NT) {
-        const Span s = span_of<MODE>(a, r, sh.groups);
-        if (r == tid) mine = s;
-        sum.v[0] += s.u;
-        if (s.n > 0) sum.f += tiles_about<MODE>(a, s);
-        sum.v[1] |= s.bad;
-        const int64_t swept = MODE == kChunkWindow ? min(int64_t(s.ctx), int64_t(a.window) + s.n)
-                                                   : (MODE == kChunkGroups ? int64_t(s.ctx) - s.lo : int64_t(s.ctx));
-        sum.v[2] |= s.u > 1 && swept * (kDqk * 2) > kSharedBytes;
-        sum.v[3] |= s.bad_order;
-        if (s.u > 0) sum.most = max(sum.most, s.m);
+    __syncthreads();
+    if (warp == 0) {
+        Totals sum = lane < active ? sh.totals[lane] : Totals{};
+        warp_totals(sum);
+        const int U = sum.u, longest = sum.most;
+        const float C = sum.f, G = float(a.pairs);
+        const float ideal = (C + kItemCost * float(U)) / G;
+        const float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
+        const bool may_cut = a.cap_slots > 0 && U > 0 && best > 1.02f * ideal + kMergeCost;
+        // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
+        const float even = ideal + kItemCost + 2.f * G * kSlotCost + kMergeCost;
+        // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles;
+        // positions times pairs stay below 2^31)
+        const int64_t tiles_most = int64_t(U) * longest;
+        const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
+                          (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
+                          tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
+        const bool is_even = may_cut && room && U <= kEvenTiles * NT && a.pairs <= 256 && !(sum.flags & kFarApart) && even < best;
+        if (lane < kCuts) sh.choice.len[lane] = max(1, int(ceilf(C / (G * float(lane + 1)))));
+        if (lane == 0) {
+            sh.choice.U = U;
+            sh.choice.longest = longest;
+            sh.choice.best_len = INT_MAX;
+            sh.choice.dealt = U;                   // the items of a dealt plan
+            sh.choice.C = C;
+            sh.choice.best = best;
+            sh.choice.bad = (sum.flags & kBadLength) != 0;
+            sh.choice.bad_order = (sum.flags & kBadOrder) != 0;
+            sh.choice.is_even = is_even;
+            sh.choice.cuts = may_cut && !is_even;
+        }
     }
-    block_totals(sum, sh.totals);
+    __syncthreads();
     // Requests whose rows overlap could ask for more items than there is room for, so offsets out of order
     // leave the whole call without work.
-    if (sum.v[3]) {
+    if (sh.choice.bad_order) {
         if (writer && tid == 0)
             *reinterpret_cast<ChunkHeader*>(a.ws) = ChunkHeader{SPLASH_DEVICE_BAD_INPUT, kChunkMagic, 0, 2 * a.pairs};
         return make_int2(0, 0);
     }
-    const int U = sum.v[0], longest = sum.most;
-    const float C = sum.f;
-
-    const float G = float(a.pairs);
-    const float ideal = (C + kItemCost * float(U)) / G;
-    int best_len = INT_MAX, dealt = U;            // the items of a dealt plan
-    float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
-    const bool may_cut = a.cap_slots > 0 && U > 0 && best > 1.02f * ideal + kMergeCost;
-    // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
-    const float even = ideal + kItemCost + 2.f * G * kSlotCost + kMergeCost;
-    // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles;
-    // positions times pairs stay below 2^31)
-    const int64_t tiles_most = int64_t(U) * longest;
-    const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
-                      (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
-                      tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
-    const bool is_even = may_cut && room && U <= kEvenTiles * NT && a.pairs <= 256 && sum.v[2] == 0 && even < best;
-    if (!is_even && may_cut) {
-        Totals<2 * kCuts> n = {};
-        for (int r = tid; r < B; r += NT) {
-            const Span s = r == tid ? mine : span_of<MODE>(a, r, sh.groups);
+    if (sh.choice.cuts) {
+        if (warp < active) {
+            int n[2 * kCuts] = {};
+            for (int r = tid; r < B; r += NT) {
+                const Span s = r == tid ? mine : span_of<MODE>(a, r, sh.groups);
+#pragma unroll
+                for (int w = 0; w < kCuts; ++w) {
+                    const int len = sh.choice.len[w];
+                    const int np = max(1, (s.m + len - 1) / len);
+                    n[w] += s.u * np;
+                    if (np > 1 || (MODE == kChunkGroups && s.group != kOwn)) n[kCuts + w] += s.u * np;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < 2 * kCuts; ++w) {
+                n[w] = __reduce_add_sync(0xffffffffu, n[w]);
+                if (lane == w) sh.cuts[warp][w] = n[w];
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane w: the w-th piece length
+            const float C = sh.choice.C, G = float(a.pairs);
+            int items_n = 0, slots_n = 0;
+            if (lane < kCuts)
+                for (int w = 0; w < active; ++w) {
+                    items_n += sh.cuts[w][lane];
+                    slots_n += sh.cuts[w][kCuts + lane];
+                }
+            const int len = sh.choice.len[lane & (kCuts - 1)];
+            const float cost = fmaxf(float(len) + kItemCost, ceilf(float(items_n) / G) * (C / float(items_n) + kItemCost)) +
+                               float(slots_n) * kSlotCost + kMergeCost;
+            const bool fits = lane < kCuts && len < sh.choice.longest && slots_n <= a.cap_slots;
+            float best = sh.choice.best;
+            int at = -1;
 #pragma unroll
             for (int w = 0; w < kCuts; ++w) {
-                const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
-                const int np = max(1, (s.m + len - 1) / len);
-                n.v[w] += s.u * np;
-                if (np > 1 || (MODE == kChunkGroups && s.group != kOwn)) n.v[kCuts + w] += s.u * np;
+                const float c = __shfl_sync(0xffffffffu, cost, w);
+                if (__shfl_sync(0xffffffffu, int(fits), w) && c < best) {
+                    best = c;
+                    at = w;
+                }
+            }
+            if (lane == at) {
+                sh.choice.best_len = len;
+                sh.choice.dealt = items_n;
             }
         }
-        block_totals(n, sh.cuts);
-#pragma unroll
-        for (int w = 0; w < kCuts; ++w) {
-            const int len = max(1, int(ceilf(C / (G * float(w + 1)))));
-            const float cost = fmaxf(float(len) + kItemCost, ceilf(float(n.v[w]) / G) * (C / float(n.v[w]) + kItemCost)) +
-                               float(n.v[kCuts + w]) * kSlotCost + kMergeCost;
-            if (len < longest && n.v[kCuts + w] <= a.cap_slots && cost < best) {
-                best = cost;
-                best_len = len;
-                dealt = n.v[w];
-            }
-        }
+        __syncthreads();
     }
+    const int U = sh.choice.U, best_len = sh.choice.best_len, dealt = sh.choice.dealt;
+    const bool is_even = sh.choice.is_even, bad_input = sh.choice.bad;
 
     const int t0 = MODE == kChunkWindow ? 0 : a.tok_lo / kChunkKeys;
     int num_splits = 0;
@@ -402,7 +465,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         for (int r0 = 0; r0 < B; r0 += NT) {
             const Span s = r0 + tid >= B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid, sh.groups));
             int v[1] = {s.u}, tot[1];
-            block_scan<1>(v, tot, sh.scan1);
+            block_scan<1>(v, tot, sh.scan1, warps_of(B - r0));
             sh.from[tid] = base + v[0];
             sh.spans[tid] = s;
             if (MODE == kChunkGroups && r0 + tid < a.groups) sh.groups.split0[r0 + tid] = base + v[0];   // (each is split)
@@ -422,10 +485,11 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         // positions along the sequence in tiles, an item's own cost included: pair j's run is
         // [j T / P, (j + 1) T / P), and a row tile's tiles lie at [A + own, A + own + tiles)
         const int own = int(kItemCost);
+        const int holders = warps_of((U + kEvenTiles - 1) / kEvenTiles);
         int v[1] = {0}, W[1];
 #pragma unroll
         for (int e = 0; e < kEvenTiles; ++e) v[0] += tid * kEvenTiles + e < U ? tiles[e] + own : 0;
-        block_scan<1>(v, W, sh.scan1);
+        block_scan<1>(v, W, sh.scan1, holders);
         // Runs are own + kLeastPiece long at least, so that only one boundary can fall on a row tile's own
         // cost and first tiles, and one on its last: only its first and last piece can come out too
         // short, and then go to their neighbours.
@@ -463,11 +527,11 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             at += tiles[e] + own;
         }
         if constexpr (MODE == kChunkGroups) {
-            block_scan<3>(sums, totals, sh.scan3);
+            block_scan<3>(sums, totals, sh.scan3, holders);
         } else {
             // in one word: at most 1,024 + pairs, 2 pairs, pairs
             int packed[1] = {sums[0] | sums[1] << 12 | sums[2] << 22}, tot[1];
-            block_scan<1>(packed, tot, sh.scan1);
+            block_scan<1>(packed, tot, sh.scan1, holders);
             sums[0] = packed[0] & 0xfff;
             sums[1] = packed[0] >> 12 & 0x3ff;
             sums[2] = packed[0] >> 22;
@@ -509,7 +573,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         num_splits = totals[2];
     } else {
         // item i is the (i / pairs)-th of pair i mod pairs, whose items lie next to each other
-        const int per_pair = (dealt + a.pairs - 1) / a.pairs;
+        const int per_pair = a.by_pairs(dealt + a.pairs - 1);
         const int64_t x0 = int64_t(pair) * per_pair;
         int slot_base = 0, base = 0;
         for (int r0 = 0; r0 < B; r0 += NT) {
@@ -523,21 +587,28 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             sh.spans[tid] = s;
             const int n = s.u * np;
             const bool split_up = np > 1 || (MODE == kChunkGroups && r < B && s.group != kOwn);
-            int c[3] = {n, split_up ? n : 0, split_up ? s.u : 0}, tot[3];
-            block_scan<3>(c, tot, sh.scan3);
+            int c[3] = {n, split_up ? n : 0, split_up ? s.u : 0}, tot[3] = {};
+            if (MODE != kChunkGroups && best_len == INT_MAX) {
+                int one[1] = {n}, sum[1];                        // nothing is split
+                block_scan<1>(one, sum, sh.scan1, warps_of(B - r0));
+                c[0] = one[0];
+                tot[0] = sum[0];
+            } else {
+                block_scan<3>(c, tot, sh.scan3, warps_of(B - r0));
+            }
             sh.from[tid] = c[0];
             sh.slot0[tid] = slot_base + c[1];
             sh.split0[tid] = c[2];
             sh.pieces[tid] = np;
-            sh.piece_tiles[tid] = (s.m + np - 1) / np;
+            sh.piece_tiles[tid] = np == 1 ? s.m : (s.m + np - 1) / np;
             if (MODE == kChunkGroups && r < a.groups) sh.groups.split0[r] = num_splits + c[2];
             __syncthreads();
             // this pair's items among the batch's [base, base + tot[0])
-            const int k0 = (base - pair + a.pairs - 1) / a.pairs;
+            const int k0 = a.by_pairs(base - pair + a.pairs - 1);
             for (int k = (k0 > 0 ? k0 : 0) + tid;; k += NT) {
                 const int64_t i = int64_t(k) * a.pairs + pair - base;
                 if (i >= tot[0]) break;
-                const int q = last_at_most(sh.from, NT, int(i));
+                const int q = last_at_most(sh.from, min(NT, B - r0), int(i));
                 const int pc = sh.pieces[q], local = int(i) - sh.from[q];
                 const int tile = pc == 1 ? local : local / pc, piece = pc == 1 ? 0 : local % pc;
                 int tiles;
@@ -550,7 +621,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             }
             if (writer)
                 for (int i = tid; i < tot[2]; i += NT) {
-                    const int q = last_at_most(sh.split0, NT, i);   // (others share a start with the next split request)
+                    const int q = last_at_most(sh.split0, min(NT, B - r0), i);   // (others share a start with the next split request)
                     int tiles;
                     const ChunkItem it = row_tile<MODE>(a, sh.spans[q], i - sh.split0[q], &tiles);
                     splits[num_splits + i] = split_of<MODE>(a, it, sh.slot0[q] + (i - sh.split0[q]) * sh.pieces[q],
@@ -561,12 +632,12 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             num_splits += tot[2];
             __syncthreads();
         }
-        const int64_t y0 = x0 + (base - pair + a.pairs - 1) / a.pairs;
+        const int64_t y0 = x0 + a.by_pairs(base - pair + a.pairs - 1);
         range = make_int2(int(x0), int(y0));
     }
     if (writer && tid == 0) {
         ChunkHeader* head = reinterpret_cast<ChunkHeader*>(a.ws);
-        head->status = sum.v[1] ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
+        head->status = bad_input ? uint32_t(SPLASH_DEVICE_BAD_INPUT) : 0u;
         head->magic = kChunkMagic;
         head->num_splits = num_splits;
         head->words = 2 * a.pairs;

@@ -638,6 +638,7 @@ size_t chunk_shape(const splash_attn_desc* desc, const splash_chunk_ext* ext, in
     a->max_ctx = desc->max_pages_per_req * desc->page_size;
     a->past_row = desc->num_pages > 0 ? desc->num_pages * desc->page_size : 1;
     a->pairs = *sms / 2;
+    a->by_pairs = fast_div(a->pairs);
     a->tile = chunk_tiling(a->H, a->Hs);
     a->scale = desc->scale;
     if (ext) {

@@ -101,6 +101,7 @@ struct ChunkHeader {
     uint32_t magic;
     int32_t num_splits;   // row tiles cut into several items
     int32_t words;        // status words
+    int32_t split_rows;   // grouped: rows of a request's row tile, at most
 };
 
 // One pair's work: the rows of one token block and head group pair against key tiles

@@ -88,12 +88,26 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     const ChunkSplit* splits = reinterpret_cast<const ChunkSplit*>(a.ws + a.splits_off);
     const int lane = threadIdx.x & 31;
     const int64_t warps = int64_t(gridDim.x) * 8, first = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t rows = int64_t(head->num_splits) * (2 * kChunkRows);
+    // Grouped: a request's row tile may have few rows (16 of 128 for a single token and 16 heads), and the rows
+    // that it cannot have are not visited
+    const int per_split = GROUPS ? head->split_rows : 2 * kChunkRows;
+    const int64_t rows = int64_t(head->num_splits) * per_split;
     const int parts = rows * 4 <= warps ? 4 : 1;
     for (int64_t w = first; w < rows * parts; w += warps) {
         const int64_t r = parts == 4 ? w >> 2 : w;
-        const ChunkSplit sp = splits[r / (2 * kChunkRows)];
-        const int row = int(r % (2 * kChunkRows));
+        int split, row;
+        if (GROUPS) {                             // (splits times rows: the workspace has a slot of 262 KB for each split)
+            split = int(uint32_t(r) / uint32_t(per_split));
+            row = int(r) - split * per_split;
+            if (!a.tile.flat) {                   // the row's token and head, to its place in the pair's rows
+                const int token = a.tile.by_heads(row), second = token >= a.tile.tokens;
+                row += second * (kChunkRows - a.tile.tokens * a.tile.heads);
+            }
+        } else {
+            split = int(r / (2 * kChunkRows));
+            row = int(r % (2 * kChunkRows));
+        }
+        const ChunkSplit sp = splits[split];
         const ChunkRow at = chunk_row(a.tile, a.Hs, sp.row0, sp.ntok, sp.pair_group, row / kChunkRows, row % kChunkRows);
         if (!at.live) continue;
         int pre_pieces = 0;

@@ -20,13 +20,15 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "chunk.h"
 #include "common.cuh"
 
 namespace splash {
 
 constexpr int kPlanThreads = 512;         // threads of the block
-constexpr int kEvenTiles = 2;             // row tiles of an even cut per thread
+constexpr int kEvenTiles = 2;             // row tiles of an even cut per thread, at most
 constexpr int kCuts = 4;                  // piece lengths tried: an even share of 1..4 rounds of the pairs
 // Costs in key tiles (1.15 us each): what an item costs beside its tiles (first loads, epilogue), what a
 // partial costs to write and merge, and the merge's own latency.
@@ -158,13 +160,15 @@ __device__ __forceinline__ float tiles_about(const ChunkArgs& a, const Span& s) 
 constexpr uint32_t kBadLength = 1, kBadOrder = 2;
 constexpr uint32_t kFarApart = 4;         // a request's row tiles sweep more than L2 holds
 struct Totals {
-    int u, most;
+    int u, most, rows;
     float f;
     uint32_t flags;
 };
+template <bool GROUPS>
 __device__ __forceinline__ void warp_totals(Totals& x) {
     x.u = __reduce_add_sync(0xffffffffu, x.u);
     x.most = __reduce_max_sync(0xffffffffu, x.most);
+    if (GROUPS) x.rows = __reduce_max_sync(0xffffffffu, x.rows);
     x.flags = __reduce_or_sync(0xffffffffu, x.flags);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x.f += __shfl_xor_sync(0xffffffffu, x.f, o);
@@ -248,6 +252,7 @@ struct PlanScratch {
     int cuts[32][2 * kCuts];
     struct {
         int U, longest, best_len, dealt;   // row tiles; key tiles of the longest; the plan
+        int split_rows;                    // grouped: rows of a request's row tile, at most
         int len[kCuts];                    // piece lengths to try
         float C, best;
         bool bad, bad_order, is_even, cuts;
@@ -282,7 +287,7 @@ __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh)
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, active = warps_of(a.groups);
     if (warp < active) {
-        Totals gain = {};
+        float gain = 0.f;
         for (int g = threadIdx.x; g < a.groups; g += kPlanThreads) {
             const int r0 = gs.cu[g], r1 = gs.cu[g + 1], given = a.prefix_lens[g];
             const int p = min(max(given, 0), a.max_ctx);
@@ -291,16 +296,17 @@ __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh)
             const int c0 = min(max(a.cu_q[r0], 0), a.total_q), n = min(max(a.cu_q[max(r0, r1)], c0), a.total_q) - c0;
             const float x = gain_of_sharing(a, r1 - r0, n, p);
             gs.prefix[g] = x > 0.f ? p : ~p;
-            gain.f += fmaxf(x, 0.f);
+            gain += fmaxf(x, 0.f);
         }
-        warp_totals(gain);
-        if (lane == 0) sh.totals[warp].f = gain.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) gain += __shfl_xor_sync(0xffffffffu, gain, o);
+        if (lane == 0) sh.totals[warp].f = gain;
     }
     __syncthreads();
     if (warp < active) {
-        float gain = 0.f;
-        for (int w = 0; w < active; ++w) gain += sh.totals[w].f;
-        if (gain <= kMergeCost * float(a.pairs))
+        float all = 0.f;
+        for (int w = 0; w < active; ++w) all += sh.totals[w].f;
+        if (all <= kMergeCost * float(a.pairs))
             for (int g = threadIdx.x; g < a.groups; g += kPlanThreads)
                 if (gs.prefix[g] >= 0) gs.prefix[g] = ~gs.prefix[g];
     }
@@ -358,32 +364,41 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                                                        : (MODE == kChunkGroups ? int64_t(s.ctx) - s.lo : int64_t(s.ctx));
             if (s.u > 1 && swept * (kDqk * 2) > kSharedBytes) sum.flags |= kFarApart;
             if (s.u > 0) sum.most = max(sum.most, s.m);
+            if (MODE == kChunkGroups && s.group != kPrefix) sum.rows = max(sum.rows, min(s.n, a.tile.per) * a.tile.heads);
         }
-        warp_totals(sum);
+        warp_totals<MODE == kChunkGroups>(sum);
         if (lane == 0) sh.totals[warp] = sum;
     }
     __syncthreads();
     if (warp == 0) {
         Totals sum = lane < active ? sh.totals[lane] : Totals{};
-        warp_totals(sum);
+        warp_totals<MODE == kChunkGroups>(sum);
         const int U = sum.u, longest = sum.most;
         const float C = sum.f, G = float(a.pairs);
-        const float ideal = (C + kItemCost * float(U)) / G;
-        const float best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
-        const bool may_cut = a.cap_slots > 0 && U > 0 && best > 1.02f * ideal + kMergeCost;
-        // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
-        const float even = ideal + kItemCost + 2.f * G * kSlotCost + kMergeCost;
+        float best = 0.f;
+        bool may_cut = true, is_even = false;
         // (cuts make at most pairs - 1 more items, two partials each, and no more than there are tiles;
         // positions times pairs stay below 2^31)
         const int64_t tiles_most = int64_t(U) * longest;
         const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
                           (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
                           tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
-        const bool is_even = may_cut && room && U <= kEvenTiles * NT && a.pairs <= 256 && !(sum.flags & kFarApart) && even < best;
+        const bool even_fits = room && U <= kEvenTiles * NT && a.pairs <= 256 && !(sum.flags & kFarApart);
+        if (MODE == kChunkGroups && even_fits && U > 0) {
+            is_even = true;                        // (the results of most row tiles are merged anyhow)
+        } else {
+            const float ideal = (C + kItemCost * float(U)) / G;
+            best = U > 0 ? fmaxf(float(longest) + kItemCost, ceilf(float(U) / G) * (C / float(U) + kItemCost)) : 0.f;
+            may_cut = a.cap_slots > 0 && U > 0 && best > 1.02f * ideal + kMergeCost;
+            // an even cut: a run of every pair is (C + item costs) / G, and up to pairs - 1 cuts make two partials each
+            const float even = ideal + kItemCost + 2.f * G * kSlotCost + kMergeCost;
+            is_even = may_cut && even_fits && even < best;
+        }
         if (lane < kCuts) sh.choice.len[lane] = max(1, int(ceilf(C / (G * float(lane + 1)))));
         if (lane == 0) {
             sh.choice.U = U;
             sh.choice.longest = longest;
+            sh.choice.split_rows = min(sum.rows, 2 * kChunkRows);
             sh.choice.best_len = INT_MAX;
             sh.choice.dealt = U;                   // the items of a dealt plan
             sh.choice.C = C;
@@ -458,10 +473,11 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     const int t0 = MODE == kChunkWindow ? 0 : a.tok_lo / kChunkKeys;
     int num_splits = 0;
     int2 range;
-    if (is_even) {
-        // kEvenTiles consecutive row tiles per thread; from[] holds the requests' first row tiles
-        ChunkItem it[kEvenTiles] = {};
-        int tiles[kEvenTiles] = {}, group[kEvenTiles], base = 0;
+    // An even cut with E consecutive row tiles per thread; from[] holds the requests' first row tiles.
+    auto cut_even = [&](auto row_tiles_a_thread) {
+        constexpr int E = decltype(row_tiles_a_thread)::value;
+        ChunkItem it[E] = {};
+        int tiles[E] = {}, group[E], base = 0;
         for (int r0 = 0; r0 < B; r0 += NT) {
             const Span s = r0 + tid >= B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid, sh.groups));
             int v[1] = {s.u}, tot[1];
@@ -471,8 +487,8 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             if (MODE == kChunkGroups && r0 + tid < a.groups) sh.groups.split0[r0 + tid] = base + v[0];   // (each is split)
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < kEvenTiles; ++e) {
-                const int x = tid * kEvenTiles + e;
+            for (int e = 0; e < E; ++e) {
+                const int x = tid * E + e;
                 if (x >= base && x < base + tot[0]) {
                     const int k = last_at_most(sh.from, min(NT, B - r0), x);
                     it[e] = row_tile<MODE>(a, sh.spans[k], x - sh.from[k], &tiles[e]);
@@ -485,18 +501,18 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         // positions along the sequence in tiles, an item's own cost included: pair j's run is
         // [j T / P, (j + 1) T / P), and a row tile's tiles lie at [A + own, A + own + tiles)
         const int own = int(kItemCost);
-        const int holders = warps_of((U + kEvenTiles - 1) / kEvenTiles);
+        const int holders = warps_of((U + E - 1) / E);
         int v[1] = {0}, W[1];
 #pragma unroll
-        for (int e = 0; e < kEvenTiles; ++e) v[0] += tid * kEvenTiles + e < U ? tiles[e] + own : 0;
+        for (int e = 0; e < E; ++e) v[0] += tid * E + e < U ? tiles[e] + own : 0;
         block_scan<1>(v, W, sh.scan1, holders);
         // Runs are own + kLeastPiece long at least, so that only one boundary can fall on a row tile's own
         // cost and first tiles, and one on its last: only its first and last piece can come out too
         // short, and then go to their neighbours.
         const uint32_t T = uint32_t(W[0]);
         const uint32_t P = max(1u, min(uint32_t(a.pairs), T / uint32_t(own + kLeastPiece)));
-        int np[kEvenTiles] = {}, j0[kEvenTiles] = {}, j1[kEvenTiles] = {}, A[kEvenTiles] = {};
-        bool no_first[kEvenTiles] = {};
+        int np[E] = {}, j0[E] = {}, j1[E] = {}, A[E] = {};
+        bool no_first[E] = {};
         auto cut = [&](int e, int j) -> int {     // first tile of pair j's piece
             if (j <= j0[e]) return 0;
             if (j > j1[e]) return tiles[e];
@@ -505,12 +521,12 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         };
         // items, partials and split row tiles
         int sums[3] = {}, totals[3];
-        bool split_up[kEvenTiles] = {};
+        bool split_up[E] = {};
         int at = v[0];
 #pragma unroll
-        for (int e = 0; e < kEvenTiles; ++e) {
+        for (int e = 0; e < E; ++e) {
             A[e] = at;
-            if (tid * kEvenTiles + e >= U) continue;
+            if (tid * E + e >= U) continue;
             j0[e] = int((uint32_t(at + 1) * P - 1) / T);
             j1[e] = int((uint32_t(at + own + tiles[e]) * P - 1) / T);
             np[e] = j1[e] - j0[e] + 1;
@@ -545,7 +561,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         // the items are in the order of their pairs, so a pair's are a range
         int item = sums[0], slot = sums[1], split = sums[2];
 #pragma unroll
-        for (int e = 0; e < kEvenTiles; ++e) {
+        for (int e = 0; e < E; ++e) {
             if (np[e] > 0 && pair >= j0[e] && pair <= j1[e]) {
                 const int lo = cut(e, pair), hi = cut(e, pair + 1);
                 const bool empty = tiles[e] == 0;
@@ -571,6 +587,12 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         __syncthreads();
         range = make_int2(sh.first < sh.last ? sh.first : 0, sh.first < sh.last ? sh.last : 0);
         num_splits = totals[2];
+    };
+    if (is_even) {
+        // (a row tile a thread is shorter where that is enough, but the other forms seldom come here, and a second
+        // copy of the code costs them 1 us)
+        if (MODE == kChunkGroups && U <= NT) cut_even(std::integral_constant<int, MODE == kChunkGroups ? 1 : kEvenTiles>{});
+        else cut_even(std::integral_constant<int, kEvenTiles>{});
     } else {
         // item i is the (i / pairs)-th of pair i mod pairs, whose items lie next to each other
         const int per_pair = a.by_pairs(dealt + a.pairs - 1);
@@ -641,6 +663,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         head->magic = kChunkMagic;
         head->num_splits = num_splits;
         head->words = 2 * a.pairs;
+        if (MODE == kChunkGroups) head->split_rows = sh.choice.split_rows;
     }
     return range;
 }

@@ -274,49 +274,83 @@ SPLASH_API int splash_kv_migrate(const void* src_pool, void* dst_pool, size_t pa
  * ------------------------------------------------------------------------- */
 
 /*
- * The arrays of a ragged batch from its request lengths, with pages from a free list: what a step begins
- * with, built on the device, so that lengths and tables need not come back to the host.
- *   desc         num_reqs, page_size, num_pages and max_pages_per_req; d_qk = 576, d_v = 512 and a positive
- *                num_heads, all three otherwise unused, as is scale
+ * A ragged batch whose arrays the device builds (host struct, read during the call only).
+ *   num_reqs, page_size, num_pages, max_pages_per_req   as in splash_attn_desc
+ *   total_q      rows that positions and slots have, 2^30 at most;  reserved is 0
  *   past_lens    int32 [B]: tokens of request r in the cache;  new_lens int32 [B]: its new tokens (0 or more)
+ *   free_pages   int32 [num_pages], a stack: entries [0, *free_count) are free pages' ids, the last one on top
+ *   free_count   int32 [1]; a value outside [0, num_pages] is clamped into it
  *   block_table  int32 [B][max_pages_per_req]: entries for the past tokens' pages are there already; those
  *                that the new tokens add are written, the others left as they are
- *   free_pages   int32 [num_pages], a stack: entries [0, *free_count) are free pages' ids, the last one on top.
- *                It is read, not written (see left)
- *   free_count   int32 [1]; a value outside [0, num_pages] is clamped into it
- *   total_q      rows that positions and slots have, 2^30 at most
  *   cu_q, ctx_lens   int32 [B + 1] and [B]: as above; ctx_lens[r] = past_lens[r] + new_lens[r]
  *   positions, slots int32 [total_q]: a new token's position, and its row of the pool: page id * P + position % P
  *                (-1 where the page id is outside [0, num_pages)).  Rows past cu_q[B] are left as they are
  *   left         int32 [2]: free pages left, the next *free_count; requests served
- * Pages are taken from the top of the stack in the order of the requests and of their pages.  The batch is
- * served up to the first request that cannot be: one for which rows or free pages do not
- * suffice, or whose lengths are negative or add up to more than max_pages_per_req * P.  That request and the ones
- * after it get neither rows (cu_q[r + 1] = cu_q[r]) nor pages, and ctx_lens[r] = past_lens[r].
- * ctx_lens may be past_lens, and left may begin at free_count; otherwise no two arrays may overlap.
  */
-SPLASH_API int splash_batch_tables(const splash_attn_desc* desc, const int32_t* past_lens, const int32_t* new_lens,
-                                   int32_t* block_table, const int32_t* free_pages, const int32_t* free_count,
-                                   int total_q, int32_t* cu_q, int32_t* ctx_lens, int32_t* positions,
-                                   int32_t* slots, int32_t* left, splash_stream_t stream);
+typedef struct {
+    int32_t num_reqs;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages_per_req;
+    int32_t total_q;
+    int32_t reserved;
+    const int32_t* past_lens;
+    const int32_t* new_lens;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* block_table;
+    int32_t* cu_q;
+    int32_t* ctx_lens;
+    int32_t* positions;
+    int32_t* slots;
+    int32_t* left;
+} splash_batch;
 
 /*
- * Gives pages back to the free list: those of tokens that are dropped (a request that ends, drafted tokens that
- * are rejected), and those that a sliding window has left behind.
- *   desc, block_table, free_pages, free_count: as above; free_pages and *free_count are updated
+ * The arrays of a ragged batch from its request lengths, with pages from a free list: what a step begins
+ * with, built on the device, so that lengths and tables need not come back to the host.
+ * Pages are taken from the top of the stack in the order of the requests and of their pages; the stack is read,
+ * not written (left holds its new height).  The batch is served up to the first request that cannot be:
+ * one for which rows or free pages do not suffice, or whose lengths are negative or add up to more than
+ * max_pages_per_req * P.  That request and the ones after it get neither rows (cu_q[r + 1] = cu_q[r]) nor pages, and
+ * ctx_lens[r] = past_lens[r].
+ * ctx_lens may be past_lens, and left may begin at free_count; otherwise no two arrays may overlap.
+ */
+SPLASH_API int splash_batch_tables(const splash_batch* batch, splash_stream_t stream);
+
+/*
+ * Tokens to drop from a batch (host struct, read during the call only).
+ *   num_reqs, page_size, num_pages, max_pages_per_req, block_table, free_pages, free_count: as in splash_batch;
+ *                the three arrays are updated
  *   ctx_lens     int32 [B], in and out: request r keeps its first keep_lens[r] tokens (all, if it has fewer or
  *                keep_lens is NULL; a negative value keeps none), and ctx_lens[r] becomes their number k
  *   window, sinks  window > 0: also the pages all of whose tokens lie in [sinks, k + 1 - window), which no later
  *                token sees (see splash_chunk_attn_ex).  0: none; sinks is then unused
+ */
+typedef struct {
+    int32_t num_reqs;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages_per_req;
+    int32_t window;
+    int32_t sinks;
+    int32_t* ctx_lens;
+    const int32_t* keep_lens;
+    int32_t* block_table;
+    int32_t* free_pages;
+    int32_t* free_count;
+} splash_batch_drop;
+
+/*
+ * Gives pages back to the free list: those of tokens that are dropped (a request that ends, drafted tokens that
+ * are rejected), and those that a sliding window has left behind.
  * Pages [ceil(k / P), ceil(ctx / P)) and the window's go on the stack, and their entries become -1.  An entry
  * outside [0, num_pages) has no page: it is passed over.  The pages go on so that the first request's first one lies
  * on top: after splash_batch_tables, dropping the same new tokens puts the stack back as it was.
  * A page that several requests share must be kept by all of them but one, or it is on the list more than
  * once.  Pages that do not fit on the stack are lost.  No two arrays may overlap (keep_lens may be ctx_lens).
  */
-SPLASH_API int splash_batch_release(const splash_attn_desc* desc, int32_t* ctx_lens, const int32_t* keep_lens,
-                                    int32_t* block_table, int32_t* free_pages, int32_t* free_count, int window,
-                                    int sinks, splash_stream_t stream);
+SPLASH_API int splash_batch_release(const splash_batch_drop* drop, splash_stream_t stream);
 
 /* Element types of splash_rope and of splash_chunk_attn's output. */
 enum { SPLASH_BF16 = 0, SPLASH_F16 = 1, SPLASH_F32 = 2 };

@@ -538,68 +538,75 @@ int page_log(int P) { return P == 16 ? 4 : (P == 32 ? 5 : (P == 64 ? 6 : 7)); }
 
 }  // namespace
 
-int splash_batch_tables(const splash_attn_desc* desc, const int32_t* past_lens, const int32_t* new_lens,
-                        int32_t* block_table, const int32_t* free_pages, const int32_t* free_count, int total_q,
-                        int32_t* cu_q, int32_t* ctx_lens, int32_t* positions, int32_t* slots, int32_t* left,
-                        splash_stream_t stream) {
-    const int st = validate_desc(desc);
+namespace {
+
+int batch_shape_error(int reqs, int page_size, int num_pages, int max_pages) {
+    const splash_attn_desc d = {reqs, 1, kDqk, kDv, page_size, num_pages, max_pages, 1.f};
+    return validate_desc(&d);
+}
+
+}  // namespace
+
+int splash_batch_tables(const splash_batch* b, splash_stream_t stream) {
+    if (!b) return SPLASH_ERR_INVALID_ARG;
+    const int st = batch_shape_error(b->num_reqs, b->page_size, b->num_pages, b->max_pages_per_req);
     if (st != SPLASH_OK) return st;
-    if (total_q < 0) return SPLASH_ERR_INVALID_ARG;
-    if (total_q > 1 << 30) return SPLASH_ERR_UNSUPPORTED;
-    if (!cu_q || !left || !free_count) return SPLASH_ERR_INVALID_ARG;
-    if (desc->num_reqs > 0 && (!past_lens || !new_lens || !ctx_lens)) return SPLASH_ERR_INVALID_ARG;
-    if (desc->num_reqs > 0 && desc->max_pages_per_req > 0 && !block_table) return SPLASH_ERR_INVALID_ARG;
-    if ((desc->num_pages > 0 && !free_pages) || (total_q > 0 && (!positions || !slots))) return SPLASH_ERR_INVALID_ARG;
-    for (const void* p : {static_cast<const void*>(past_lens), static_cast<const void*>(new_lens),
-                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
-                          static_cast<const void*>(free_count), static_cast<const void*>(cu_q),
-                          static_cast<const void*>(ctx_lens), static_cast<const void*>(positions),
-                          static_cast<const void*>(slots), static_cast<const void*>(left)})
+    if (b->total_q < 0 || b->reserved != 0) return SPLASH_ERR_INVALID_ARG;
+    if (b->total_q > 1 << 30) return SPLASH_ERR_UNSUPPORTED;
+    if (!b->cu_q || !b->left || !b->free_count) return SPLASH_ERR_INVALID_ARG;
+    if (b->num_reqs > 0 && (!b->past_lens || !b->new_lens || !b->ctx_lens)) return SPLASH_ERR_INVALID_ARG;
+    if (b->num_reqs > 0 && b->max_pages_per_req > 0 && !b->block_table) return SPLASH_ERR_INVALID_ARG;
+    if ((b->num_pages > 0 && !b->free_pages) || (b->total_q > 0 && (!b->positions || !b->slots)))
+        return SPLASH_ERR_INVALID_ARG;
+    for (const int32_t* p : {b->past_lens, b->new_lens, b->free_pages, b->free_count,
+                             static_cast<const int32_t*>(b->block_table), static_cast<const int32_t*>(b->cu_q),
+                             static_cast<const int32_t*>(b->ctx_lens), static_cast<const int32_t*>(b->positions),
+                             static_cast<const int32_t*>(b->slots), static_cast<const int32_t*>(b->left)})
         if (!aligned(p, 4)) return SPLASH_ERR_INVALID_ARG;
     BatchTablesArgs a = {};
-    a.past = past_lens;
-    a.fresh = new_lens;
-    a.table = block_table;
-    a.free_pages = free_pages;
-    a.free_count = free_count;
-    a.cu = cu_q;
-    a.ctx = ctx_lens;
-    a.positions = positions;
-    a.slots = slots;
-    a.left = left;
-    a.B = desc->num_reqs;
-    a.total_q = total_q;
-    a.P_log = page_log(desc->page_size);
-    a.num_pages = desc->num_pages;
-    a.max_pages = desc->max_pages_per_req;
-    a.wide = aligned(positions, 16) && aligned(slots, 16);
+    a.past = b->past_lens;
+    a.fresh = b->new_lens;
+    a.table = b->block_table;
+    a.free_pages = b->free_pages;
+    a.free_count = b->free_count;
+    a.cu = b->cu_q;
+    a.ctx = b->ctx_lens;
+    a.positions = b->positions;
+    a.slots = b->slots;
+    a.left = b->left;
+    a.B = b->num_reqs;
+    a.total_q = b->total_q;
+    a.P_log = page_log(b->page_size);
+    a.num_pages = b->num_pages;
+    a.max_pages = b->max_pages_per_req;
+    a.wide = aligned(b->positions, 16) && aligned(b->slots, 16);
     if (launch_batch_tables(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPLASH_ERR_CUDA;
     return SPLASH_OK;
 }
 
-int splash_batch_release(const splash_attn_desc* desc, int32_t* ctx_lens, const int32_t* keep_lens,
-                         int32_t* block_table, int32_t* free_pages, int32_t* free_count, int window, int sinks,
-                         splash_stream_t stream) {
-    const int st = validate_desc(desc);
+int splash_batch_release(const splash_batch_drop* d, splash_stream_t stream) {
+    if (!d) return SPLASH_ERR_INVALID_ARG;
+    const int st = batch_shape_error(d->num_reqs, d->page_size, d->num_pages, d->max_pages_per_req);
     if (st != SPLASH_OK) return st;
-    if (window < 0 || sinks < 0) return SPLASH_ERR_INVALID_ARG;
-    if (desc->num_reqs == 0 || desc->max_pages_per_req == 0) return SPLASH_OK;
-    if (!ctx_lens || !block_table || !free_count || (desc->num_pages > 0 && !free_pages)) return SPLASH_ERR_INVALID_ARG;
-    if (!aligned(ctx_lens, 4) || !aligned(keep_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
-        !aligned(free_count, 4))
+    if (d->window < 0 || d->sinks < 0) return SPLASH_ERR_INVALID_ARG;
+    if (d->num_reqs == 0 || d->max_pages_per_req == 0) return SPLASH_OK;
+    if (!d->ctx_lens || !d->block_table || !d->free_count || (d->num_pages > 0 && !d->free_pages))
+        return SPLASH_ERR_INVALID_ARG;
+    if (!aligned(d->ctx_lens, 4) || !aligned(d->keep_lens, 4) || !aligned(d->block_table, 4) ||
+        !aligned(d->free_pages, 4) || !aligned(d->free_count, 4))
         return SPLASH_ERR_INVALID_ARG;
     BatchReleaseArgs a = {};
-    a.ctx = ctx_lens;
-    a.keep = keep_lens;
-    a.table = block_table;
-    a.free_pages = free_pages;
-    a.free_count = free_count;
-    a.B = desc->num_reqs;
-    a.P_log = page_log(desc->page_size);
-    a.num_pages = desc->num_pages;
-    a.max_pages = desc->max_pages_per_req;
-    a.window = window;
-    a.sinks = sinks;
+    a.ctx = d->ctx_lens;
+    a.keep = d->keep_lens;
+    a.table = d->block_table;
+    a.free_pages = d->free_pages;
+    a.free_count = d->free_count;
+    a.B = d->num_reqs;
+    a.P_log = page_log(d->page_size);
+    a.num_pages = d->num_pages;
+    a.max_pages = d->max_pages_per_req;
+    a.window = d->window;
+    a.sinks = d->sinks;
     if (launch_batch_release(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPLASH_ERR_CUDA;
     return SPLASH_OK;
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -73,10 +74,10 @@ class SplashNormDesc(ctypes.Structure):
                 ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
 
 
-class SplashNormRows(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
-                ("y", ctypes.c_void_p), ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
-                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+# Structs that hold a call's pointers, packed (a ctypes structure takes five times as long to fill).
+_BATCH = struct.Struct("@6i10P")          # splash_batch
+_BATCH_DROP = struct.Struct("@6i5P")      # splash_batch_drop
+_NORM_ROWS = struct.Struct("@PqqPqqPii")  # splash_norm_rows
 
 
 class SplashChunkExt(ctypes.Structure):
@@ -118,8 +119,7 @@ def load_library(path: str | None = None):
         rp = ctypes.POINTER(SplashRopeDesc)
         lib.splash_rope.argtypes = [rp, i32, vp, i64, i64, vp, i64, i64, vp, i32, i32, vp]
         lib.splash_rope.restype = i32
-        np = ctypes.POINTER(SplashNormRows)
-        lib.splash_norm_rope.argtypes = [ctypes.POINTER(SplashNormDesc), rp, i32, np, np, vp, i32, vp]
+        lib.splash_norm_rope.argtypes = [ctypes.POINTER(SplashNormDesc), rp, i32, vp, vp, vp, i32, vp]
         lib.splash_norm_rope.restype = i32
         lib.splash_kv_append.argtypes = [dp, rp, i32, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp]
         lib.splash_kv_append.restype = i32
@@ -135,9 +135,9 @@ def load_library(path: str | None = None):
         lib.splash_chunk_workspace_size_ex.restype = sz
         lib.splash_chunk_attn_ex.argtypes = [dp, ep, vp, vp, vp, i32, vp, vp, i32, i32, i64, i64, i32, vp, vp, vp, sz, vp]
         lib.splash_chunk_attn_ex.restype = i32
-        lib.splash_batch_tables.argtypes = [dp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+        lib.splash_batch_tables.argtypes = [vp, vp]
         lib.splash_batch_tables.restype = i32
-        lib.splash_batch_release.argtypes = [dp, vp, vp, vp, vp, vp, i32, i32, vp]
+        lib.splash_batch_release.argtypes = [vp, vp]
         lib.splash_batch_release.restype = i32
         lib.splash_workspace_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         lib.splash_workspace_status.restype = i32
@@ -377,11 +377,14 @@ def _shape_desc(B: int, H: int, P: int, num_pages: int, max_pages: int, scale: f
     return SplashAttnDesc(B, H, 576, 512, P, num_pages, max_pages, scale)
 
 
-def _int32_arrays(where: str, **arrays) -> None:
-    """Contiguous int32 tensors, each of the shape given beside it."""
-    for name, (t, shape) in arrays.items():
-        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous int32 {list(shape)}")
+def _int32_arrays(where: str, dev: int, arrays) -> None:
+    """Each (name, tensor, entries): contiguous int32 of so many entries on device `dev`."""
+    i32 = torch.int32
+    for name, t, n in arrays:
+        if t.dtype is not i32 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous int32 of {n} entries")
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: tensors must live on one CUDA device")
 
 
 def splash_batch_tables(past_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, page_size: int,
@@ -393,19 +396,19 @@ def splash_batch_tables(past_lens: torch.Tensor, new_lens: torch.Tensor, block_t
     [B + 1], ctx_lens [B], positions and slots [N rows] and left [2] = (free pages left, requests served).
     ctx_lens may be past_lens, and free_count left[:1]; see splash.h for batches that do not fit."""
     where = "splash_batch_tables"
-    dev = _device_of(where, past_lens, new_lens, block_table, free_pages, free_count, cu_q, ctx_lens, positions, slots,
-                     left)
-    shape = block_table.shape
-    if len(shape) != 2 or free_pages.dim() != 1 or positions.dim() != 1:
-        raise ValueError(f"{where}: block_table [B][max_pages], free_pages [num_pages] and positions [N]")
-    B, N = shape[0], positions.shape[0]
-    _int32_arrays(where, past_lens=(past_lens, (B,)), new_lens=(new_lens, (B,)), block_table=(block_table, shape),
-                  free_pages=(free_pages, free_pages.shape), free_count=(free_count, (1,)), cu_q=(cu_q, (B + 1,)),
-                  ctx_lens=(ctx_lens, (B,)), positions=(positions, (N,)), slots=(slots, (N,)), left=(left, (2,)))
-    _call(dev, stream, where, (_lib or load_library()).splash_batch_tables,
-          _shape_desc(B, 1, int(page_size), free_pages.shape[0], shape[1], 1.0), past_lens.data_ptr(), new_lens.data_ptr(),
-          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), N, cu_q.data_ptr(), ctx_lens.data_ptr(),
-          positions.data_ptr(), slots.data_ptr(), left.data_ptr())
+    dev = _device_of(where, block_table)
+    if block_table.dim() != 2:
+        raise ValueError(f"{where}: block_table must be [B][max_pages]")
+    B, pages = block_table.shape
+    N, F = positions.numel(), free_pages.numel()
+    _int32_arrays(where, dev, (
+        ("past_lens", past_lens, B), ("new_lens", new_lens, B), ("block_table", block_table, B * pages),
+        ("free_pages", free_pages, F), ("free_count", free_count, 1), ("cu_q", cu_q, B + 1), ("ctx_lens", ctx_lens, B),
+        ("positions", positions, N), ("slots", slots, N), ("left", left, 2)))
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_tables, _BATCH.pack(
+        B, page_size, F, pages, N, 0, past_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+        free_count.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), ctx_lens.data_ptr(), positions.data_ptr(),
+        slots.data_ptr(), left.data_ptr()))
 
 
 def splash_batch_release(ctx_lens: torch.Tensor, keep_lens: torch.Tensor | None, block_table: torch.Tensor,
@@ -416,17 +419,18 @@ def splash_batch_release(ctx_lens: torch.Tensor, keep_lens: torch.Tensor | None,
     of splash_batch_tables, whose first entry is the count), their entries of block_table become -1, and ctx_lens [B]
     the tokens that are left."""
     where = "splash_batch_release"
-    dev = _device_of(where, ctx_lens, block_table, free_pages, free_count, *(() if keep_lens is None else (keep_lens,)))
-    shape = block_table.shape
-    if len(shape) != 2 or free_pages.dim() != 1 or free_count.dim() != 1 or free_count.shape[0] not in (1, 2):
-        raise ValueError(f"{where}: block_table [B][max_pages], free_pages [num_pages] and free_count [1]")
-    B = shape[0]
-    _int32_arrays(where, ctx_lens=(ctx_lens, (B,)), block_table=(block_table, shape), free_pages=(free_pages, free_pages.shape),
-                  free_count=(free_count, free_count.shape), keep_lens=(ctx_lens if keep_lens is None else keep_lens, (B,)))
-    _call(dev, stream, where, (_lib or load_library()).splash_batch_release,
-          _shape_desc(B, 1, int(page_size), free_pages.shape[0], shape[1], 1.0), ctx_lens.data_ptr(),
-          None if keep_lens is None else keep_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
-          free_count.data_ptr(), int(window), int(sinks))
+    dev = _device_of(where, block_table)
+    count = free_count.numel()
+    if block_table.dim() != 2 or not 1 <= count <= 2:
+        raise ValueError(f"{where}: block_table must be [B][max_pages], free_count [1] (or left [2])")
+    B, pages = block_table.shape
+    F = free_pages.numel()
+    _int32_arrays(where, dev, (
+        ("ctx_lens", ctx_lens, B), ("keep_lens", ctx_lens if keep_lens is None else keep_lens, B),
+        ("block_table", block_table, B * pages), ("free_pages", free_pages, F), ("free_count", free_count, count)))
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_release, _BATCH_DROP.pack(
+        B, page_size, F, pages, window, sinks, ctx_lens.data_ptr(), 0 if keep_lens is None else keep_lens.data_ptr(),
+        block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr()))
 
 
 def make_rope_desc(dims: int, base: float = 10000.0, interleaved: bool = True, scaling: str = "none",
@@ -466,23 +470,25 @@ def _norm_desc(width: int, norm_dims: int, rope_lo: int, weight_dtype: int, eps:
     return SplashNormDesc(width, norm_dims, rope_lo, weight_dtype, eps, offset)
 
 
-def _norm_rows(where: str, x, weight, out, T: int, D: int, n: int, dtype, weight_dtype) -> SplashNormRows:
+def _norm_rows(where: str, dev: int, x, weight, out, T: int, D: int, n: int, dtype, weight_dtype) -> bytes:
     shape = x.shape
     if len(shape) != 3 or shape[0] != T or shape[2] != D or out.shape != shape:
         raise ValueError(f"{where}: rows and their results must be [T][heads][D], q's and k's with the same T and D")
-    if x.dtype != dtype or out.dtype != dtype:
+    if x.dtype is not dtype or out.dtype is not dtype:
         raise ValueError(f"{where}: rows and results must share one dtype")
+    if x.get_device() != dev or out.get_device() != dev or (weight is not None and weight.get_device() != dev):
+        raise ValueError(f"{where}: tensors must live on one CUDA device")
     xt, xh, x1 = x.stride()
     yt, yh, y1 = out.stride()
     H = shape[1]
     if (x1 != 1 or y1 != 1) and D > 1 and T and H:
         raise ValueError(f"{where}: rows must be dense")
-    w = None
+    w = 0
     if weight is not None:
-        if weight.dtype != weight_dtype or weight.shape != (n,) or not weight.is_contiguous():
+        if weight.dtype is not weight_dtype or weight.numel() != n or not weight.is_contiguous():
             raise ValueError(f"{where}: weights must be dense [norm_dims] of one floating dtype")
         w = weight.data_ptr()
-    return SplashNormRows(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, w, H, 0)
+    return _NORM_ROWS.pack(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, w, H, 0)
 
 
 def splash_norm_rope(q: torch.Tensor, q_weight: torch.Tensor | None, q_out: torch.Tensor, k: torch.Tensor | None,
@@ -494,27 +500,29 @@ def splash_norm_rope(q: torch.Tensor, q_weight: torch.Tensor | None, q_out: torc
     int32 [T] (rope None: no rotation).  All are views with dense rows and any token and head strides; an output
     may be its input."""
     where = "splash_norm_rope"
+    dev = _device_of(where, q)
     if (k is None) != (k_out is None):
         raise ValueError(f"{where}: k and k_out belong together")
-    weight = q_weight if q_weight is not None else k_weight
-    dev = _device_of(where, q, q_out, *(t for t in (q_weight, k, k_weight, k_out, positions) if t is not None))
-    if q.dim() != 3:
+    shape, dt = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError(f"{where}: q must be [T][heads][D]")
-    T, _, D = q.shape
+    T, _, D = shape
     n = D if norm_dims is None else int(norm_dims)
-    dtype = _DTYPES.get(q.dtype)
-    weight_dtype = SPLASH_F32 if weight is None else _DTYPES.get(weight.dtype)
+    weight = q_weight if q_weight is not None else k_weight
+    wt = torch.float32 if weight is None else weight.dtype
+    dtype, weight_dtype = _DTYPES.get(dt), _DTYPES.get(wt)
     if dtype is None or weight_dtype is None:
         raise ValueError(f"{where}: rows and weights must be bfloat16, float16 or float32")
-    if rope is not None and (positions is None or positions.dtype != torch.int32 or positions.shape != (T,)
-                             or not positions.is_contiguous()):
-        raise ValueError(f"{where}: positions must be contiguous int32 [T]")
-    wd = None if weight is None else weight.dtype
-    a = _norm_rows(where, q, q_weight, q_out, T, D, n, q.dtype, wd)
-    b = None if k is None else _norm_rows(where, k, k_weight, k_out, T, D, n, q.dtype, wd)
+    at = None
+    if rope is not None:
+        if (positions is None or positions.dtype is not torch.int32 or positions.shape != (T,)
+                or not positions.is_contiguous() or positions.get_device() != dev):
+            raise ValueError(f"{where}: positions must be contiguous int32 [T] on q's device")
+        at = positions.data_ptr()
+    a = _norm_rows(where, dev, q, q_weight, q_out, T, D, n, dt, wt)
+    b = None if k is None else _norm_rows(where, dev, k, k_weight, k_out, T, D, n, dt, wt)
     _call(dev, stream, where, (_lib or load_library()).splash_norm_rope,
-          _norm_desc(D, n, int(rope_lo), weight_dtype, float(eps), float(weight_offset)), rope, dtype, a, b,
-          None if positions is None else positions.data_ptr(), T)
+          _norm_desc(D, n, rope_lo, weight_dtype, eps, weight_offset), rope, dtype, a, b, at, T)
 
 
 def splash_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, cu_q: torch.Tensor,
@@ -607,6 +615,12 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
     _call(dev, stream, "splash_chunk_attn", (_lib or load_library()).splash_chunk_attn, *args)
 
 
+@functools.lru_cache(maxsize=256)
+def _window_ext(window: int, sinks: int) -> SplashChunkExt:
+    """A window without groups (read-only; the library reads it during the call)."""
+    return SplashChunkExt(window, sinks)
+
+
 def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
                          ctx_lens: torch.Tensor, head_lo: int, head_hi: int, tok_lo: int, tok_hi: int,
                          out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, scale: float, window: int = 0,
@@ -621,11 +635,10 @@ def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Ten
     if (cu_groups is None) != (prefix_lens is None):
         raise ValueError(f"{where}: cu_groups and prefix_lens belong together")
     if cu_groups is None:
-        ext = SplashChunkExt(int(window), int(sinks))
+        ext = _window_ext(int(window), int(sinks))
     else:
-        _device_of(where, q, cu_groups, prefix_lens)
         G = prefix_lens.numel()
-        _int32_arrays(where, cu_groups=(cu_groups, (G + 1,)), prefix_lens=(prefix_lens, (G,)))
+        _int32_arrays(where, dev, (("cu_groups", cu_groups, G + 1), ("prefix_lens", prefix_lens, G)))
         ext = SplashChunkExt(int(window), int(sinks), cu_groups.data_ptr(), prefix_lens.data_ptr(), G)
     _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn_ex, args[0], ext, *args[1:])
 

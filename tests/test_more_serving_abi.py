@@ -1,5 +1,10 @@
 """Host-side refusals of the batch tables, the norm with rope and the attention's windows and groups.  CPU only:
 no call here reaches a kernel."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
 import pytest
 import torch
 
@@ -25,45 +30,68 @@ def desc(**kw):
 
 # ------------------------------------------------------------------ batch tables
 
-def tables(lib, d, past=FAKE, new=FAKE, table=FAKE, pages=FAKE, count=FAKE, n=6, cu=FAKE, ctx=FAKE, pos=FAKE, slots=FAKE,
-           left=FAKE):
-    return lib.splash_batch_tables(d, past, new, table, pages, count, n, cu, ctx, pos, slots, left, None)
+def tables(lib, reqs=2, page=16, pages=11, most=7, n=6, reserved=0, past=FAKE, new=FAKE, free=FAKE, count=FAKE, table=FAKE,
+           cu=FAKE, ctx=FAKE, pos=FAKE, slots=FAKE, left=FAKE):
+    return lib.splash_batch_tables(S._BATCH.pack(reqs, page, pages, most, n, reserved, past, new, free, count, table, cu, ctx,
+                                                 pos, slots, left), None)
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(past=0), INVALID), (dict(new=0), INVALID), (dict(table=0), INVALID), (dict(pages=0), INVALID),
+    (dict(past=0), INVALID), (dict(new=0), INVALID), (dict(table=0), INVALID), (dict(free=0), INVALID),
     (dict(count=0), INVALID), (dict(cu=0), INVALID), (dict(ctx=0), INVALID), (dict(pos=0), INVALID),
     (dict(slots=0), INVALID), (dict(left=0), INVALID), (dict(n=-1), INVALID), (dict(n=(1 << 30) + 1), UNSUPPORTED),
-    (dict(past=FAKE + 2), INVALID), (dict(slots=FAKE + 1), INVALID), (dict(left=FAKE + 2), INVALID),
+    (dict(past=FAKE + 2), INVALID), (dict(slots=FAKE + 1), INVALID), (dict(left=FAKE + 2), INVALID), (dict(reserved=1), INVALID),
+    (dict(page=48), UNSUPPORTED), (dict(page=0), UNSUPPORTED), (dict(reqs=-1), INVALID), (dict(pages=1 << 28), UNSUPPORTED),
+    (dict(pages=-1), INVALID), (dict(most=-1), INVALID), (dict(most=1 << 27), UNSUPPORTED),
 ])
 def test_tables_rejects_bad_arguments(lib, kw, code):
-    assert tables(lib, desc(), **kw) == code
+    assert tables(lib, **kw) == code
+    assert lib.splash_batch_tables(None, None) == INVALID
 
 
-def test_tables_rejects_bad_shapes(lib):
-    assert tables(lib, None) == INVALID
-    for kw, code in ((dict(page_size=48), UNSUPPORTED), (dict(num_reqs=-1), INVALID), (dict(d_v=576), UNSUPPORTED),
-                     (dict(num_pages=1 << 28), UNSUPPORTED), (dict(max_pages_per_req=-1), INVALID)):
-        assert tables(lib, desc(**kw)) == code
-
-
-def release(lib, d, ctx=FAKE, keep=FAKE, table=FAKE, pages=FAKE, count=FAKE, window=0, sinks=0):
-    return lib.splash_batch_release(d, ctx, keep, table, pages, count, window, sinks, None)
+def release(lib, reqs=2, page=16, pages=11, most=7, window=0, sinks=0, ctx=FAKE, keep=FAKE, table=FAKE, free=FAKE, count=FAKE):
+    return lib.splash_batch_release(S._BATCH_DROP.pack(reqs, page, pages, most, window, sinks, ctx, keep, table, free, count), None)
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(ctx=0), INVALID), (dict(table=0), INVALID), (dict(pages=0), INVALID), (dict(count=0), INVALID),
+    (dict(ctx=0), INVALID), (dict(table=0), INVALID), (dict(free=0), INVALID), (dict(count=0), INVALID),
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(keep=FAKE + 2), INVALID), (dict(table=FAKE + 1), INVALID),
+    (dict(page=8), UNSUPPORTED), (dict(reqs=-1), INVALID),
 ])
 def test_release_rejects_bad_arguments(lib, kw, code):
-    assert release(lib, desc(), **kw) == code
+    assert release(lib, **kw) == code
+    assert lib.splash_batch_release(None, None) == INVALID
 
 
 def test_release_of_nothing_is_fine(lib):
-    assert release(lib, None) == INVALID
-    assert release(lib, desc(page_size=8)) == UNSUPPORTED
-    assert release(lib, desc(num_reqs=0), ctx=0, table=0) == S.SPLASH_OK
-    assert release(lib, desc(max_pages_per_req=0), ctx=0, table=0) == S.SPLASH_OK
+    assert release(lib, reqs=0, ctx=0, table=0) == S.SPLASH_OK
+    assert release(lib, most=0, ctx=0, table=0) == S.SPLASH_OK
+
+
+def test_packed_structs_are_laid_out_as_in_the_header():
+    """A C program states the sizes and offsets that the binding's packed structs rely on."""
+    src = r"""
+#include <stddef.h>
+#include <stdio.h>
+#include "splash.h"
+int main(void) {
+    printf("%zu %zu %zu %zu %zu ", sizeof(splash_batch), offsetof(splash_batch, past_lens), offsetof(splash_batch, block_table),
+           offsetof(splash_batch, cu_q), offsetof(splash_batch, left));
+    printf("%zu %zu %zu ", sizeof(splash_batch_drop), offsetof(splash_batch_drop, ctx_lens), offsetof(splash_batch_drop, free_count));
+    printf("%zu %zu %zu %zu ", sizeof(splash_norm_rows), offsetof(splash_norm_rows, y), offsetof(splash_norm_rows, weight),
+           offsetof(splash_norm_rows, heads));
+    printf("%zu %zu %zu\n", sizeof(splash_chunk_ext), offsetof(splash_chunk_ext, cu_groups), offsetof(splash_chunk_ext, num_groups));
+    return 0;
+}
+"""
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "sizes.c"), os.path.join(d, "sizes")
+        with open(c, "w") as f:
+            f.write(src)
+        subprocess.run(["gcc", "-I", B.INCLUDE, c, "-o", exe], check=True)
+        out = [int(v) for v in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert out == [S._BATCH.size, 24, 56, 64, 96, S._BATCH_DROP.size, 24, 56, S._NORM_ROWS.size, 24, 48, 56,
+                   ctypes.sizeof(S.SplashChunkExt), 8, 24]
 
 
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
@@ -74,11 +102,13 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
     with pytest.raises(ValueError, match="CUDA"):
         S.splash_batch_release(i, None, t, 16, i, i)
     with pytest.raises(ValueError, match="past_lens"):
-        S._int32_arrays("x", past_lens=(i.long(), (2,)))
+        S._int32_arrays("x", -1, (("past_lens", i.long(), 2),))
     with pytest.raises(ValueError, match="cu_q"):
-        S._int32_arrays("x", cu_q=(i, (3,)))
+        S._int32_arrays("x", -1, (("cu_q", i, 3),))
     with pytest.raises(ValueError, match="slots"):
-        S._int32_arrays("x", slots=(t[:, 0], (2,)))
+        S._int32_arrays("x", -1, (("slots", t[:, 0], 2),))
+    with pytest.raises(ValueError, match="device"):
+        S._int32_arrays("x", 0, (("slots", i, 2),))
 
 
 # ------------------------------------------------------------------ norm with rope
@@ -87,7 +117,7 @@ def rows(**kw):
     d = dict(x=FAKE, x_token_stride=1024, x_head_stride=128, y=FAKE << 8, y_token_stride=1024, y_head_stride=128,
              weight=FAKE, heads=4, reserved=0)
     d.update(kw)
-    return S.SplashNormRows(**d)
+    return S._NORM_ROWS.pack(*d.values())
 
 
 def norm(lib, n=None, r="rope", dtype=0, q="rows", k=None, pos=FAKE, T=3, **kw):

@@ -25,6 +25,10 @@ namespace {
 constexpr int kNormThreads = 128;    // a block's, at most
 constexpr int kNormPasses = 8;       // rows of a lane one after the other, at most
 constexpr int kNormUnits = 4;        // units of a lane, at most
+// Blocks an SM has room for: one more than the compiler's choice of registers leaves (a unit a lane: 52.5 to 50.6 us for
+// the large prompt; three: 24.1 to 21.7 for 2,000 tokens x 17 heads x 576 dims, with 24 bytes spilled; two more are slower).
+template <int K>
+constexpr int kNormBlocks = K == 1 ? 8 : (K == 3 ? 4 : 1);
 constexpr int kNormPairs = 1024;     // cos / sin a block holds, at most (one token has 128 at most)
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -89,7 +93,7 @@ __device__ __forceinline__ float range_scale(float ss, float eps) {
 
 // VE elements a vector, K units a lane.
 template <typename T, bool INTER, int VE, int K>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel(const __grid_constant__ NormArgs a) {
     // Weights and cos / sin in runs with gaps, so that lanes at different runs read different banks.
     constexpr int kWRun = VE >= 8 ? VE + 4 : VE;
     constexpr int RN = INTER && VE > 1 ? VE / 2 : VE;  // pairs whose cos / sin a lane reads together

@@ -107,7 +107,8 @@ struct ChunkHeader {
 // One pair's work: the rows of one token block and head group pair against key tiles
 // [t_lo, t_hi).  A tile is two blocks of 64 keys.  In the windowed form the first tokens' blocks and the window's
 // are counted as one sequence, with `base` between a block's number in it and its place in the context.
-// In the grouped form an item's keys begin at `base`, and a group's own item is one of all its requests' rows.
+// In the grouped form an item's keys begin at `base`, its tiles are counted from that key's block, and a group's own item is
+// one of all its requests' rows.
 constexpr int kItemAlone = 1;    // few row tiles share these keys: they are prefetched into L2
 constexpr int kItemPrefix = 2;   // every row sees every key up to ctx: a group's rows over its prefix
 struct alignas(16) ChunkItem {

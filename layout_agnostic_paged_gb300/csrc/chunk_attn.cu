@@ -119,7 +119,8 @@ __device__ __forceinline__ int tile_key(const ChunkArgs& a, const ChunkItem& it,
         const int b = 2 * t + half;
         return (b + (b < a.sink_blocks ? a.tok_lo / kChunkRows : it.base)) * kChunkRows;
     }
-    return t * kChunkKeys + half * kChunkRows;
+    const int from = MODE == kChunkGroups ? it.base & ~(kChunkRows - 1) : 0;
+    return from + t * kChunkKeys + half * kChunkRows;
 }
 
 // No row of the item sees keys before it.
@@ -291,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // next tile's into L2, each page's rows as one run (35 requests of 3-9 tokens and 16 heads
                 // over some 10,000 keys: 117 -> 106 us; further ahead is slower, and where pairs share
                 // the keys it costs 2%).
-                const int ahead = MODE == kChunkWindow ? tile_key<MODE>(a, it, t + 1, int(rank)) + lane * R : key + kChunkKeys;
+                const int ahead = MODE != kChunkPlain ? tile_key<MODE>(a, it, t + 1, int(rank)) + lane * R : key + kChunkKeys;
                 if ((it.flags & kItemAlone) && t + 1 < it.t_hi && lane < loads && !second && !left_behind<MODE>(a, start, ahead, R)) {
                     const int id = page_of(a, table, ahead, it.ctx);
                     if (id >= 0)
@@ -317,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int start = item_start<MODE>(a, it);
             for (int t = it.t_lo; t < it.t_hi && ok; ++t) {
                 int key = t * kChunkKeys + lane * R;            // lane k < 2 * loads: load k of the tile
-                if (MODE == kChunkWindow) key = lane < loads ? tile_key<MODE>(a, it, t, 0) + lane * R : tile_key<MODE>(a, it, t, 1) + (lane - loads) * R;
+                if (MODE != kChunkPlain) key = lane < loads ? tile_key<MODE>(a, it, t, 0) + lane * R : tile_key<MODE>(a, it, t, 1) + (lane - loads) * R;
                 int row = past;
                 if (lane < 2 * loads && !left_behind<MODE>(a, start, key, R)) {
                     const int id = page_of(a, table, key, it.ctx);
@@ -474,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int32_t* table = a.block_table + int64_t(it.r) * a.max_pages;
             float m = -INFINITY, l = 0.f;        // maximum and sum (this thread's keys) of c * x
             for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
-                const int key0 = MODE == kChunkWindow ? tile_key<MODE>(a, it, t, half) + part * 32 : t * kChunkKeys + share * 32;
+                const int key0 = MODE != kChunkPlain ? tile_key<MODE>(a, it, t, half) + part * 32 : t * kChunkKeys + share * 32;
                 uint32_t gone = 0;               // bit k: this thread's keys k R .. have no page
                 for (int k = 0; k * R < 32; ++k)
                     if (key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;

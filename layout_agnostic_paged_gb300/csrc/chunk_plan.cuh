@@ -84,6 +84,8 @@ __device__ __forceinline__ int key_tiles(const ChunkArgs& a, int lo, int first, 
         if (base) *base = w - a.sink_blocks;
         return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
     }
+    // (grouped: from the block in which the prefix ends, not from the tile)
+    if constexpr (MODE == kChunkGroups) return (e - lo / kChunkRows * kChunkRows + kChunkKeys - 1) / kChunkKeys;
     return (e + kChunkKeys - 1) / kChunkKeys - lo / kChunkKeys;
 }
 
@@ -470,7 +472,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     const int U = sh.choice.U, best_len = sh.choice.best_len, dealt = sh.choice.dealt;
     const bool is_even = sh.choice.is_even, bad_input = sh.choice.bad;
 
-    const int t0 = MODE == kChunkWindow ? 0 : a.tok_lo / kChunkKeys;
+    const int t0 = MODE == kChunkPlain ? a.tok_lo / kChunkKeys : 0;
     int num_splits = 0;
     int2 range;
     // An even cut with E consecutive row tiles per thread; from[] holds the requests' first row tiles.
@@ -568,9 +570,8 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 if (empty ? pair == j0[e] : hi > lo) {
                     const int k = empty ? 0 : pair - j0[e] - no_first[e];
                     ChunkItem o = it[e];
-                    const int from = MODE == kChunkGroups ? o.base / kChunkKeys : t0;
-                    o.t_lo = from + (empty ? 0 : lo);
-                    o.t_hi = from + (empty ? 0 : hi);
+                    o.t_lo = t0 + (empty ? 0 : lo);
+                    o.t_hi = t0 + (empty ? 0 : hi);
                     o.slot = split_up[e] ? slot + k : -1;
                     items[item + k] = o;
                     atomicMin(&sh.first, item + k);
@@ -635,9 +636,8 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 const int tile = pc == 1 ? local : local / pc, piece = pc == 1 ? 0 : local % pc;
                 int tiles;
                 ChunkItem it = row_tile<MODE>(a, sh.spans[q], tile, &tiles);
-                const int from = MODE == kChunkGroups ? it.base / kChunkKeys : t0;
-                it.t_lo = from + min(tiles, piece * sh.piece_tiles[q]);
-                it.t_hi = from + min(tiles, (piece + 1) * sh.piece_tiles[q]);
+                it.t_lo = t0 + min(tiles, piece * sh.piece_tiles[q]);
+                it.t_hi = t0 + min(tiles, (piece + 1) * sh.piece_tiles[q]);
                 if (pc > 1 || (MODE == kChunkGroups && sh.spans[q].group != kOwn)) it.slot = sh.slot0[q] + local;
                 items[x0 + k] = it;
             }

@@ -28,7 +28,9 @@
 namespace splash {
 
 constexpr int kPlanThreads = 512;         // threads of the block
-constexpr int kEvenTiles = 2;             // row tiles of an even cut per thread, at most
+// Row tiles of an even cut per thread (one makes shorter code, and grouped calls take the even cut more often).
+template <int MODE>
+constexpr int even_tiles = MODE == kChunkGroups ? 1 : 2;
 constexpr int kCuts = 4;                  // piece lengths tried: an even share of 1..4 rounds of the pairs
 // Costs in key tiles (1.15 us each): what an item costs beside its tiles (first loads, epilogue), what a
 // partial costs to write and merge, and the merge's own latency.
@@ -63,6 +65,7 @@ struct GroupScratch {
 // The last index in [0, n) with from[i] <= x (from[0] <= x, ascending).
 __device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
     int lo = 0, hi = n;
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (from[mid] <= x) lo = mid;
@@ -283,6 +286,7 @@ __device__ __forceinline__ float gain_of_sharing(const ChunkArgs& a, int m, int 
 __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh) {
     GroupScratch& gs = sh.groups;
     int2 bad = {0, 0};
+#pragma unroll 1
     for (int g = threadIdx.x; g <= a.groups; g += kPlanThreads) {
         const int r = a.cu_groups[g];
         gs.cu[g] = min(max(r, 0), a.B);
@@ -292,6 +296,7 @@ __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, active = warps_of(a.groups);
     if (warp < active) {
         float gain = 0.f;
+#pragma unroll 1
         for (int g = threadIdx.x; g < a.groups; g += kPlanThreads) {
             const int r0 = gs.cu[g], r1 = gs.cu[g + 1], given = a.prefix_lens[g];
             const int p = min(max(given, 0), a.max_ctx);
@@ -309,8 +314,10 @@ __device__ __forceinline__ int2 read_groups(const ChunkArgs& a, PlanScratch& sh)
     __syncthreads();
     if (warp < active) {
         float all = 0.f;
+#pragma unroll 1
         for (int w = 0; w < active; ++w) all += sh.totals[w].f;
         if (all <= kMergeCost * float(a.pairs))
+#pragma unroll 1
             for (int g = threadIdx.x; g < a.groups; g += kPlanThreads)
                 if (gs.prefix[g] >= 0) gs.prefix[g] = ~gs.prefix[g];
     }
@@ -358,6 +365,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     if (warp < active) {
         Totals sum = {};
         sum.flags = (bad.x ? kBadLength : 0) | (bad.y ? kBadOrder : 0);
+#pragma unroll 1
         for (int r = tid; r < B; r += NT) {
             const Span s = span_of<MODE>(a, r, sh.groups);
             if (r == tid) mine = s;
@@ -388,7 +396,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
                           (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
                           tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
-        const bool even_fits = room && U <= kEvenTiles * NT && a.pairs <= 256 && !(sum.flags & kFarApart);
+        const bool even_fits = room && U <= even_tiles<MODE> * NT && a.pairs <= 256 && !(sum.flags & kFarApart);
         if (MODE == kChunkGroups && even_fits && (sum.flags & kShared)) {
             is_even = true;                        // (the results of most row tiles are merged anyhow)
         } else {
@@ -425,6 +433,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
     if (sh.choice.cuts) {
         if (warp < active) {
             int n[2 * kCuts] = {};
+#pragma unroll 1
             for (int r = tid; r < B; r += NT) {
                 const Span s = r == tid ? mine : span_of<MODE>(a, r, sh.groups);
 #pragma unroll
@@ -447,6 +456,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             const float C = sh.choice.C, G = float(a.pairs);
             int items_n = 0, slots_n = 0;
             if (lane < kCuts)
+#pragma unroll 1
                 for (int w = 0; w < active; ++w) {
                     items_n += sh.cuts[w][lane];
                     slots_n += sh.cuts[w][kCuts + lane];
@@ -483,6 +493,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         constexpr int E = decltype(row_tiles_a_thread)::value;
         ChunkItem it[E] = {};
         int tiles[E] = {}, group[E], base = 0;
+#pragma unroll 1
         for (int r0 = 0; r0 < B; r0 += NT) {
             const Span s = r0 + tid >= B ? Span{} : (r0 == 0 ? mine : span_of<MODE>(a, r0 + tid, sh.groups));
             int v[1] = {s.u}, tot[1];
@@ -593,15 +604,13 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         num_splits = totals[2];
     };
     if (is_even) {
-        // (a row tile a thread is shorter where that is enough, but the other forms seldom come here, and a second
-        // copy of the code costs them 1 us)
-        if (MODE == kChunkGroups && U <= NT) cut_even(std::integral_constant<int, MODE == kChunkGroups ? 1 : kEvenTiles>{});
-        else cut_even(std::integral_constant<int, kEvenTiles>{});
+        cut_even(std::integral_constant<int, even_tiles<MODE>>{});
     } else {
         // item i is the (i / pairs)-th of pair i mod pairs, whose items lie next to each other
         const int per_pair = a.by_pairs(dealt + a.pairs - 1);
         const int64_t x0 = int64_t(pair) * per_pair;
         int slot_base = 0, base = 0;
+#pragma unroll 1
         for (int r0 = 0; r0 < B; r0 += NT) {
             const int r = r0 + tid;
             Span s = {};
@@ -631,6 +640,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
             __syncthreads();
             // this pair's items among the batch's [base, base + tot[0])
             const int k0 = a.by_pairs(base - pair + a.pairs - 1);
+#pragma unroll 1
             for (int k = (k0 > 0 ? k0 : 0) + tid;; k += NT) {
                 const int64_t i = int64_t(k) * a.pairs + pair - base;
                 if (i >= tot[0]) break;
@@ -645,6 +655,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 items[x0 + k] = it;
             }
             if (writer)
+#pragma unroll 1
                 for (int i = tid; i < tot[2]; i += NT) {
                     const int q = last_at_most(sh.split0, min(NT, B - r0), i);   // (others share a start with the next split request)
                     int tiles;

@@ -237,6 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (i + 1 < range.y) next = items[i + 1];
             if (it.t_lo >= it.t_hi) continue;
             const int2 at = q_at(it);
+#pragma unroll 1
             for (int g = 0; g < kKGroups && ok && second == fresh; ++g) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[g], qph ^ 1, abort_flag, status))) { ok = false; break; }
                 const uint32_t bar = map_to_rank(smem_u32(&q_full[g]), 0);
@@ -268,6 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     else if (key + R > first_key<MODE>(a, it) && key < min(it.ctx, a.tok_hi) && !second)   // a page of the share
                         atomicOr(status, uint32_t(SPLASH_DEVICE_BAD_INPUT));
                 }
+#pragma unroll 1
                 for (int g = 0; g < kKGroups; ++g) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[g], ph ^ 1, abort_flag, status))) {
                         ok = false;
@@ -324,6 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int id = page_of(a, table, key, it.ctx);
                     if (id >= 0) row = (id << a.P_log) + (key & (a.P - 1));
                 }
+#pragma unroll 1
                 for (int hh = 0; hh < 2; ++hh) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[hh], ph ^ 1, abort_flag, status))) {
                         ok = false;
@@ -344,8 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int n = it.ctx - __shfl_sync(0xffffffffu, key, src);   // valid rows, 0 < n < R
                         if (lane < 4) {
                             const uint32_t d0 = sv + src * R * 512 + lane * R * 128;
+#pragma unroll 1
                             for (int o = 0, b = 2; o < R;) {        // runs of 16, 4 and 1 rows
                                 const int end = o < n ? n : R;
+#pragma unroll 1
                                 while (o + (1 << 2 * b) > end) --b;
                                 tma_pair_3d(d0 + o * 128, &maps.rows[b], bar, 0, o < n ? y + o : past, 4 * int(rank) + lane);
                                 o += 1 << 2 * b;
@@ -477,6 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = it.t_lo; t < it.t_hi; ++t, ++g) {
                 const int key0 = MODE != kChunkPlain ? tile_key<MODE>(a, it, t, half) + part * 32 : t * kChunkKeys + share * 32;
                 uint32_t gone = 0;               // bit k: this thread's keys k R .. have no page
+#pragma unroll 1
                 for (int k = 0; k * R < 32; ++k)
                     if (key0 + k * R < it.ctx && page_of(a, table, key0 + k * R, it.ctx) < 0) gone |= 1u << k;
                 if (!__all_sync(0xffffffffu, mbar_wait(&s_full[g & 1], (g >> 1) & 1, abort_flag, status)))

@@ -31,6 +31,7 @@ constexpr int kPlanThreads = 512;         // threads of the block
 // Row tiles of an even cut per thread (one makes shorter code, and grouped calls take the even cut more often).
 template <int MODE>
 constexpr int even_tiles = MODE == kChunkGroups ? 1 : 2;
+constexpr int kMostPairs = 256;           // an even cut is for so many pairs
 constexpr int kCuts = 4;                  // piece lengths tried: an even share of 1..4 rounds of the pairs
 // Costs in key tiles (1.15 us each): what an item costs beside its tiles (first loads, epilogue), what a
 // partial costs to write and merge, and the merge's own latency.
@@ -268,6 +269,7 @@ struct PlanScratch {
     int pieces[kPlanThreads], piece_tiles[kPlanThreads];
     Span spans[kPlanThreads];
     int first, last;
+    int bound[kMostPairs];             // an even cut's first position of every pair
     GroupScratch groups;
 };
 
@@ -396,7 +398,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         const bool room = U + (tiles_most < a.pairs ? tiles_most : a.pairs) <= a.cap_items &&
                           (MODE == kChunkGroups ? int64_t(U) + 2 * a.pairs : (tiles_most < 2 * a.pairs ? tiles_most : 2 * a.pairs)) <= a.cap_slots &&
                           tiles_most + 4 * int64_t(U) < (int64_t(1) << 31) / (a.pairs + 1);
-        const bool even_fits = room && U <= even_tiles<MODE> * NT && a.pairs <= 256 && !(sum.flags & kFarApart);
+        const bool even_fits = room && U <= even_tiles<MODE> * NT && a.pairs <= kMostPairs && !(sum.flags & kFarApart);
         if (MODE == kChunkGroups && even_fits && (sum.flags & kShared)) {
             is_even = true;                        // (the results of most row tiles are merged anyhow)
         } else {
@@ -527,12 +529,14 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         // short, and then go to their neighbours.
         const uint32_t T = uint32_t(W[0]);
         const uint32_t P = max(1u, min(uint32_t(a.pairs), T / uint32_t(own + kLeastPiece)));
+        if (tid < int(P)) sh.bound[tid] = int(uint32_t(tid) * T / P);
+        __syncthreads();
         int np[E] = {}, j0[E] = {}, j1[E] = {}, A[E] = {};
         bool no_first[E] = {};
         auto cut = [&](int e, int j) -> int {     // first tile of pair j's piece
             if (j <= j0[e]) return 0;
             if (j > j1[e]) return tiles[e];
-            const int x = int(uint32_t(j) * T / P) - A[e] - own;
+            const int x = sh.bound[j] - A[e] - own;
             return x < kLeastPiece ? 0 : (tiles[e] - x < kLeastPiece ? tiles[e] : x);
         };
         // items, partials and split row tiles

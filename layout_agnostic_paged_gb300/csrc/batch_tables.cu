@@ -207,6 +207,7 @@ __device__ __forceinline__ Gone gone_of(const BatchReleaseArgs& a, int r) {
 template <typename F>
 __device__ __forceinline__ void for_pages(const BatchReleaseArgs& a, int r0, int r1, F each) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int rb = r0; rb < r1; rb += 32) {
         const Gone g = gone_of(a, rb + lane < r1 ? rb + lane : a.B);
         uint32_t sum = uint32_t(g.n0 + g.n1);      // (a request has fewer than 2^27 pages: 32 of them fit)
@@ -217,6 +218,7 @@ __device__ __forceinline__ void for_pages(const BatchReleaseArgs& a, int r0, int
         }
         const uint32_t total = __shfl_sync(0xffffffffu, sum, 31);
         const uint32_t start = sum - uint32_t(g.n0 + g.n1);
+#pragma unroll 1
         for (uint32_t i0 = 0; i0 < total; i0 += 32) {
             const uint32_t i = i0 + lane;
             int j = 0;                             // the last request with start <= i (others share a start with the next)
@@ -284,6 +286,7 @@ __global__ void __cluster_dims__(kReleaseCtas, 1, 1) __launch_bounds__(kTableThr
         place -= __popc(m);
     });
     __syncwarp();
+#pragma unroll 1
     for (int r = r0 + lane; r < r1; r += 32) {     // (behind the last read of the warp's lengths)
         const int keep = gone_of(a, r).keep;
         a.ctx[r] = keep;

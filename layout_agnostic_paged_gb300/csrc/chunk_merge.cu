@@ -28,6 +28,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& 
     // lane s reads piece s; a NaN stays
     float m = -INFINITY;
     bool nan = false;
+#pragma unroll 1
     for (int s0 = 0; s0 < pieces; s0 += 32) {
         const float x = s0 + lane < pieces ? lse[piece(s0 + lane)] : -INFINITY;
         nan |= __any_sync(0xffffffffu, x != x);
@@ -39,6 +40,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& a, const ChunkSplit& 
     float acc[Q][4] = {};
     float l = 0.f;
     if (m != -INFINITY)
+#pragma unroll 1
         for (int s0 = 0; s0 < pieces; s0 += 32) {
             const int n = min(32, pieces - s0);
             const float x = lane < n ? lse[piece(s0 + lane)] : -INFINITY;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     const int per_split = GROUPS ? head->split_rows : 2 * kChunkRows;
     const int64_t rows = int64_t(head->num_splits) * per_split;
     const int parts = rows * 4 <= warps ? 4 : 1;
+#pragma unroll 1
     for (int64_t w = first; w < rows * parts; w += warps) {
         const int64_t r = parts == 4 ? w >> 2 : w;
         int split, row;

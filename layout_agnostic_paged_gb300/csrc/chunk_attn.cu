@@ -133,7 +133,7 @@ __device__ __forceinline__ int first_key(const ChunkArgs& a, const ChunkItem& it
 // its rows: their page may be gone, and nothing of it is read.
 template <int MODE>
 __device__ __forceinline__ int item_start(const ChunkArgs& a, const ChunkItem& it) {
-    return MODE == kChunkWindow ? it.seen + a.tile.by_heads(it.row0) - a.window : (MODE == kChunkGroups ? it.base : 0);
+    return MODE == kChunkWindow ? max(it.seen + a.tile.by_heads(it.row0), 1) - a.window : (MODE == kChunkGroups ? it.base : 0);
 }
 template <int MODE>
 __device__ __forceinline__ bool left_behind(const ChunkArgs& a, int start, int key, int n) {

@@ -84,7 +84,7 @@ __device__ __forceinline__ int key_tiles(const ChunkArgs& a, int lo, int first, 
     if (e <= lo) return 0;
     if constexpr (MODE == kChunkWindow) {
         const int b0 = lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
-        const int w = max(b0 + a.sink_blocks, max(first - a.window, 0) / kChunkRows);
+        const int w = max(b0 + a.sink_blocks, max(max(first, 1) - a.window, 0) / kChunkRows);
         if (base) *base = w - a.sink_blocks;
         return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
     }

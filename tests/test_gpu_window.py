@@ -199,6 +199,18 @@ def test_a_workspace_serves_windowed_and_plain_calls():
         assert_chunk(b, out, lse, attention_reference(b, 0, 128, window, 4), 0, 128, f"window {window}")
 
 
+@pytest.mark.parametrize("page,heads", [(16, 16), (64, 128)])
+def test_more_new_tokens_than_the_context_holds(page, heads):
+    # the first rows lie before the first position and see nothing
+    b = Batch([40, 3], [300, 90], heads, page, 21, DEV)
+    b.ctx[0], b.keys[0] = 30, b.keys[0][:30]
+    b.ctx_t[0] = 30
+    for window, sinks in ((5, 2), (200, 0)):
+        out, lse, ws = run(b, window, sinks)
+        assert S.splash_workspace_status(ws) == 0 and (out[:10] == 0).all() and torch.isinf(lse[:10]).all()
+        assert_chunk(b, out, lse, attention_reference(b, 0, heads, window, sinks), 0, heads, f"window {window}")
+
+
 def test_refusals():
     b = Batch([1], [5], 8, 16, 1, DEV)
     for kw in (dict(window=-1, sinks=0), dict(window=5, sinks=-1)):

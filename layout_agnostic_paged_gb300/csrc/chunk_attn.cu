@@ -36,12 +36,27 @@
 //
 // Measured.  The last 1,024 tokens of a 16K-token prompt, 128 heads (4.53 TFLOP): 2.52 ms, 1,795 TF/s,
 // 93% of the library's burst rate for matrix products and more than its sustained one: the SMs run at
-// 1.6 GHz there, held by power.  16 requests of 1-256 tokens over up to 3,840: 0.975 ms
-// (89%).  Four whole prompts of 257-1,024 tokens: 0.26 ms (51%), an item being three tiles long on average
+// 1.6 GHz there, held by power.  16 requests of 1-256 tokens over up to 3,840: 0.975 to 1.07 ms (81 to
+// 89%).  Four whole prompts of 257-1,024 tokens: 0.24 ms (55%), an item being three tiles long on average
 // and the causal edge half of one; what is left is the chain from an item's last scores over
 // their softmax and O to the next item's first (6,400 clocks for an item of one tile).  64 requests of 4
-// drafted tokens, 16 heads, over 512-4,096 (173 MB): 54 us, 3.2 TB/s: 15 tiles a pair, each held
+// drafted tokens, 16 heads, over 512-4,096 (173 MB): 51 us, 3.4 TB/s: 15 tiles a pair, each held
 // by the latency of its keys, between the start (5 us) and the merge (6 us).
+//
+// Windows.  A token sees its last keys and some first ones, two ranges that move from row tile to row tile.  They are
+// laid end to end in blocks of 64 keys, two to a tile, so that four first tokens cost half a tile and a window
+// begins within 64 keys of its first.  1,024 tokens over a window of 4,096 and 64 first tokens, 128 heads: 0.67 to 0.73 ms,
+// 83 to 90% of the library's rate; three prompts of 700-2,600 tokens over a window of 512: 0.47 to 0.52 ms, 54 to 60%: an
+// item is five tiles for 516 keys, and its Q (72 KB a CTA) comes in at the same 62 bytes a clock as its keys.
+//
+// Groups.  Requests with a common prefix have its keys multiplied with all their rows at once: the group's rows make
+// row tiles of their own, every row tile's result is a partial one, and the merge joins a request's with its group's.
+// 256 single tokens of 16 heads behind 32,768 shared keys: 0.22 ms (68% of the library's rate) where each by itself takes
+// 2.0 ms; 64 behind 8,192: 39 us, of which the tiles take 14.
+//
+// Code length counts: the roles' loops share an instruction cache, and a launch fetches the code of its first tiles
+// anew.  Loops of the loading warps that are not unrolled took whole prompts from 254 to 242 us, the plan's decisions in one
+// copy each drafted tokens from 52.4 to 51.5 us.
 //
 // The tensor cores' fp32 additions truncate, so O comes out small where one item sums very many keys: by
 // 0.05% over 131,072 keys and 0.44% over a million, measured with values of one sign, which is the worst case

@@ -107,7 +107,7 @@ struct BatchReleaseArgs {
     int window, sinks;            // window 0: none
 };
 constexpr int kReleaseCtas = 8;
-constexpr int kSmallBatchRows = 2048;   // up to so many rows one CTA writes them all
+constexpr int kSmallBatchRows = 2048;   // up to so many rows one CTA writes them all, two for each of its threads
 cudaError_t launch_batch_tables(const BatchTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_batch_release(const BatchReleaseArgs& a, cudaStream_t stream);
 

@@ -51,8 +51,8 @@
 //
 // Groups.  Requests with a common prefix have its keys multiplied with all their rows at once: the group's rows make
 // row tiles of their own, every row tile's result is a partial one, and the merge joins a request's with its group's.
-// 256 single tokens of 16 heads behind 32,768 shared keys: 0.22 ms (68% of the library's rate) where each by itself takes
-// 2.0 ms; 64 behind 8,192: 39 us, of which the tiles take 14.
+// 256 single tokens of 16 heads behind 32,768 shared keys: 0.22 to 0.23 ms (68% of the library's rate) where each by itself
+// takes 1.28 ms; 64 behind 8,192: 39 us instead of 103, of which the tiles take 14.
 //
 // Code length counts: the roles' loops share an instruction cache, and a launch fetches the code of its first tiles
 // anew.  Loops of the loading warps that are not unrolled took whole prompts from 254 to 242 us, the plan's decisions in one

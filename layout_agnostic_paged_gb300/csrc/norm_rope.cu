@@ -11,7 +11,7 @@
 // in the row, the weights and the tokens' cos / sin are worked out once for all of them.
 //
 // What bounds it is the issue of instructions, not HBM: 73% of all issue slots in the large case.  With a block per
-// token it took 25 instructions an element; now 17, the products and sums two to an instruction.  8,191 tokens x 72
+// token it took 25 instructions an element; now 18, the products and sums two to an instruction.  8,191 tokens x 72
 // heads x 128 dims in bf16, half of them rotated (302 MB): 50.2 us, 6.0 TB/s, 90% of the copy bandwidth (47.3 us in fp32 with half
 // the tokens); 32,768 latent rows of 576 dims, whose 32 angles serve one row each: 23.3 us (48%); 256 tokens x 18 heads:
 // 3.2 us.

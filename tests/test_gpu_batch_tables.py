@@ -129,7 +129,7 @@ def test_lengths_around_page_borders():
     check_build(Cache([p for p, _ in both], [n for _, n in both], P, 500))
 
 
-@pytest.mark.parametrize("rows", [2047, 2048, 2049, 2052])
+@pytest.mark.parametrize("rows", [2047, 2048, 2049, 4095, 4096, 4097, 4100])
 def test_rows_at_the_border_of_the_two_forms(rows):
     check_build(Cache([5, 0, 77], [rows - 901, 900, 1], 64, 200))
 

@@ -172,6 +172,16 @@ def test_nothing():
     check_build(Cache([0, 0], [0, 0], 16, 0, rows=4, width=1))
 
 
+def test_a_table_without_pages():
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32, device=DEV)
+    past, new, table, left = i(3), torch.tensor([0, 0, 1], dtype=torch.int32, device=DEV), i(3, 0), i(2)
+    cu, ctx, pos, slots = i(4), i(3), i(5), i(5)
+    S.splash_batch_tables(past, new, table, 16, i(0), left[:1], cu, ctx, pos, slots, left)
+    assert left.tolist() == [0, 2] and cu.tolist() == [0] * 4 and ctx.tolist() == [0] * 3
+    S.splash_batch_release(ctx, None, table, 16, i(0), left)
+    assert ctx.tolist() == [0] * 3 and left[0].item() == 0
+
+
 def test_counts_out_of_range_are_clamped():
     c = Cache([0, 0], [9, 9], 16, 2)
     c.device()

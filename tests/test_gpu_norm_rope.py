@@ -206,6 +206,19 @@ def test_a_captured_call_replays_and_streams_run_side_by_side():
     assert all(torch.equal(o, want) for o in outs)
 
 
+def test_rows_that_are_read_more_than_once():
+    # a token's key for every head, and one row for every token: strides of zero
+    x = make((7, 1, 128), torch.bfloat16, 12)
+    w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    pos = torch.arange(7, dtype=torch.int32, device=DEV)
+    rope = S.make_rope_desc(64, interleaved=False)
+    compare.dtype = torch.bfloat16
+    for src in (x.expand(7, 5, 128), x[2:3].expand(7, 5, 128)):
+        out = torch.empty(7, 5, 128, dtype=torch.bfloat16, device=DEV)
+        S.splash_norm_rope(src, w, out, None, None, None, pos, rope, 1e-6)
+        compare(out, *reference(src, w, pos, {}, 64, 1e-6, 128, 0, interleaved=False))
+
+
 def test_refusals_of_the_binding():
     x, out = make((4, 2, 64), torch.bfloat16, 1), make((4, 2, 64), torch.bfloat16, 2)
     w, pos = torch.ones(64, dtype=torch.bfloat16, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)

@@ -258,6 +258,28 @@ def test_all_heads_of_128_are_the_plain_call():
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+def test_calls_without_requests_or_tokens_clear_the_status():
+    b = shared([(1024, SINGLE(40))], 16, 64, 94)
+    good, ws = b.cu_groups, None
+    b.cu_groups = ints([5, 3])
+    _, _, ws = run(b)
+    assert S.splash_workspace_status(ws) == S.SPLASH_DEVICE_BAD_INPUT
+    S.splash_chunk_attn_ex(b.q[:0], b.pool, torch.zeros_like(b.cu), b.table, b.ctx_t, 0, 16, 0, -1,
+                           torch.empty(0, 16, 512, device=DEV), torch.empty(0, 16, device=DEV), ws, b.scale, cu_groups=good,
+                           prefix_lens=b.prefix)
+    assert S.splash_workspace_status(ws) == 0
+    S.splash_chunk_attn_ex(b.q, b.pool, b.cu[:1], b.table[:0], b.ctx_t[:0], 0, 16, 0, -1,
+                           torch.empty(b.rows, 16, 512, device=DEV), torch.empty(b.rows, 16, device=DEV), ws, b.scale,
+                           cu_groups=ints([0, 0]), prefix_lens=ints([64]))
+    assert S.splash_workspace_status(ws) == 0
+
+
+def test_as_many_groups_as_there_can_be():
+    b = shared([(512, SINGLE(40)), (800, SINGLE(40, 1))], 16, 64, 95)
+    b.cu_groups, b.prefix = ints([0] * 1023 + [40, 80]), ints([9] * 1022 + [512, 800])
+    check(b, "1,024 groups")
+
+
 def test_refusals():
     b = shared([(100, SINGLE(4))], 16, 64, 93)
     small = S.chunk_workspace(b.q, b.pool, b.table, b.scale)

@@ -348,7 +348,8 @@ typedef struct {
  * outside [0, num_pages) has no page: it is passed over.  The pages go on so that the first request's first one lies
  * on top: after splash_batch_tables, dropping the same new tokens puts the stack back as it was.
  * A page that several requests share must be kept by all of them but one, or it is on the list more than
- * once.  Pages that do not fit on the stack are lost.  No two arrays may overlap (keep_lens may be ctx_lens).
+ * once.  Pages that do not fit on the stack are lost.  num_reqs * max_pages_per_req is below 2^31.  No two arrays may
+ * overlap (keep_lens may be ctx_lens).
  */
 SPLASH_API int splash_batch_release(const splash_batch_drop* drop, splash_stream_t stream);
 

@@ -589,6 +589,7 @@ int splash_batch_release(const splash_batch_drop* d, splash_stream_t stream) {
     const int st = batch_shape_error(d->num_reqs, d->page_size, d->num_pages, d->max_pages_per_req);
     if (st != SPLASH_OK) return st;
     if (d->window < 0 || d->sinks < 0) return SPLASH_ERR_INVALID_ARG;
+    if (int64_t(d->num_reqs) * d->max_pages_per_req >= (int64_t(1) << 31)) return SPLASH_ERR_UNSUPPORTED;
     if (d->num_reqs == 0 || d->max_pages_per_req == 0) return SPLASH_OK;
     if (!d->ctx_lens || !d->block_table || !d->free_count || (d->num_pages > 0 && !d->free_pages))
         return SPLASH_ERR_INVALID_ARG;

@@ -258,6 +258,44 @@ def test_long_requests():
     check_release(c, ctx, [17, 12, 0])
 
 
+def check_sparse(B, most, P, ctx_lo, keep_lo, window, sinks, holes, seed):
+    """Tables with entries that went back before (a share `holes` of them) and that never were pages, against a mask."""
+    g = torch.Generator().manual_seed(seed)
+    ints = lambda lo, hi, *n: torch.randint(lo, hi, n, generator=g, dtype=torch.int32)
+    pages = 1 << 20
+    table = ints(-5, pages + 40, B, most)
+    table[torch.rand(B, most, generator=g) < holes] = -1
+    ctx = ints(ctx_lo, most * P + 1, B)
+    keep = torch.minimum(ints(keep_lo, most * P + 1, B), ctx) if keep_lo is not None else ctx.clone()
+    page = torch.arange(most)
+    kept = -(-keep // P)
+    gone = (page >= kept[:, None]) & (page < -(-ctx[:, None] // P))
+    if window:
+        gone |= (page * P >= sinks) & ((page + 1) * P <= keep[:, None] + 1 - window)
+    ids = table[gone & (table >= 0) & (table < pages)]
+    top = 11
+    want = torch.full((pages,), -7, dtype=torch.int32)
+    n = min(len(ids), pages - top)
+    assert n == len(ids)
+    want[top:top + n] = ids.flip(0)
+    t, c, stack = table.to(DEV), ctx.to(DEV), torch.full((pages,), -7, dtype=torch.int32, device=DEV)
+    left = torch.tensor([top, 5], dtype=torch.int32, device=DEV)
+    S.splash_batch_release(c, keep.to(DEV) if keep_lo is not None else None, t, P, stack, left, window, sinks)
+    assert torch.equal(stack.cpu(), want) and left.tolist() == [top + n, 5] and torch.equal(c.cpu(), keep)
+    assert torch.equal(t.cpu(), torch.where(gone, -1, table))
+
+
+# runs of a warp within one request and over many; several passes over the requests; more groups than there are marks
+@pytest.mark.parametrize("B,most,P,ctx_lo,keep_lo,window,sinks,holes", [
+    (1, 3000, 64, 180000, None, 4096, 4, .5), (1, 9000, 16, 140000, 0, 0, 0, .0), (64, 2048, 64, 100000, None, 4096, 100, .999),
+    (5, 2100, 128, 0, 0, 1000, 300, .3), (1024, 40, 16, 0, 0, 100, 17, .2), (1025, 40, 16, 0, 0, 100, 17, .2),
+    (3000, 70, 32, 0, None, 64, 0, .9), (4100, 3, 16, 0, 0, 0, 0, .5), (2500, 900, 16, 10000, None, 500, 1, .8),
+    (3, 750000, 16, 11000000, None, 2048, 1, .95), (2049, 1200, 16, 19000, 19000, 333, 0, .97),
+])
+def test_pages_that_went_back_before(B, most, P, ctx_lo, keep_lo, window, sinks, holes):
+    check_sparse(B, most, P, ctx_lo, keep_lo, window, sinks, holes, B + most)
+
+
 def test_a_full_stack_and_bad_counts():
     c, ctx = built([16, 16, 16], [1, 1, 1], 16, 5)
     c.free = c.num_pages - 2                       # a count that does not fit the pages that are out

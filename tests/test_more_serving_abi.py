@@ -56,7 +56,7 @@ def release(lib, reqs=2, page=16, pages=11, most=7, window=0, sinks=0, ctx=FAKE,
 @pytest.mark.parametrize("kw,code", [
     (dict(ctx=0), INVALID), (dict(table=0), INVALID), (dict(free=0), INVALID), (dict(count=0), INVALID),
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(keep=FAKE + 2), INVALID), (dict(table=FAKE + 1), INVALID),
-    (dict(page=8), UNSUPPORTED), (dict(reqs=-1), INVALID),
+    (dict(page=8), UNSUPPORTED), (dict(reqs=-1), INVALID), (dict(reqs=1 << 10, most=1 << 21), UNSUPPORTED),
 ])
 def test_release_rejects_bad_arguments(lib, kw, code):
     assert release(lib, **kw) == code

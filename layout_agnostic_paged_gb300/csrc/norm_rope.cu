@@ -17,6 +17,9 @@
 // 3.2 us.
 #include <limits.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,7 +37,7 @@ constexpr int kNormUnits = 4;        // units of a lane, at most
 // the large prompt; three: 24.1 to 21.7 for 2,000 tokens x 17 heads x 576 dims, with 24 bytes spilled; two more are slower).
 template <int K>
 constexpr int kNormBlocks = K == 1 ? 8 : (K == 3 ? 4 : 1);
-constexpr int kNormPairs = 1024;     // cos / sin a block holds, at most (one token has 128 at most)
+constexpr int kNormPairs = 2048;     // cos / sin a block holds, at most (one token has 128 at most)
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -305,15 +308,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
     }
 }
 
-// The rows of a side's blocks: one row a lane where there are few, up to kNormPasses where the blocks still fill the GPU
-// several times over.
-void plan_side(const NormArgs& a, int sms, NormRows* s) {
+// The rows of a side's blocks, `passes` to a lane.
+void plan_side(const NormArgs& a, int64_t passes, NormRows* s) {
     s->blocks = 0;
     if (s->H == 0) return;
     const int64_t rows = int64_t(a.T) * s->H;
     const int groups = kNormThreads / a.G;
-    int64_t passes = int64_t(a.T) * (a.q.H + a.k.H) / (int64_t(sms) * 8 * groups);
-    passes = passes < 1 ? 1 : (passes > kNormPasses ? kNormPasses : passes);
     int64_t per = passes * groups;
     // the tokens that so many rows can touch have to fit the table
     if (a.dims > 0) {
@@ -332,13 +332,29 @@ void plan_side(const NormArgs& a, int sms, NormRows* s) {
 
 template <typename T, bool INTER, int VE, int K>
 cudaError_t launch_units(NormArgs& a, int sms, cudaStream_t stream) {
-    plan_side(a, sms, &a.q);
-    plan_side(a, sms, &a.k);
+    const auto kernel = norm_rope_kernel<T, INTER, VE, K>;
+    static std::atomic<int> most{0};                   // blocks that an SM's registers have room for
+    int per_sm = most.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kNormThreads, 0);
+        if (e != cudaSuccess) return e;
+        most.store(per_sm, std::memory_order_relaxed);
+    }
+    // As many rows a lane as make whole waves of blocks
+    const int64_t wave = int64_t(per_sm) * sms, work = int64_t(a.T) * (a.q.H + a.k.H) * a.G / kNormThreads + 1;
+    const int64_t waves = (work + wave * kNormPasses - 1) / (wave * kNormPasses);
+    int64_t passes = (work + wave * waves - 1) / (wave * waves);
+    for (;; ++passes) {
+        plan_side(a, passes, &a.q);
+        plan_side(a, passes, &a.k);
+        if (passes >= kNormPasses || a.q.blocks + a.k.blocks <= wave * waves) break;
+    }
     // (with room for the gaps between runs)
     a.weight_len = (a.norm_dims + 7) / 8 * 12;
-    const size_t smem = size_t(a.weight_len) * sizeof(float) + (a.dims > 0 ? size_t(kNormPairs) * 3 * sizeof(float) : 0);
-    return launch_pdl(norm_rope_kernel<T, INTER, VE, K>, dim3(static_cast<unsigned>(a.q.blocks + a.k.blocks)), dim3(kNormThreads),
-                      smem, stream, a);
+    auto pairs = [&](const NormRows& s) { return s.blocks ? ((s.rows_per_block + s.H - 2) / s.H + 1) * (a.dims / 2) : 0; };
+    const int held = std::max(pairs(a.q), pairs(a.k));
+    const size_t smem = (size_t(a.weight_len) + size_t(held + 7) / 8 * 24) * sizeof(float);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.q.blocks + a.k.blocks)), dim3(kNormThreads), smem, stream, a);
 }
 
 template <typename T, bool INTER>

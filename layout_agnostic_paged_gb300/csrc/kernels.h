@@ -135,7 +135,7 @@ struct NormArgs {
     // set by the launcher
     float inv_n;
     int weight_len;               // floats of a weight array in shared memory
-    int units, rot_units, plain_units;   // of a row: two vectors each, the rotated ones first
+    int units, rot_units, plain_pairs;   // of a row, the rotated ones first; units of two other vectors (the rest: one)
     int G, G_log;                 // lanes of a row
 };
 // vectors: pointers, strides and the parts of a row allow 16-byte vectors, whose pairs lie in one unit.

@@ -13,8 +13,8 @@
 // What bounds it is the issue of instructions, not HBM: 73% of all issue slots in the large case.  With a block per
 // token it took 25 instructions an element; now 18, the products and sums two to an instruction.  8,191 tokens x 72
 // heads x 128 dims in bf16, half of them rotated (302 MB): 50.2 us, 6.0 TB/s, 90% of the copy bandwidth (47.3 us in fp32 with half
-// the tokens); 32,768 latent rows of 576 dims, whose 32 angles serve one row each: 23.3 us (48%); 256 tokens x 18 heads:
-// 3.2 us.
+// the tokens); 1,024 tokens x 129 latent heads x 576 dims 54.6 us (82%); 32,768 latent rows of 576 dims, whose 32 angles
+// serve one row each: 19.1 us (58%); 256 tokens x 18 heads: 3.2 us.
 #include <limits.h>
 
 #include <algorithm>
@@ -34,7 +34,8 @@ constexpr int kNormThreads = 128;    // a block's, at most
 constexpr int kNormPasses = 8;       // rows of a lane one after the other, at most
 constexpr int kNormUnits = 4;        // units of a lane, at most
 // Blocks an SM has room for: one more than the compiler's choice of registers leaves (a unit a lane: 52.5 to 50.6 us for
-// the large prompt; three: 24.1 to 21.7 for 2,000 tokens x 17 heads x 576 dims, with 24 bytes spilled; two more are slower).
+// the large prompt; three: 24.1 to 21.7 for 2,000 tokens x 17 heads x 576 dims at that time; one more still takes
+// 22 us there where this takes 17.8).
 template <int K>
 constexpr int kNormBlocks = K == 1 ? 8 : (K == 3 ? 4 : 1);
 constexpr int kNormPairs = 2048;     // cos / sin a block holds, at most (one token has 128 at most)
@@ -99,8 +100,10 @@ __device__ __forceinline__ float range_scale(float ss, float eps) {
     return ss < __uint_as_float((127u - 110u) << 23) && eps < __uint_as_float((127u - 80u) << 23) ? up : 1.f;
 }
 
-// VE elements a vector, K units a lane.
-template <typename T, bool INTER, int VE, int K>
+// VE elements a vector, K units a lane.  SINGLE: the last of them has one vector, which leaves out the other's
+// instructions (576 dims are five places on 16 lanes, not six: 1,024 tokens x 129 heads 59.2 to 54.6 us.  Left out at run time
+// they cost 3 us more than they save).
+template <typename T, bool INTER, int VE, int K, bool SINGLE>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel(const __grid_constant__ NormArgs a) {
     // Weights and cos / sin in runs with gaps, so that lanes at different runs read different banks.
     constexpr int kWRun = VE >= 8 ? VE + 4 : VE;
@@ -132,11 +135,13 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
             eb[k] = ea[k] + (INTER && VE == 1 ? 1 : half);
         } else if (u < a.units) {
             // (the later half first: with half of a row rotated, lanes then meet in no bank of the weights)
-            const int p = u - a.rot_units, other = p + a.plain_units;
-            eb[k] = p * VE < a.rope_lo ? p * VE : p * VE + a.dims;
-            if (other * VE < a.width - a.dims) ea[k] = other * VE < a.rope_lo ? other * VE : other * VE + a.dims;
+            const int p = u - a.rot_units, first = p < a.plain_pairs ? p : p + a.plain_pairs, other = p + a.plain_pairs;
+            eb[k] = first * VE < a.rope_lo ? first * VE : first * VE + a.dims;
+            if (p < a.plain_pairs) ea[k] = other * VE < a.rope_lo ? other * VE : other * VE + a.dims;
         }
     }
+    // no lane has the vector (k, s)
+    auto none = [](int k, int s) constexpr { return SINGLE && k == K - 1 && s == 0; };
     // the lane's next row: token and head counted from t0 and 0, and where it lies
     int i = tid >> a.G_log, token = (h0 + i) / H, h = h0 + i - token * H;
     const T* px = static_cast<const T*>(side.x) + int64_t(t0 + token) * side.xt + int64_t(h) * side.xh;
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
         r.token = token;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (ea[k] >= 0) load_vec<T, VE>(r.v[k][0], px + ea[k]);
+            if (!none(k, 0) && ea[k] >= 0) load_vec<T, VE>(r.v[k][0], px + ea[k]);
             if (eb[k] >= 0) load_vec<T, VE>(r.v[k][1], px + eb[k]);
         }
         i += groups;
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if ((s ? eb[k] : ea[k]) < a.norm_dims) {
+                    if (!none(k, s) && (s ? eb[k] : ea[k]) < a.norm_dims) {
                         if constexpr (VE == 1) sum[0] = fmaf(x[k][s][0], x[k][s][0], sum[0]);
                         else {
 #pragma unroll
@@ -208,8 +213,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
+                if (!none(k, s))
 #pragma unroll
-                for (int e = 0; e < VE; ++e) x[k][s][e] = to_f32(row.v[k][s][e]);
+                    for (int e = 0; e < VE; ++e) x[k][s][e] = to_f32(row.v[k][s][e]);
         squares();
         const float scale = range_scale(ss, a.eps);
         if (__any_sync(0xffffffffu, scale != 1.f)) {
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if ((s ? eb[k] : ea[k]) < a.norm_dims)
+                    if (!none(k, s) && (s ? eb[k] : ea[k]) < a.norm_dims)
 #pragma unroll
                         for (int e = 0; e < VE; ++e) x[k][s][e] *= scale;
             squares();
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int e0 = s ? eb[k] : ea[k];
-                if (e0 >= 0 && e0 < a.norm_dims) {
+                if (!none(k, s) && e0 >= 0 && e0 < a.norm_dims) {
                     alignas(16) float w[VE];
                     const float* from = wts + e0 / VE * kWRun;
 #pragma unroll
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
                 }
             }
             const int unit = lane + k * a.G;
-            if (unit < a.rot_units) {
+            if (!none(k, 0) && unit < a.rot_units) {
                 if constexpr (INTER && VE > 1) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int e0 = s ? eb[k] : ea[k];
-                if (e0 >= 0) {
+                if (!none(k, s) && e0 >= 0) {
                     alignas(16) T o[VE];
                     if constexpr (VE == 1) from_f32(o[0], x[k][s][0]);
                     else {
@@ -330,9 +336,9 @@ void plan_side(const NormArgs& a, int64_t passes, NormRows* s) {
     s->y_wrap = s->yt - s->H * s->yh;
 }
 
-template <typename T, bool INTER, int VE, int K>
+template <typename T, bool INTER, int VE, int K, bool SINGLE>
 cudaError_t launch_units(NormArgs& a, int sms, cudaStream_t stream) {
-    const auto kernel = norm_rope_kernel<T, INTER, VE, K>;
+    const auto kernel = norm_rope_kernel<T, INTER, VE, K, SINGLE>;
     static std::atomic<int> most{0};                   // blocks that an SM's registers have room for
     int per_sm = most.load(std::memory_order_relaxed);
     if (per_sm == 0) {
@@ -363,31 +369,40 @@ cudaError_t launch_typed(NormArgs& a, bool vectors, int sms, cudaStream_t stream
     const int ve = vectors ? V16 : 1;
     a.rot_units = a.dims / 2 / ve;
     const int plain = (a.width - a.dims) / ve;
-    a.plain_units = (plain + 1) / 2;
-    a.units = a.rot_units + a.plain_units;
+    a.plain_pairs = plain / 2;
+    a.units = a.rot_units + plain - a.plain_pairs;
     // lanes and units a lane: as few idle places as can be, then as few units
     int per_lane = 16;
+    bool single = false;
     if (vectors) {
         int best = INT_MAX;
         for (int k = 1; k <= kNormUnits; ++k) {
             int g = 0;
             while (g < 5 && (k << g) < a.units) ++g;
-            if ((k << g) >= a.units && (k << g) < best) {
-                best = k << g;
+            if ((k << g) >= a.units && (2 * k << g) < best) {
+                best = 2 * k << g;
                 per_lane = k;
                 a.G_log = g;
             }
+        }
+        // if one vector each does for the last units, the other's place is left out
+        const int before = ((per_lane - 1) << a.G_log) - a.rot_units;
+        if (per_lane == 3 && before >= 0 && plain - 2 * before <= 1 << a.G_log) {
+            single = true;
+            a.plain_pairs = before;
+            a.units = a.rot_units + plain - before;
         }
     } else {
         a.G_log = 0;
         while (a.G_log < 5 && (1 << a.G_log) < a.units) ++a.G_log;
     }
     a.G = 1 << a.G_log;
-    if (!vectors) return launch_units<T, INTER, 1, 16>(a, sms, stream);
-    if (per_lane == 1) return launch_units<T, INTER, V16, 1>(a, sms, stream);
-    if (per_lane == 2) return launch_units<T, INTER, V16, 2>(a, sms, stream);
-    if (per_lane == 3) return launch_units<T, INTER, V16, 3>(a, sms, stream);
-    return launch_units<T, INTER, V16, 4>(a, sms, stream);
+    if (!vectors) return launch_units<T, INTER, 1, 16, false>(a, sms, stream);
+    if (per_lane == 1) return launch_units<T, INTER, V16, 1, false>(a, sms, stream);
+    if (per_lane == 2) return launch_units<T, INTER, V16, 2, false>(a, sms, stream);
+    if (per_lane == 3 && single) return launch_units<T, INTER, V16, 3, true>(a, sms, stream);
+    if (per_lane == 3) return launch_units<T, INTER, V16, 3, false>(a, sms, stream);
+    return launch_units<T, INTER, V16, 4, false>(a, sms, stream);
 }
 static_assert(kMaxNormWidth <= 2 * 16 * 32, "a row of single elements: 16 units a lane");
 static_assert(kMaxNormWidth * 4 <= 2 * kNormUnits * 32 * 16, "a row of vectors");

@@ -104,6 +104,17 @@ def test_latent_rows_of_many_tokens():
     check(4099, 1, 0, 576, torch.bfloat16, 512, 512, 64)
 
 
+# several rows a lane, blocks of one wave and of several, runs that the angles' room ends, one and two vectors in the last unit
+@pytest.mark.parametrize("T,Hq,Hk,D,n,lo,dims,interleaved", [
+    (30001, 1, 0, 64, 64, 0, 64, False), (16411, 1, 1, 576, 512, 512, 64, False), (517, 33, 1, 576, 512, 512, 64, True),
+    (9001, 3, 0, 192, 128, 128, 64, True), (3001, 5, 2, 256, 256, 0, 256, False), (2503, 1, 0, 1024, 1024, 0, 64, False),
+    (777, 16, 3, 320, 320, 256, 64, False), (4001, 2, 1, 448, 448, 0, 0, True), (8009, 1, 1, 96, 96, 0, 32, True),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_rows(T, Hq, Hk, D, n, lo, dims, interleaved, dtype):
+    check(T, Hq, Hk, D, dtype, n, lo, dims, interleaved, seed=T)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lead,pad", [(0, 8), (1, 0), (0, 1), (4, 4), (3, 5), (8, 24)])
 def test_strides_and_alignments(lead, pad, dtype):

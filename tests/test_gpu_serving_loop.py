@@ -1,6 +1,9 @@
 """Steps of a serving loop from request lengths to attention (marked gpu): tables from a free list, norm and rotation
 of queries and keys, the cache, attention over a window or behind a shared prefix, and pages given back."""
 import math
+import os
+import subprocess
+import sys
 import types
 
 import numpy as np
@@ -154,3 +157,40 @@ def test_two_layers_side_by_side():
         torch.cuda.synchronize()
         for loop in loops:
             loop.verify(new, f"step {t}")
+
+
+FIRST_CALLS = """
+import torch
+from layout_agnostic_paged_gb300 import splash as S
+D = "cuda"
+ints = lambda *n: torch.zeros(*n, dtype=torch.int32, device=D)
+q, k = torch.randn(40, 16, 576, device=D).bfloat16(), torch.randn(40, 1, 576, device=D).bfloat16()
+w, pos, rope = torch.ones(512, dtype=torch.bfloat16, device=D), ints(40), S.make_rope_desc(64)
+pool, table, lens, new = torch.zeros(200, 64, 576, dtype=torch.bfloat16, device=D), ints(40, 4), ints(40), ints(40) + 1
+stack, left, cu, slots = torch.arange(200, dtype=torch.int32, device=D), ints(2) + 200, ints(41), ints(40)
+out, lse = torch.empty(40, 16, 512, dtype=torch.bfloat16, device=D), torch.empty(40, 16, device=D)
+groups, prefix = torch.tensor([0, 40], dtype=torch.int32, device=D), ints(1)
+ws, wg = S.chunk_workspace(q, pool, table, .1), S.chunk_workspace(q, pool, table, .1, num_groups=1)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    S.splash_batch_tables(lens, new, table, 64, stack, left[:1], cu, lens, pos, slots, left)
+    S.splash_norm_rope(q, w, q, k, w, k, pos, rope, 1e-6, norm_dims=512, rope_lo=512)
+    S.splash_kv_append(k[:, 0, :512], k[:, 0, 512:], cu, table, lens, pool)
+    S.splash_chunk_attn_ex(q, pool, cu, table, lens, 0, 16, 0, -1, out, lse, ws, .1, window=100, sinks=4)
+    S.splash_chunk_attn_ex(q, pool, cu, table, lens, 0, 16, 0, -1, out, lse, wg, .1, cu_groups=groups, prefix_lens=prefix)
+    S.splash_batch_release(lens, None, table, 64, stack, left, window=100, sinks=4)
+for _ in range(3):
+    g.replay()
+torch.cuda.synchronize()
+assert lens.tolist() == [3] * 40 and left.tolist() == [160, 40] and torch.isfinite(out.float()).all()
+assert S.splash_workspace_status(ws) == 0 and S.splash_workspace_status(wg) == 0
+print("replayed")
+"""
+
+
+def test_a_process_may_begin_with_a_captured_step():
+    # nothing has been launched before: kernels are loaded and their limits asked for during the capture
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr[-2000:]

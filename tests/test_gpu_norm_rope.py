@@ -247,3 +247,18 @@ def test_refusals_of_the_binding():
         a.update(kw)
         with pytest.raises(S.SplashError):
             S.splash_norm_rope(**a)
+
+
+def test_offsets_past_32_bits():
+    T, H, D, apart = 3, 2, 128, 1 << 30    # the last token's rows begin 2^31 elements on
+    buf = torch.empty(2 * apart + H * D, dtype=torch.bfloat16, device=DEV)
+    x = make((T, H, D), torch.bfloat16, 71)
+    far = torch.as_strided(buf, (T, H, D), (apart, D, 1))
+    far.copy_(x)
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    pos = torch.tensor([3, 70000, 11], dtype=torch.int32, device=DEV)
+    rope = S.make_rope_desc(64, interleaved=False)
+    compare.dtype = torch.bfloat16
+    want = reference(x, w, pos, {}, 64, 1e-6, D, 0, interleaved=False)
+    S.splash_norm_rope(far, w, far, None, None, None, pos, rope, 1e-6)
+    compare(far, *want)

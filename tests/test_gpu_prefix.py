@@ -297,3 +297,13 @@ def test_refusals():
         call(cu_groups=b.cu_groups, prefix_lens=b.prefix, window=5)
     with pytest.raises(S.SplashError, match="UNSUPPORTED"):
         call(cu_groups=torch.zeros(1026, dtype=torch.int32, device=DEV), prefix_lens=torch.zeros(1025, dtype=torch.int32, device=DEV))
+
+
+def test_a_pool_past_32_bits():
+    n = 60000                              # 4.4 GB
+    b = shared([(1000, SINGLE(33)), (2048, [(4, 7), (2, 90), (1, 0)])], 16, 64, 96)
+    few = b.pool.shape[0]
+    pool = torch.zeros(n, 64, 576, dtype=torch.bfloat16, device=DEV)
+    pool[n - few:] = b.pool
+    b.pool, b.table = pool, torch.where(b.table < 0, b.table, b.table + (n - few))
+    check(b, "the last pages of 4.4 GB")

@@ -216,3 +216,13 @@ def test_refusals():
     for kw in (dict(window=-1, sinks=0), dict(window=5, sinks=-1)):
         with pytest.raises(S.SplashError):
             run(b, **kw)
+
+
+def test_a_pool_past_32_bits():
+    n = 60000                              # 4.4 GB
+    b = Batch([1, 9, 130], [700, 333, 900], 16, 64, 60, DEV)
+    few = b.pool.shape[0]
+    pool = torch.zeros(n, 64, 576, dtype=torch.bfloat16, device=DEV)
+    pool[n - few:] = b.pool
+    b.pool, b.table = pool, torch.where(b.table < 0, b.table, b.table + (n - few))
+    check(b, "the last pages of 4.4 GB", 200, 70)

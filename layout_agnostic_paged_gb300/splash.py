@@ -341,7 +341,7 @@ def splash_kv_migrate(src_pool: torch.Tensor, dst_pool: torch.Tensor, src_ids: t
 
 def _call(dev: int, stream, where: str, fn, *args):
     """fn(*args, stream) with device `dev` current; stream None is the device's current stream."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:          # (torch is set up: there are tensors on the GPU)
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
@@ -353,9 +353,11 @@ def _call(dev: int, stream, where: str, fn, *args):
 def _device_of(where: str, *ts) -> int:
     """Index of the CUDA device that all the tensors live on."""
     dev = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError(f"{where}: tensors must live on one CUDA device")
+    for t in ts[1:]:
+        if t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError(f"{where}: tensors must live on one CUDA device")
     return dev
 
 
@@ -394,16 +396,17 @@ def splash_batch_tables(past_lens: torch.Tensor, new_lens: torch.Tensor, block_t
     """A step's arrays from its requests' lengths (all int32): takes pages for the new tokens from the top of
     the stack free_pages [num_pages] (free_count [1] entries) into block_table [B][max_pages], and writes cu_q
     [B + 1], ctx_lens [B], positions and slots [N rows] and left [2] = (free pages left, requests served).
-    ctx_lens may be past_lens, and free_count left[:1]; see splash.h for batches that do not fit."""
+    ctx_lens may be past_lens, and free_count left (its first entry is the count); see splash.h for batches that do not fit."""
     where = "splash_batch_tables"
     dev = _device_of(where, block_table)
-    if block_table.dim() != 2:
-        raise ValueError(f"{where}: block_table must be [B][max_pages]")
+    count = free_count.numel()
+    if block_table.dim() != 2 or not 1 <= count <= 2:
+        raise ValueError(f"{where}: block_table must be [B][max_pages], free_count [1] (or left [2])")
     B, pages = block_table.shape
     N, F = positions.numel(), free_pages.numel()
     _int32_arrays(where, dev, (
         ("past_lens", past_lens, B), ("new_lens", new_lens, B), ("block_table", block_table, B * pages),
-        ("free_pages", free_pages, F), ("free_count", free_count, 1), ("cu_q", cu_q, B + 1), ("ctx_lens", ctx_lens, B),
+        ("free_pages", free_pages, F), ("free_count", free_count, count), ("cu_q", cu_q, B + 1), ("ctx_lens", ctx_lens, B),
         ("positions", positions, N), ("slots", slots, N), ("left", left, 2)))
     _call(dev, stream, where, (_lib or load_library()).splash_batch_tables, _BATCH.pack(
         B, page_size, F, pages, N, 0, past_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
@@ -515,7 +518,7 @@ def splash_norm_rope(q: torch.Tensor, q_weight: torch.Tensor | None, q_out: torc
         raise ValueError(f"{where}: rows and weights must be bfloat16, float16 or float32")
     at = None
     if rope is not None:
-        if (positions is None or positions.dtype is not torch.int32 or positions.shape != (T,)
+        if (positions is None or positions.dtype is not torch.int32 or positions.numel() != T or positions.dim() != 1
                 or not positions.is_contiguous() or positions.get_device() != dev):
             raise ValueError(f"{where}: positions must be contiguous int32 [T] on q's device")
         at = positions.data_ptr()

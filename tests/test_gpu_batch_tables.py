@@ -172,6 +172,16 @@ def test_nothing():
     check_build(Cache([0, 0], [0, 0], 16, 0, rows=4, width=1))
 
 
+def test_the_count_may_be_left_itself():
+    c, other = Cache([0, 20, 64], [5, 1, 30], 16, 9), Cache([0, 20, 64], [5, 1, 30], 16, 9)
+    check_build(c)
+    d = other.device()
+    S.splash_batch_tables(d["past"], d["new"], d["table"], 16, d["stack"], d["left"], d["cu"], d["ctx"], d["pos"], d["slots"],
+                          d["left"])
+    for name in ("table", "cu", "ctx", "pos", "slots", "left"):
+        assert torch.equal(d[name], c.d[name]), name
+
+
 def test_a_table_without_pages():
     i = lambda *n: torch.zeros(*n, dtype=torch.int32, device=DEV)
     past, new, table, left = i(3), torch.tensor([0, 0, 1], dtype=torch.int32, device=DEV), i(3, 0), i(2)

@@ -12,6 +12,7 @@ constexpr int kChunkRows = 64;         // query rows of one CTA; a pair works on
 constexpr int kChunkKeys = 128;        // keys of one tile
 constexpr int kChunkKBlocks = 3;       // 64-dim blocks of the keys loaded and released together
 constexpr int kChunkMaxGroups = 1024;
+constexpr int kEarlyUnits = 2;         // units of 64 keys that a CTA asks for before the plan
 constexpr int kChunkSlotsPerPair = 8;  // partial results the workspace holds, per CTA pair
 
 // What a call's kernels are compiled for.  Each form has its own code, so that the plain one pays for nothing else.
@@ -155,6 +156,8 @@ struct ChunkArgs {
     const int32_t* cu_groups;     // grouped: [groups + 1], requests of group g from cu_groups[g] on
     const int32_t* prefix_lens;   // [groups]
     int groups;
+    int early;            // units of 64 keys that are asked for before the plan, per request
+    FastDiv by_early;
     int pairs;            // CTA pairs of the grid
     FastDiv by_pairs;
     ChunkTiling tile;

@@ -40,7 +40,7 @@
 // 89%).  Four whole prompts of 257-1,024 tokens: 0.24 ms (55%), an item being three tiles long on average
 // and the causal edge half of one; what is left is the chain from an item's last scores over
 // their softmax and O to the next item's first (6,400 clocks for an item of one tile).  64 requests of 4
-// drafted tokens, 16 heads, over 512-4,096 (173 MB): 51 us, 3.4 TB/s: 15 tiles a pair, each held
+// drafted tokens, 16 heads, over 512-4,096 (173 MB): 50 us, 3.4 TB/s: 15 tiles a pair, each held
 // by the latency of its keys, between the start (5 us) and the merge (6 us).
 //
 // Windows.  A token sees its last keys and some first ones, two ranges that move from row tile to row tile.  They are
@@ -52,7 +52,7 @@
 // Groups.  Requests with a common prefix have its keys multiplied with all their rows at once: the group's rows make
 // row tiles of their own, every row tile's result is a partial one, and the merge joins a request's with its group's.
 // 256 single tokens of 16 heads behind 32,768 shared keys: 0.22 to 0.23 ms (68% of the library's rate) where each by itself
-// takes 1.28 ms; 64 behind 8,192: 39 us instead of 103, of which the tiles take 14.
+// takes 1.28 ms; 64 behind 8,192: 37 us instead of 103, of which the tiles take 14.
 //
 // Code length counts: the roles' loops share an instruction cache, and a launch fetches the code of its first tiles
 // anew.  Loops of the loading warps that are not unrolled took whole prompts from 254 to 242 us, the plan's decisions in one
@@ -155,6 +155,25 @@ __device__ __forceinline__ bool left_behind(const ChunkArgs& a, int start, int k
     return MODE != kChunkPlain && key + n <= start && (MODE != kChunkWindow || key >= a.sinks);
 }
 
+// Asks for the first keys of every request (grouped: of every prefix) into L2 while the plan is made, during which HBM has
+// nothing else to do: block b's share of the units of 64 keys, `early` to a request.  A window over 64 single tokens 30.5 to
+// 29.0 us, drafted tokens 51.1 to 50.1, 64 single tokens behind a prefix 38.6 to 37.4.  Twice the units change nothing;
+// the smallest call (2 requests of 100 keys), whose code it lengthens, takes 10.7 us where it took 10.6.
+template <int MODE>
+__device__ __forceinline__ void ask_early(const ChunkArgs& a, int lane) {
+    const int R = min(a.P, kChunkRows), loads = kChunkRows / R;
+    const int u = int(blockIdx.x + gridDim.x * (lane / loads)), i = a.by_early(u);
+    if (lane >= kEarlyUnits * loads || i >= (MODE == kChunkGroups ? a.groups : a.B)) return;
+    const int r = MODE == kChunkGroups ? min(max(a.cu_groups[i], 0), a.B - 1) : i;
+    const int end = min(min(MODE == kChunkGroups ? a.prefix_lens[i] : a.ctx_lens[i], a.max_ctx), a.tok_hi);
+    int start = a.tok_lo;
+    if (MODE == kChunkWindow) start = max(start, end - min(max(a.cu_q[r + 1] - a.cu_q[r], 0), a.total_q) + 1 - a.window);
+    const uint32_t key = (uint32_t(start) / kChunkRows + uint32_t(u - i * a.early)) * kChunkRows + lane % loads * R;
+    if (end <= 0 || key >= uint32_t(end)) return;
+    const int id = page_of(a, a.block_table + int64_t(r) * a.max_pages, int(key), end);
+    if (id >= 0) prefetch_l2(a.kv + ((int64_t(id) << a.P_log) + (key & (a.P - 1))) * (kDqk * 2), R * kDqk * 2);
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkArgs a) {
@@ -215,7 +234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     static_assert(sizeof(PlanScratch) <= 9 * kBlk, "the plan's scratch fits in K's buffer");
     int2* planned = reinterpret_cast<int2*>(smem + kMiscOff + 24);
     {
-        const int2 r = plan_items<MODE>(a, pair, blockIdx.x == 0, *reinterpret_cast<PlanScratch*>(smem + kKOff));
+        const int2 r = plan_items<MODE>(a, pair, blockIdx.x == 0, *reinterpret_cast<PlanScratch*>(smem + kKOff),
+                                         [&]() { ask_early<MODE>(a, lane); });
         if (threadIdx.x == 0) *planned = r;
     }
     fence_proxy_async_smem();

@@ -349,9 +349,10 @@ __device__ __forceinline__ ChunkSplit split_of(const ChunkArgs& a, const ChunkIt
 }
 
 // The items [x, y) of `pair`, written to the workspace's item array (by both of its CTAs, the same
-// values).  `writer`: also write the header and the split row tiles.  Called by the whole block.
-template <int MODE>
-__device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool writer, PlanScratch& sh) {
+// values).  `writer`: also write the header and the split row tiles.  Called by the whole block, whose last warp does
+// `meanwhile` while the first one weighs the ways.
+template <int MODE, typename F>
+__device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool writer, PlanScratch& sh, F meanwhile) {
     const int tid = threadIdx.x;
     constexpr int NT = kPlanThreads;
     ChunkItem* items = reinterpret_cast<ChunkItem*>(a.ws + a.items_off);
@@ -385,6 +386,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
         if (lane == 0) sh.totals[warp] = sum;
     }
     __syncthreads();
+    if (warp == NT / 32 - 1) meanwhile();
     if (warp == 0) {
         Totals sum = lane < active ? sh.totals[lane] : Totals{};
         warp_totals<MODE == kChunkGroups>(sum);

@@ -663,6 +663,8 @@ size_t chunk_shape(const splash_attn_desc* desc, const splash_chunk_ext* ext, in
             a->prefix_lens = ext->prefix_lens;
         }
     }
+    a->early = max(1, 2 * a->pairs * kEarlyUnits / max(1, a->mode == kChunkGroups ? a->groups : a->B));
+    a->by_early = fast_div(a->early);
     const size_t bytes = chunk_layout(*a);
     if (a->cap_items >= (int64_t(1) << 31)) return 0;
     return bytes;

@@ -47,7 +47,9 @@ struct ChunkTiling {
     int groups;   // head groups of a token block: 1 or an even number (flat: 1)
     int heads;    // heads of a group (the last may have fewer); flat: all heads
     int tokens;   // tokens of a CTA's block (flat: unused)
-    int per;      // new tokens that a pair's rows span, at most
+    int per;      // new tokens whose rows fill a pair's, if the first one's begin with them
+    int span;     // new tokens that a row tile's rows belong to, at most.  Flat: row tiles begin wherever 128 i falls, so 128 rows
+                  //   of 80 heads are of two tokens or of three
     FastDiv by_heads, by_per;
     __host__ __device__ int pair_groups() const { return groups == 1 ? 1 : groups / 2; }
     __host__ __device__ int pair_tokens() const { return per; }
@@ -66,6 +68,10 @@ inline ChunkTiling chunk_tiling(int H, int Hs) {
     t.heads = (Hs + t.groups - 1) / t.groups;
     t.tokens = t.flat ? 0 : kChunkRows / t.heads;
     t.per = t.flat ? (2 * kChunkRows + t.heads - 1) / t.heads : (t.groups == 1 ? 2 * t.tokens : t.tokens);
+    // (rows 128 i begin at multiples of gcd(heads, 128) within a token: the last of these leaves the fewest rows to the first token)
+    int gcd = 2 * kChunkRows;
+    while (t.heads % gcd != 0) gcd /= 2;
+    t.span = t.flat ? (t.heads - gcd + 2 * kChunkRows - 1) / t.heads + 1 : t.per;
     t.by_heads = fast_div(t.heads);
     t.by_per = fast_div(t.per);
     return t;
@@ -164,6 +170,29 @@ struct ChunkArgs {
     int out_f32;
     float scale;
 };
+
+// Key tiles of a row tile whose tokens see the keys from `lo` on before `first` .. `last` (positions + 1).  Windowed: the
+// blocks of the first tokens, then those from the first token's window on; *base is the item's.
+template <int MODE>
+__host__ __device__ inline int key_tiles(const ChunkArgs& a, int lo, int first, int last, int* base = nullptr) {
+    const int e = min(last, a.tok_hi);
+    if (MODE == kChunkGroups && base) *base = lo;
+    if (e <= lo) return 0;
+    if constexpr (MODE == kChunkWindow) {
+        const int b0 = lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
+        const int w = max(b0 + a.sink_blocks, max(max(first, 1) - a.window, 0) / kChunkRows);
+        if (base) *base = w - a.sink_blocks;
+        return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
+    }
+    // (grouped: from the block in which the prefix ends, not from the tile)
+    if constexpr (MODE == kChunkGroups) return (e - lo / kChunkRows * kChunkRows + kChunkKeys - 1) / kChunkKeys;
+    return (e + kChunkKeys - 1) / kChunkKeys - lo / kChunkKeys;
+}
+
+// Windowed: the key tiles of any row tile, at most.  Its tokens' windows span window + tokens - 1 keys, wherever those begin.
+__host__ __device__ inline int most_window_tiles(const ChunkArgs& a) {
+    return (a.sink_blocks + (a.window + a.tile.span - 1 + 2 * (kChunkRows - 1)) / kChunkRows + 1) / 2;
+}
 
 struct ChunkMaps {
     CUtensorMap q;        // [9][total_q][H][64] box {64, heads, tokens, 1}; flat: [9][1][total_q * H][64] box {64, 64, 1, 1}

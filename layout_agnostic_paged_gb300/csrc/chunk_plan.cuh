@@ -75,24 +75,6 @@ __device__ __forceinline__ int last_at_most(const int* from, int n, int x) {
     return lo;
 }
 
-// Key tiles of a row tile whose tokens see the keys from `lo` on before `first` .. `last` (positions + 1).  Windowed: the
-// blocks of the first tokens, then those from the first token's window on; *base is the item's.
-template <int MODE>
-__device__ __forceinline__ int key_tiles(const ChunkArgs& a, int lo, int first, int last, int* base = nullptr) {
-    const int e = min(last, a.tok_hi);
-    if (MODE == kChunkGroups && base) *base = lo;
-    if (e <= lo) return 0;
-    if constexpr (MODE == kChunkWindow) {
-        const int b0 = lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
-        const int w = max(b0 + a.sink_blocks, max(max(first, 1) - a.window, 0) / kChunkRows);
-        if (base) *base = w - a.sink_blocks;
-        return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
-    }
-    // (grouped: from the block in which the prefix ends, not from the tile)
-    if constexpr (MODE == kChunkGroups) return (e - lo / kChunkRows * kChunkRows + kChunkKeys - 1) / kChunkKeys;
-    return (e + kChunkKeys - 1) / kChunkKeys - lo / kChunkKeys;
-}
-
 // The rows of request r.
 template <int MODE>
 __device__ __forceinline__ Span request_span(const ChunkArgs& a, int r) {
@@ -108,9 +90,7 @@ __device__ __forceinline__ Span request_span(const ChunkArgs& a, int r) {
     s.lo = a.tok_lo;
     s.group = kOwn;
     s.m = key_tiles<kChunkPlain>(a, s.lo, s.ctx, s.ctx);
-    // windowed: a row tile's windows span window + tokens - 1 keys, wherever they begin
-    if constexpr (MODE == kChunkWindow)
-        s.m = min(s.m, (a.sink_blocks + (a.window + a.tile.pair_tokens() - 1 + 126) / kChunkRows + 1) / 2);
+    if constexpr (MODE == kChunkWindow) s.m = min(s.m, most_window_tiles(a));
     return s;
 }
 
@@ -656,7 +636,7 @@ __device__ __forceinline__ int2 plan_items(const ChunkArgs& a, int pair, bool wr
                 int tiles;
                 ChunkItem it = row_tile<MODE>(a, sh.spans[q], tile, &tiles);
                 it.t_lo = t0 + min(tiles, piece * sh.piece_tiles[q]);
-                it.t_hi = t0 + min(tiles, (piece + 1) * sh.piece_tiles[q]);
+                it.t_hi = t0 + (piece + 1 == pc ? tiles : min(tiles, (piece + 1) * sh.piece_tiles[q]));
                 if (pc > 1 || (MODE == kChunkGroups && sh.spans[q].group != kOwn)) it.slot = sh.slot0[q] + local;
                 items[x0 + k] = it;
             }

@@ -171,18 +171,22 @@ struct ChunkArgs {
     float scale;
 };
 
+// (for host programs too, which have no min and max without a namespace)
+__host__ __device__ inline int lesser(int x, int y) { return x < y ? x : y; }
+__host__ __device__ inline int greater(int x, int y) { return x < y ? y : x; }
+
 // Key tiles of a row tile whose tokens see the keys from `lo` on before `first` .. `last` (positions + 1).  Windowed: the
 // blocks of the first tokens, then those from the first token's window on; *base is the item's.
 template <int MODE>
 __host__ __device__ inline int key_tiles(const ChunkArgs& a, int lo, int first, int last, int* base = nullptr) {
-    const int e = min(last, a.tok_hi);
+    const int e = lesser(last, a.tok_hi);
     if (MODE == kChunkGroups && base) *base = lo;
     if (e <= lo) return 0;
     if constexpr (MODE == kChunkWindow) {
         const int b0 = lo / kChunkRows, end = (e + kChunkRows - 1) / kChunkRows;
-        const int w = max(b0 + a.sink_blocks, max(max(first, 1) - a.window, 0) / kChunkRows);
+        const int w = greater(b0 + a.sink_blocks, greater(greater(first, 1) - a.window, 0) / kChunkRows);
         if (base) *base = w - a.sink_blocks;
-        return (min(end - b0, a.sink_blocks) + max(end - w, 0) + 1) / 2;
+        return (lesser(end - b0, a.sink_blocks) + greater(end - w, 0) + 1) / 2;
     }
     // (grouped: from the block in which the prefix ends, not from the tile)
     if constexpr (MODE == kChunkGroups) return (e - lo / kChunkRows * kChunkRows + kChunkKeys - 1) / kChunkKeys;

@@ -379,6 +379,22 @@ def _shape_desc(B: int, H: int, P: int, num_pages: int, max_pages: int, scale: f
     return SplashAttnDesc(B, H, 576, 512, P, num_pages, max_pages, scale)
 
 
+def _int32(where: str, name: str, v) -> int:
+    """v as an int32 argument of the library (ctypes would take its low 32 bits)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{where}: {name} must fit 32 bits")
+    return v
+
+
+def _packed(where: str, fmt: struct.Struct, *values) -> bytes:
+    """The packed struct of a call."""
+    try:
+        return fmt.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"{where}: sizes must be whole numbers of 32 bits ({e})") from None
+
+
 def _int32_arrays(where: str, dev: int, arrays) -> None:
     """Each (name, tensor, entries): contiguous int32 of so many entries on device `dev`."""
     i32 = torch.int32
@@ -408,8 +424,8 @@ def splash_batch_tables(past_lens: torch.Tensor, new_lens: torch.Tensor, block_t
         ("past_lens", past_lens, B), ("new_lens", new_lens, B), ("block_table", block_table, B * pages),
         ("free_pages", free_pages, F), ("free_count", free_count, count), ("cu_q", cu_q, B + 1), ("ctx_lens", ctx_lens, B),
         ("positions", positions, N), ("slots", slots, N), ("left", left, 2)))
-    _call(dev, stream, where, (_lib or load_library()).splash_batch_tables, _BATCH.pack(
-        B, page_size, F, pages, N, 0, past_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_tables, _packed(
+        where, _BATCH, B, page_size, F, pages, N, 0, past_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
         free_count.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), ctx_lens.data_ptr(), positions.data_ptr(),
         slots.data_ptr(), left.data_ptr()))
 
@@ -431,8 +447,8 @@ def splash_batch_release(ctx_lens: torch.Tensor, keep_lens: torch.Tensor | None,
     _int32_arrays(where, dev, (
         ("ctx_lens", ctx_lens, B), ("keep_lens", ctx_lens if keep_lens is None else keep_lens, B),
         ("block_table", block_table, B * pages), ("free_pages", free_pages, F), ("free_count", free_count, count)))
-    _call(dev, stream, where, (_lib or load_library()).splash_batch_release, _BATCH_DROP.pack(
-        B, page_size, F, pages, window, sinks, ctx_lens.data_ptr(), 0 if keep_lens is None else keep_lens.data_ptr(),
+    _call(dev, stream, where, (_lib or load_library()).splash_batch_release, _packed(
+        where, _BATCH_DROP, B, page_size, F, pages, window, sinks, ctx_lens.data_ptr(), 0 if keep_lens is None else keep_lens.data_ptr(),
         block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr()))
 
 
@@ -470,7 +486,8 @@ def splash_rope(x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor, rop
 @functools.lru_cache(maxsize=1024)
 def _norm_desc(width: int, norm_dims: int, rope_lo: int, weight_dtype: int, eps: float, offset: float) -> SplashNormDesc:
     """The description of a norm (read-only; the library reads it during the call)."""
-    return SplashNormDesc(width, norm_dims, rope_lo, weight_dtype, eps, offset)
+    where = "splash_norm_rope"
+    return SplashNormDesc(width, _int32(where, "norm_dims", norm_dims), _int32(where, "rope_lo", rope_lo), weight_dtype, eps, offset)
 
 
 def _norm_rows(where: str, dev: int, x, weight, out, T: int, D: int, n: int, dtype, weight_dtype) -> bytes:
@@ -600,8 +617,8 @@ def chunk_workspace(q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.T
     desc = _chunk_desc(where, q, kv_pool, *block_table.shape, scale)
     head_hi = q.shape[1] if head_hi is None else head_hi
     with torch.cuda.device(dev):
-        n = int(load_library().splash_chunk_workspace_size_ex(desc, SplashChunkExt(num_groups=int(num_groups)), q.shape[0],
-                                                              int(head_lo), int(head_hi)))
+        n = int(load_library().splash_chunk_workspace_size_ex(
+            desc, SplashChunkExt(num_groups=_int32(where, "num_groups", num_groups)), q.shape[0], int(head_lo), int(head_hi)))
     if n == 0:
         raise SplashError(SPLASH_ERR_UNSUPPORTED, where)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -621,7 +638,8 @@ def splash_chunk_attn(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor
 @functools.lru_cache(maxsize=256)
 def _window_ext(window: int, sinks: int) -> SplashChunkExt:
     """A window without groups (read-only; the library reads it during the call)."""
-    return SplashChunkExt(window, sinks)
+    where = "splash_chunk_attn_ex"
+    return SplashChunkExt(_int32(where, "window", window), _int32(where, "sinks", sinks))
 
 
 def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Tensor, block_table: torch.Tensor,
@@ -642,7 +660,8 @@ def splash_chunk_attn_ex(q: torch.Tensor, kv_pool: torch.Tensor, cu_q: torch.Ten
     else:
         G = prefix_lens.numel()
         _int32_arrays(where, dev, (("cu_groups", cu_groups, G + 1), ("prefix_lens", prefix_lens, G)))
-        ext = SplashChunkExt(int(window), int(sinks), cu_groups.data_ptr(), prefix_lens.data_ptr(), G)
+        ext = SplashChunkExt(_int32(where, "window", window), _int32(where, "sinks", sinks), cu_groups.data_ptr(),
+                             prefix_lens.data_ptr(), G)
     _call(dev, stream, where, (_lib or load_library()).splash_chunk_attn_ex, args[0], ext, *args[1:])
 
 

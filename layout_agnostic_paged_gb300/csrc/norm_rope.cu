@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<K>) norm_rope_kernel
                     const float* from = wts + e0 / VE * kWRun;
 #pragma unroll
                     for (int e = 0; e < VE; ++e) w[e] = from[e];
-                    if constexpr (VE == 1) x[k][s][0] *= r * w[0];
+                    // (the root first: x r is of size one, where r w may leave fp32's range for a weight that y has room for)
+                    if constexpr (VE == 1) x[k][s][0] = x[k][s][0] * r * w[0];
                     else {
 #pragma unroll
                         for (int e = 0; e < VE; e += 2) {
-                            mul2(w + e, w + e, r, r);
+                            mul2(&x[k][s][e], &x[k][s][e], r, r);
                             mul2(&x[k][s][e], &x[k][s][e], w[e], w[e + 1]);
                         }
                     }

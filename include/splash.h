@@ -569,8 +569,9 @@ typedef struct {
  * such pages back).
  * Groups:  the results are those of splash_chunk_attn; where it pays, the rows of a group's requests are worked on
  * together over the prefix, whose keys are then read and multiplied once for up to 128 of them (16 heads of 8
- * single tokens, for instance) instead of once a request.  With 128 heads and more a token's own rows are that many,
- * and there is nothing to gain.  Whether it pays goes by the numbers of rows and keys, so equal calls give equal bits.
+ * single tokens, for instance) instead of once a request.  Where a token's own rows fill that many (a call of all heads with 128
+ * of them or more, a slice of more than 64) there is nothing to gain: such calls are worked on as by splash_chunk_attn and read
+ * neither array, so what follows on their values holds for the other calls.  Whether it pays goes by the numbers of rows and keys, so equal calls give equal bits.
  * The prefix's entries in the tables of the group's other requests may or may not be read.  A prefix that is negative or longer than
  * max_pages_per_req * P (clamped), or longer than the tokens that one of its requests has before its new ones (whose rows
  * may then see all of it), and cu_groups that descend or leave [0, B] (no row is written then) set SPLASH_DEVICE_BAD_INPUT.

@@ -348,7 +348,8 @@ typedef struct {
  * outside [0, num_pages) has no page: it is passed over.  The pages go on so that the first request's first one lies
  * on top: after splash_batch_tables, dropping the same new tokens puts the stack back as it was.
  * A page that several requests share must be kept by all of them but one, or it is on the list more than
- * once.  Pages that do not fit on the stack are lost.  num_reqs * max_pages_per_req is below 2^31.  No two arrays may
+ * once.  Pages that do not fit on the stack are lost.  With a window, tokens are dropped in the same call or before it: what the
+ * window has left behind k tokens does not come back when a later call keeps fewer.  num_reqs * max_pages_per_req is below 2^31.  No two arrays may
  * overlap (keep_lens may be ctx_lens).
  */
 SPLASH_API int splash_batch_release(const splash_batch_drop* drop, splash_stream_t stream);
@@ -576,7 +577,8 @@ typedef struct {
  * max_pages_per_req * P (clamped), or longer than the tokens that one of its requests has before its new ones (whose rows
  * may then see all of it), and cu_groups that descend or leave [0, B] (no row is written then) set SPLASH_DEVICE_BAD_INPUT.
  * The workspace is that of splash_chunk_workspace_size_ex, which takes num_groups from ext and reads neither of its
- * arrays; a partial result of every 128 rows (262 KB) is kept for each request and group.
+ * arrays.  So it has room for a partial result (262 KB) of every 128 rows of the requests and of as many of the groups, 4 KB a
+ * row, whether a group holds them or not: prompts of many tokens are better in a call of their own.
  * Otherwise the same arguments, results and errors as splash_chunk_attn, and without groups the same workspace.
  */
 SPLASH_API size_t splash_chunk_workspace_size_ex(const splash_attn_desc* desc, const splash_chunk_ext* ext, int total_q,

@@ -145,7 +145,9 @@ size_t chunk_layout(ChunkArgs& a) {
     const int64_t u = a.tile.row_tiles(a.total_q) + int64_t(a.B) * a.tile.pair_groups();   // each request rounds up
     const int64_t most = int64_t(kChunkSlotsPerPair) * a.pairs;
     int64_t slots = tiles <= 1 ? 0 : (tiles >= most || u * tiles > most ? most : u * tiles), more = 0;
-    if (a.mode == kChunkGroups) {        // the groups' row tiles, and a partial of every row tile
+    // Grouped: the groups' row tiles, and a partial result of every row tile, two of 262 KB for 128 rows.  Only the row tiles of
+    // groups that are worth it use theirs, but which those are is in arrays on the device, and the size may not wait for it.
+    if (a.mode == kChunkGroups) {
         more = a.tile.row_tiles(a.total_q) + a.groups;
         slots += u + more;
     }

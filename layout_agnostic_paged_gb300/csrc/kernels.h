@@ -107,8 +107,9 @@ struct BatchReleaseArgs {
     int window, sinks;            // window 0: none
 };
 constexpr int kReleaseCtas = 8;
-// Up to so many rows one CTA writes them all, and no cluster has to meet: 256 rows take 3.5 us (eight CTAs: 4.0), 4,096 rows
-// 3.8 (4.3), 8,192 rows 5.7 (4.5), 30,500 rows 14 (4.5).
+// Up to so many rows one CTA writes them all, and no cluster has to meet.  Per call in replays of a graph, with 256 requests of
+// one row and 61 to 64 of more: 256 rows take 4.1 us (eight CTAs: 4.5), 4,096 rows 4.0 (4.4), 8,192 rows 5.5 (4.4),
+// 30,500 rows 13.2 (4.2).
 constexpr int kSmallBatchRows = 4096;
 cudaError_t launch_batch_tables(const BatchTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_batch_release(const BatchReleaseArgs& a, cudaStream_t stream);

@@ -14,7 +14,7 @@
 // token it took 25 instructions an element; now 18, the products and sums two to an instruction.  8,191 tokens x 72
 // heads x 128 dims in bf16, half of them rotated (302 MB): 50.2 us, 6.0 TB/s, 90% of the copy bandwidth (47.3 us in fp32 with half
 // the tokens); 1,024 tokens x 129 latent heads x 576 dims 54.6 us (82%); 32,768 latent rows of 576 dims, whose 32 angles
-// serve one row each: 19.1 us (58%); 256 tokens x 18 heads: 3.2 us.
+// serve one row each: 19.0 us (60%: a block works out the angles of all its rows before it starts on the first); 256 tokens x 18 heads: 3.2 us.
 #include <limits.h>
 
 #include <algorithm>
